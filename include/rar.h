@@ -386,6 +386,129 @@ rar_result_t rar_oneshot_allreduce_premul(const void* const* sendbufs, void* con
                                           const void* scalars, const rar_oneshot_tuning_t* tuning,
                                           void* stream);
 
+/* ---- operators around an AllReduce ------------------------------------------
+ *
+ * A model split over N virtual ranks reduces over them in three places: after
+ * a row-parallel projection, in the residual stream that follows it, and in
+ * the loss over a vocabulary split between the ranks.  The entry points below
+ * compute those reductions together with what surrounds them.  None needs a
+ * communicator or allocates anything; each is stream ordered, can be captured
+ * into a HIP graph, checks its arguments on the host before anything is
+ * launched, and gives the same bits for the same inputs.  Types: RAR_FLOAT32
+ * and RAR_BFLOAT16 (others: RAR_INVALID_ARGUMENT); sums and softmax statistics
+ * are kept in fp32 and each result is rounded to its type once.  Outputs must
+ * not overlap each other, nor inputs except where "in place" is said.  Strides
+ * count elements between rows; a NULL stride array means rows that follow
+ * each other.
+ */
+
+/* The one-shot AllReduce with dropout and a residual:
+ *   recvbufs[k][i] = residual[i] + drop(sum over r of sendbufs[r][i])
+ * folded in rank order.  drop keeps element i, multiplied by
+ * 65536 / (65536 - cut) with cut = p * 65536 rounded to nearest, where 16
+ * random bits of the element are at least cut, and makes it 0 (whatever it
+ * was) otherwise; p = 1 drops everything.  The bits come from Philox4x32 with
+ * 7 rounds (key = seed; counter = element index / 8 and the 64-bit offset;
+ * element i takes bits 16 * (i mod 8) of the 128), so the mask is not stored:
+ * the gradient draws it again.  It does not depend on the type, the number of
+ * ranks or the launch.
+ *   nsend, nrecv  1..64 inputs and copies of the output; each buffer is
+ *                 aligned to its element size.  An output may be exactly one
+ *                 of the inputs or the residual (in place).
+ *   residual      NULL for none.
+ *   count         elements; 0 launches nothing and looks at no pointer.
+ *   p             0 <= p <= 1.
+ *   rng           two uint64 in device memory, {seed, offset}, read by the
+ *                 kernel (so a replayed graph draws what they then hold).
+ *   call          added to the offset: one value for each use of dropout
+ *                 that shares the state. */
+rar_result_t rar_dropout_allreduce(const void* const* sendbufs, int nsend, void* const* recvbufs,
+                                   int nrecv, const void* residual, size_t count,
+                                   rar_dtype_t dtype, double p, const void* rng, uint64_t call,
+                                   void* stream);
+
+/* Its gradient, for the same p, rng contents and call:
+ *   dresidual[i] = sum over k of grads[k][i]        (NULL: not wanted)
+ *   dsends[r][i] = drop(that sum), the same for every r
+ * ngrads, ndsends 1..64.  An output may be exactly one of the inputs. */
+rar_result_t rar_dropout_allreduce_backward(const void* const* grads, int ngrads,
+                                            void* const* dsends, int ndsends, void* dresidual,
+                                            size_t count, rar_dtype_t dtype, double p,
+                                            const void* rng, uint64_t call, void* stream);
+
+/* Log probabilities over a vocabulary split between the ranks: rank r holds
+ * the logits of widths[r] tokens (0 allowed), which follow rank r-1's in the
+ * vocabulary (1 to 2^30 tokens in all).  With z = scale * logit, for each row:
+ *   lse = log sum e^z,  logprob = z[id] - lse,  entropy = -sum p log p,
+ * and the ntop largest logits in descending order (equal ones by the lower
+ * id) as vocabulary ids and log probabilities.  One pass over the logits; a
+ * row is split over workgroups where there are few, and a second launch joins
+ * the parts.
+ *   logits     nranks (1..64) device pointers, [rows] of widths[r] elements.
+ *   rows       0..2^23; 0 launches nothing.
+ *   scale      positive and finite: the inverse temperature.
+ *   ids        [rows] int64 in device memory; one outside the vocabulary
+ *              (such as -1) marks a row without a token: logprob 0.
+ *   ntop       0..32; top_ids and top_logprobs are [rows][ntop].
+ *   logprob, entropy, lse   [rows]; NULL for those not wanted (ids may be
+ *              NULL without logprob).
+ *   workspace  16-byte aligned device memory of the size that
+ *              rar_logprobs_workspace gives (0: NULL allowed); its contents
+ *              do not matter before or after the call.
+ * Masked tokens are -inf: they have probability 0 and are not alternatives
+ * (places left over hold id -1 and -inf).  A row masked entirely gives lse
+ * and logprob -inf, entropy 0.  A NaN or +inf gives NaN in its row's logprob
+ * and entropy; NaN is no alternative. */
+rar_result_t rar_logprobs(const void* const* logits, const int64_t* widths,
+                          const int64_t* strides, int nranks, int64_t rows, rar_dtype_t dtype,
+                          float scale, const int64_t* ids, int ntop, float* logprob,
+                          float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                          void* workspace, size_t workspace_bytes, void* stream);
+rar_result_t rar_logprobs_workspace(const int64_t* widths, int nranks, int64_t rows,
+                                    rar_dtype_t dtype, int ntop, size_t* bytes);
+
+/* The gradient of logprob, entropy and lse with respect to every logit:
+ *   grad[j] = scale * (g [j == id] + p_j (l - g - h (log p_j + entropy)))
+ * with g, h, l the incoming gradients (fp32 [rows], each NULL for zero, not
+ * all three) and lse, entropy as rar_logprobs gave them (entropy may be NULL
+ * without grad_entropy).  g counts as 0 in rows without a token; rows masked
+ * entirely get 0.  grads[r] is like logits[r] and may be exactly it (in
+ * place); grad_strides as strides. */
+rar_result_t rar_logprobs_backward(const void* const* logits, const int64_t* widths,
+                                   const int64_t* strides, int nranks, int64_t rows,
+                                   rar_dtype_t dtype, float scale, const int64_t* ids,
+                                   const float* lse, const float* entropy,
+                                   const float* grad_logprob, const float* grad_entropy,
+                                   const float* grad_lse, void* const* grads,
+                                   const int64_t* grad_strides, void* stream);
+
+/* The AllReduce of a row-parallel projection with low-rank adapters of many
+ * requests beside it.  Rank r holds widths[r] columns x_r of the input (0
+ * allowed), the partial product P_r of the shared projection and its columns
+ * A_{a,r} of every adapter's first matrix; the second matrix B_a is whole:
+ *   recvbufs[k][t] = sum_r P_r[t] + scales[a] * B_a (sum_r A_{a,r} x_r[t]),
+ * a = ids[t], for every copy k; the partials are folded in rank order.  The
+ * tokens may have their adapters in any order; it is fastest where a
+ * request's tokens stand together.  A token's id outside [0, adapters) means
+ * no adapter.  An adapter's weights are read for its own tokens only.
+ *   xs         [tokens] of widths[r] elements      partials, recvbufs [tokens]
+ *   downs      [adapters][rank][widths[r]]         of outer elements
+ *   up         [adapters][outer][rank]
+ *   ids        [tokens] int64    scales  [adapters] fp32, NULL for 1
+ *   tokens 0..2^24 (0 launches nothing), outer, adapters 1..2^24, rank 1..128,
+ *   nranks, nrecv 1..64.  An output may be exactly one of the partials.
+ *   workspace  16-byte aligned device memory, rar_adapter_workspace bytes. */
+rar_result_t rar_adapter_allreduce(const void* const* xs, const int64_t* widths,
+                                   const int64_t* x_strides, const void* const* partials,
+                                   const int64_t* partial_strides, int nranks,
+                                   void* const* recvbufs, const int64_t* recv_strides, int nrecv,
+                                   int64_t tokens, int64_t outer, rar_dtype_t dtype,
+                                   const void* const* downs, const void* up, int64_t adapters,
+                                   int rank, const int64_t* ids, const float* scales,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+rar_result_t rar_adapter_workspace(const int64_t* widths, int nranks, int64_t tokens,
+                                   rar_dtype_t dtype, int rank, size_t* bytes);
+
 /* Watchdog status: RAR_ABORTED if a launch on this communicator timed out in
  * a wait, else RAR_SUCCESS.  Does not synchronize; reflects launches the
  * device has finished. */

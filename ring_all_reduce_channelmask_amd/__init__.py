@@ -15,8 +15,11 @@ import ctypes
 
 from . import _lib
 from ._lib import RarError  # noqa: F401
+from .model_ops import (LogProbs, adapter_allreduce, dropout_allreduce,  # noqa: F401
+                        dropout_allreduce_backward, logprobs, logprobs_backward)
 
-__all__ = ["Comm", "ring_allreduce", "ring_allreduce_noalloc", "oneshot_allreduce", "ring_info", "graph_text", "plan_pieces", "RarError"]
+__all__ = ["Comm", "ring_allreduce", "ring_allreduce_noalloc", "oneshot_allreduce", "ring_info", "graph_text", "plan_pieces", "RarError",
+           "dropout_allreduce", "dropout_allreduce_backward", "logprobs", "logprobs_backward", "LogProbs", "adapter_allreduce"]
 
 
 def _dtype_name(t):

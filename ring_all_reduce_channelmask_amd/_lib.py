@@ -58,6 +58,7 @@ _lib = None
 _c = ctypes
 _vpp = _c.POINTER(_c.c_void_p)
 _ip = _c.POINTER(_c.c_int)
+_lp = _c.POINTER(_c.c_int64)
 SIGNATURES = [
     ("rar_comm_create", _c.c_int, [_c.POINTER(_c.c_void_p), _c.c_int, _ip, _c.c_uint64, _c.c_int,
                                    _c.c_size_t, _c.c_int, _c.POINTER(Tuning)]),
@@ -83,6 +84,26 @@ SIGNATURES = [
     ("rar_oneshot_allreduce_premul", _c.c_int, [_vpp, _vpp, _c.c_int, _c.c_size_t, _c.c_int,
                                                 _c.c_void_p, _c.POINTER(OneshotTuning),
                                                 _c.c_void_p]),
+    ("rar_dropout_allreduce", _c.c_int, [_vpp, _c.c_int, _vpp, _c.c_int, _c.c_void_p, _c.c_size_t,
+                                         _c.c_int, _c.c_double, _c.c_void_p, _c.c_uint64,
+                                         _c.c_void_p]),
+    ("rar_dropout_allreduce_backward", _c.c_int, [_vpp, _c.c_int, _vpp, _c.c_int, _c.c_void_p,
+                                                  _c.c_size_t, _c.c_int, _c.c_double, _c.c_void_p,
+                                                  _c.c_uint64, _c.c_void_p]),
+    ("rar_logprobs", _c.c_int, [_vpp, _lp, _lp, _c.c_int, _c.c_int64, _c.c_int, _c.c_float,
+                                _c.c_void_p, _c.c_int] + [_c.c_void_p] * 6 +
+     [_c.c_size_t, _c.c_void_p]),
+    ("rar_logprobs_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
+                                          _c.POINTER(_c.c_size_t)]),
+    ("rar_logprobs_backward", _c.c_int, [_vpp, _lp, _lp, _c.c_int, _c.c_int64, _c.c_int,
+                                         _c.c_float] + [_c.c_void_p] * 6 + [_vpp, _lp,
+                                                                            _c.c_void_p]),
+    ("rar_adapter_allreduce", _c.c_int, [_vpp, _lp, _lp, _vpp, _lp, _c.c_int, _vpp, _lp, _c.c_int,
+                                         _c.c_int64, _c.c_int64, _c.c_int, _vpp, _c.c_void_p,
+                                         _c.c_int64, _c.c_int] + [_c.c_void_p] * 3 +
+     [_c.c_size_t, _c.c_void_p]),
+    ("rar_adapter_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
+                                         _c.POINTER(_c.c_size_t)]),
     ("rar_comm_get_async_error", _c.c_int, [_c.c_void_p]),
     ("rar_comm_query_state", _c.c_int, [_c.c_void_p, _c.POINTER(_c.c_int64), _c.c_size_t,
                                         _c.POINTER(_c.c_size_t)]),

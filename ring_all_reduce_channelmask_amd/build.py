@@ -2,7 +2,8 @@
 
 The library holds the ring AllReduce kernel (one translation unit per payload
 type, each instantiating every protocol and reduction operator), the one-shot
-kernel, the host planner and the C ABI declared in ``include/rar.h``.  The
+kernel, the operators around an AllReduce (dropout, log probabilities,
+adapters), the host planner and the C ABI declared in ``include/rar.h``.  The
 sources compile to objects in parallel and are linked once.  Always compiles
 (the caller decides when).
 """
@@ -15,7 +16,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "librar.so")
 SOURCES = ["csrc/ring_kernel_i32.hip", "csrc/ring_kernel_f32.hip", "csrc/ring_kernel_bf16.hip",
-           "csrc/oneshot_kernel.hip", "csrc/plan.cpp", "csrc/capi.cpp", "csrc/noalloc.hip"]
+           "csrc/oneshot_kernel.hip", "csrc/plan.cpp", "csrc/capi.cpp", "csrc/noalloc.hip",
+           "csrc/dropout.hip", "csrc/logprobs.hip", "csrc/adapters.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

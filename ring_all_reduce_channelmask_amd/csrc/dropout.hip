@@ -1,0 +1,204 @@
+// dropout.hip -- the one-shot AllReduce with dropout and a residual in its
+// epilogue, and its gradient; the dropout mask is never stored.
+//
+//   forward   y_k[i] = residual[i] + drop(sum_r x_r[i])        k = every copy
+//   gradient  dresidual[i] = sum_k dy_k[i],  dx_r[i] = drop(dresidual[i])
+//   drop(v) at i = v * 65536 / (65536 - cut) if field(i) >= cut, else 0
+//
+// field(i) is 16 of the 128 bits that Philox4x32 with 7 rounds (Salmon,
+// Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011:
+// the fewest rounds that pass its statistical tests) gives for the key
+// `seed` and the counter (i / 8, offset): one evaluation serves 8 elements,
+// and the gradient evaluates it again instead of reading a mask.  Sums are
+// fp32 in rank order and everything is rounded to the payload type once.
+//
+// Bound by memory: (inputs + residual + outputs) * count elements move once.
+#include "op_common.h"
+
+#include <cmath>
+
+namespace rar {
+namespace {
+
+struct DropoutArgs {
+  const void* src[kMaxRanks];
+  void* dst[kMaxRanks];
+  const void* residual;  // forward: added after the dropout, or NULL
+  void* dresidual;       // gradient: the undropped sum, or NULL
+  const uint64_t* rng;   // {seed, offset} in device memory
+  uint64_t call;         // added to the offset
+  int64_t count;
+  int32_t nsrc, ndst;
+  uint32_t cut;          // of 65536: a field below it drops the element
+  float factor;          // 65536 / (65536 - cut)
+};
+
+// The 8 fields of elements 8n .. 8n+7, two to a word, the lower element in
+// the lower half.
+__device__ __forceinline__ v4u philox7(uint64_t n, uint64_t seed, uint64_t offset) {
+  uint32_t a = (uint32_t)n, b = (uint32_t)(n >> 32), c = (uint32_t)offset, d = (uint32_t)(offset >> 32);
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int round = 0; round < 7; ++round) {
+    const uint64_t u = (uint64_t)a * 0xD2511F53u, v = (uint64_t)c * 0xCD9E8D57u;
+    a = (uint32_t)(v >> 32) ^ b ^ k0;
+    b = (uint32_t)v;
+    c = (uint32_t)(u >> 32) ^ d ^ k1;
+    d = (uint32_t)u;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return v4u{a, b, c, d};
+}
+
+// One thread takes the 8 elements of one generator call: one 16-byte vector
+// of bf16, two of fp32.  Up to 4 inputs' loads are issued together.
+template <class T, int kVecs>
+struct Group {
+  v4u v[kVecs];
+};
+template <class T, int kVecs>
+__device__ __forceinline__ Group<T, kVecs> load_group(const void* base, int64_t e, int n) {
+  Group<T, kVecs> g;
+  const typename T::bits* p = static_cast<const typename T::bits*>(base) + e;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) g.v[j] = load_part<T>(p + j * T::kVec, n - j * T::kVec, 0);
+  return g;
+}
+template <class T, int kVecs>
+__device__ __forceinline__ void store_group(void* base, int64_t e, int n, const float* f) {
+  typename T::bits* p = static_cast<typename T::bits*>(base) + e;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) store_part<T>(p + j * T::kVec, n - j * T::kVec, T::round(f + j * T::kVec));
+}
+
+template <class T, bool kBackward>
+__global__ void __launch_bounds__(256) dropout_kernel(DropoutArgs) {
+  const DropoutArgs& args = kernel_args<DropoutArgs>();
+  constexpr int kVecs = 8 / T::kVec, kBatch = 4;
+  const uint64_t seed = args.rng[0], offset = args.rng[1] + args.call;
+  const int64_t groups = (args.count + 7) / 8;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < groups; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t e = i * 8;
+    const int n = args.count - e < 8 ? (int)(args.count - e) : 8;
+    float sum[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int r0 = 0; r0 < args.nsrc; r0 += kBatch) {
+      Group<T, kVecs> x[kBatch];
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r)
+        if (r0 + r < args.nsrc) x[r] = load_group<T, kVecs>(args.src[r0 + r], e, n);
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r) {
+        if (r0 + r < args.nsrc) {
+          float f[8];
+#pragma unroll
+          for (int j = 0; j < kVecs; ++j) T::widen(x[r].v[j], f + j * T::kVec);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] = r0 + r == 0 ? f[j] : sum[j] + f[j];
+        }
+      }
+    }
+    const v4u fields = philox7((uint64_t)i, seed, offset);
+    float out[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t field = j & 1 ? fields[j / 2] >> 16 : fields[j / 2] & 0xFFFFu;
+      out[j] = field >= args.cut ? sum[j] * args.factor : 0.0f;
+    }
+    if (kBackward) {
+      if (args.dresidual) store_group<T, kVecs>(args.dresidual, e, n, sum);
+    } else if (args.residual) {
+      const Group<T, kVecs> res = load_group<T, kVecs>(args.residual, e, n);
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) T::widen(res.v[j], f + j * T::kVec);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] += f[j];
+    }
+    for (int k = 0; k < args.ndst; ++k) store_group<T, kVecs>(args.dst[k], e, n, out);
+  }
+}
+
+const void* get_dropout_kernel(int dtype, bool backward) {
+  if (dtype == kFloat32)
+    return backward ? reinterpret_cast<const void*>(&dropout_kernel<F32, true>)
+                    : reinterpret_cast<const void*>(&dropout_kernel<F32, false>);
+  return backward ? reinterpret_cast<const void*>(&dropout_kernel<BF16, true>)
+                  : reinterpret_cast<const void*>(&dropout_kernel<BF16, false>);
+}
+
+rar_result_t dropout_call(const void* const* src, int nsrc, void* const* dst, int ndst, const void* residual,
+                          void* dresidual, size_t count, int dtype, double p, const void* rng, uint64_t call,
+                          void* stream, bool backward) {
+  if (nsrc < 1 || nsrc > kMaxRanks || ndst < 1 || ndst > kMaxRanks)
+    return set_error(RAR_INVALID_ARGUMENT, "the numbers of inputs and outputs must be in [1, 64]");
+  if (rar_result_t r = check_float_dtype(dtype)) return r;
+  if (!(p >= 0.0 && p <= 1.0)) return set_error(RAR_INVALID_ARGUMENT, "p must be in [0, 1]");
+  if (count == 0) return RAR_SUCCESS;
+  if (count > (size_t(1) << 40)) return set_error(RAR_INVALID_ARGUMENT, "count too large");
+  if (!src || !dst) return set_error(RAR_INVALID_ARGUMENT, "an array of buffers is NULL");
+  const size_t es = (size_t)elem_size(dtype);
+  if (rar_result_t r = check_pointer(rng, 8, "rng")) return r;
+  DropoutArgs a{};
+  const int64_t bytes = (int64_t)(count * es);
+  std::vector<Block> reads, writes;
+  reads.push_back({rng, 1, 16, 16, "rng"});
+  for (int r = 0; r < nsrc; ++r) {
+    if (rar_result_t e = check_pointer(src[r], es, "input " + std::to_string(r))) return e;
+    a.src[r] = src[r];
+    reads.push_back({src[r], 1, bytes, bytes, "an input"});
+  }
+  for (int k = 0; k < ndst; ++k) {
+    if (rar_result_t e = check_pointer(dst[k], es, "output " + std::to_string(k))) return e;
+    a.dst[k] = dst[k];
+    writes.push_back({dst[k], 1, bytes, bytes, "output"});
+  }
+  if (residual) {
+    if (rar_result_t e = check_pointer(residual, es, "residual")) return e;
+    reads.push_back({residual, 1, bytes, bytes, "residual"});
+  }
+  if (dresidual) {
+    if (rar_result_t e = check_pointer(dresidual, es, "dresidual")) return e;
+    writes.push_back({dresidual, 1, bytes, bytes, "dresidual"});
+  }
+  if (rar_result_t r = check_blocks(reads, writes, true)) return r;
+  a.residual = residual;
+  a.dresidual = dresidual;
+  a.rng = static_cast<const uint64_t*>(rng);
+  a.call = call;
+  a.count = (int64_t)count;
+  a.nsrc = nsrc;
+  a.ndst = ndst;
+  a.cut = (uint32_t)std::nearbyint(p * 65536.0);
+  a.factor = a.cut < 65536u ? (float)(65536.0 / (65536.0 - a.cut)) : 0.0f;
+  const int64_t groups = ((int64_t)count + 7) / 8;
+  const int64_t blocks = std::min<int64_t>((groups + 255) / 256, 4096);
+  return launch_kernel(get_dropout_kernel(dtype, backward), dim3((unsigned)blocks), dim3(256), &a, stream);
+}
+
+}  // namespace
+}  // namespace rar
+
+extern "C" {
+
+rar_result_t rar_dropout_allreduce(const void* const* sendbufs, int nsend, void* const* recvbufs, int nrecv,
+                                   const void* residual, size_t count, rar_dtype_t dtype, double p,
+                                   const void* rng, uint64_t call, void* stream) {
+  return rar::guarded([&] {
+    return rar::dropout_call(sendbufs, nsend, recvbufs, nrecv, residual, nullptr, count, dtype, p, rng, call, stream,
+                             false);
+  });
+}
+
+rar_result_t rar_dropout_allreduce_backward(const void* const* grads, int ngrads, void* const* dsends, int ndsends,
+                                            void* dresidual, size_t count, rar_dtype_t dtype, double p,
+                                            const void* rng, uint64_t call, void* stream) {
+  return rar::guarded([&] {
+    return rar::dropout_call(grads, ngrads, dsends, ndsends, nullptr, dresidual, count, dtype, p, rng, call, stream,
+                             true);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,709 @@
+// logprobs.hip -- log probabilities of given tokens over a vocabulary split
+// over N virtual ranks, with the entropy and the most probable tokens, and
+// the gradient of both.
+//
+//   z = scale * x,  lse = log sum_j e^{z_j},  logprob = z_id - lse,
+//   entropy = lse - sum_j p_j z_j,  p_j = e^{z_j - lse}
+//   dx_j = scale * (g [j == id] + p_j (l - g - h (log p_j + entropy)))
+// for the gradients g, h, l of logprob, entropy and lse.
+//
+// Forward: one pass over the logits.  With m a running maximum (in units of
+// log 2: M = m * scale * log2 e) and d_j = x_j * scale * log2 e - M, a thread
+// keeps s = sum 2^{d_j} and u = sum 2^{d_j} d_j, and rescales both by
+// 2^{M - M'} (u also by the shift) when its maximum grows; two such triples
+// join the same way.  Then lse = ln 2 (M + log2 s) and entropy = ln 2
+// (log2 s - u / s).  All of it is fp32.
+//
+// The logits are cut into tiles that do not cross ranks; a workgroup takes a
+// run of consecutive tiles of one row.  Where there are few rows a row is
+// split over several workgroups, which leave (M, s, u) and their best tokens
+// in the workspace for a second kernel to join.
+#include "op_common.h"
+
+#include <cmath>
+
+namespace rar {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / kWaveSize;
+constexpr int kVecsPerTile = 4;  // 16-byte vectors of a tile per thread
+constexpr int kMaxTop = 32;
+constexpr int kCandidates = 1024;  // best-token candidates a workgroup holds
+constexpr int kMaxSplits = 256;
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // 256 threads each: a grid holds less than 2^32
+constexpr int64_t kMaxRows = int64_t(1) << 23;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -3.402823466e+38f;
+
+struct Shards {
+  const void* ptr[kMaxRanks];
+  int64_t stride[kMaxRanks];       // elements between rows
+  int32_t first[kMaxRanks + 1];    // first vocabulary id of each rank; the last entry is the vocabulary
+  int32_t tile0[kMaxRanks + 1];    // first tile of each rank
+  int32_t nranks;
+};
+struct LogprobsArgs {
+  Shards x;
+  int64_t rows;
+  int32_t splits, ntop;
+  float scale, scale2;             // scale, scale * log2 e
+  const int64_t* ids;
+  float *logprob, *entropy, *lse;
+  int32_t* top_ids;
+  float* top_logprobs;
+  v4f* parts;                      // [rows][splits] M, s, u
+  uint64_t* keys;                  // [rows][splits][ntop]
+};
+
+template <class T>
+constexpr int tile_elems() { return kThreads * kVecsPerTile * T::kVec; }
+
+// The rank that holds tile t (or id v, from `first`).  Uniform: scalar code.
+__device__ __forceinline__ int rank_of(const int32_t* starts, int nranks, int at) {
+  int r = 0;
+  while (r + 1 < nranks && starts[r + 1] <= at) ++r;
+  return r;
+}
+
+// A token's rank among alternatives: a larger logit first, then a lower id,
+// as one whole number.  -0 and 0 are equal.
+__device__ __forceinline__ uint64_t key_of(float x, int id) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t up = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return (uint64_t)up << 32 | (0xFFFFFFFFu - (uint32_t)id);
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const uint32_t up = (uint32_t)(key >> 32);
+  return __uint_as_float(up & 0x80000000u ? up & 0x7FFFFFFFu : ~up);
+}
+__device__ __forceinline__ int key_id(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
+// The least logit above that of `key`: what a later, higher id has to reach.
+__device__ __forceinline__ float above(uint64_t key) {
+  const uint64_t next = ((key >> 32) + 1) << 32;
+  return key_logit(next);
+}
+
+struct Stat {
+  float m, s, u;  // M in units of log 2 (-inf: nothing seen), and the sums
+};
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
+
+// Move a triple to a maximum that is no lower than its own.
+__device__ __forceinline__ void shift_to(Stat& a, float m) {
+  if (a.m == m) return;
+  const float d = fmaxf(a.m - m, -200.0f);  // 2^-200 is 0 in fp32
+  const float f = exp2_(d);
+  // A triple that no longer counts is dropped, but for its NaN: far out, where
+  // M's rounding exceeds the range of 2^d, its sums may be infinite.
+  a.u = f > 0.0f ? f * (a.u + a.s * d) : 0.0f;
+  a.s = f > 0.0f || a.s != a.s ? f * a.s : 0.0f;
+  a.m = m;
+}
+__device__ __forceinline__ Stat join(Stat a, Stat b) {
+  const float m = fmaxf(a.m, b.m);
+  shift_to(a, m);
+  shift_to(b, m);
+  return Stat{m, a.s + b.s, a.u + b.u};
+}
+__device__ __forceinline__ Stat wave_join(Stat a) {
+#pragma unroll
+  for (int d = 1; d < kWaveSize; d <<= 1) {
+    Stat b{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.u, d)};
+    a = join(a, b);
+  }
+  return a;
+}
+
+// Candidates for the most probable tokens, in LDS.
+struct Top {
+  uint64_t key[kCandidates];
+  uint64_t best[kMaxTop];
+  uint32_t count[3];  // appended in tile t: count[t % 3]
+  float wave_cut[kWaves];
+  uint64_t wave_best[kWaves];
+};
+
+// Keep the `k` largest of the n <= kCandidates keys (all different), sorted,
+// in `best`, unused places zero.  Every thread of the workgroup calls it.
+__device__ __forceinline__ void select_top(Top& top, int n, int k) {
+  for (int i = threadIdx.x; i < k; i += kThreads) top.best[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t mine = top.key[i];
+    int above_me = 0;
+    for (int j = 0; j < n; ++j) above_me += top.key[j] > mine;
+    if (above_me < k) top.best[above_me] = mine;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ uint64_t wave_max_key(uint64_t a) {
+#pragma unroll
+  for (int d = 1; d < kWaveSize; d <<= 1) {
+    const uint64_t b = __shfl_xor((unsigned long long)a, d);
+    a = a > b ? a : b;
+  }
+  return a;
+}
+
+// The k-th largest of the wave's 64 values (NaN counts as -inf): bitonic sort
+// across lanes, descending.
+__device__ __forceinline__ float wave_kth(float v, int k) {
+  const int lane = threadIdx.x & 63;
+  v = fmaxf(v, -INFINITY);
+#pragma unroll
+  for (int size = 2; size <= 64; size <<= 1) {
+#pragma unroll
+    for (int d = size / 2; d > 0; d >>= 1) {
+      const float o = __shfl_xor(v, d);
+      const bool larger = ((lane & size) == 0) == ((lane & d) == 0);
+      v = larger ? fmaxf(v, o) : fminf(v, o);
+    }
+  }
+  return __shfl(v, k - 1);
+}
+
+// A row whose largest logit is so far out that d_j = fma(x_j, scale2, -M) says
+// nothing (M's rounding alone passes kFar * 2^-24 = 16, or M overflows), as one
+// whose tokens are all masked by the type's lowest value: the triple again,
+// with z rounded before M is taken off, and M and d in units of 1.  `seen` is
+// the row's triple; one without any finite logit keeps M = -inf.  Every thread
+// of the workgroup calls it.
+constexpr float kFar = 268435456.0f;  // 2^28
+template <class T>
+__device__ __forceinline__ Stat rescan(const Shards& x, int64_t row, float scale, Stat seen, Stat* wave_stat) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float m = -INFINITY;
+  for (int r = 0; r < x.nranks; ++r) {
+    const typename T::bits* src = static_cast<const typename T::bits*>(x.ptr[r]) + row * x.stride[r];
+    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += kThreads) m = fmaxf(m, T::widen1(src[c]) * scale);
+  }
+#pragma unroll
+  for (int d = 1; d < kWaveSize; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  __syncthreads();
+  if (lane == 0) wave_stat[wave].m = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, wave_stat[w].m);
+  if (m == -INFINITY) return Stat{m, seen.s, 0.0f};
+  float s = 0.0f, u = 0.0f;
+  for (int r = 0; r < x.nranks; ++r) {
+    const typename T::bits* src = static_cast<const typename T::bits*>(x.ptr[r]) + row * x.stride[r];
+    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += kThreads) {
+      const float d = T::widen1(src[c]) * scale - m;
+      const float e = exp2_(d * kLog2e);
+      s += e;
+      u = __builtin_fmaf(e, fmaxf(d, -200.0f), u);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWaveSize; d <<= 1) {
+    s += __shfl_xor(s, d);
+    u += __shfl_xor(u, d);
+  }
+  __syncthreads();
+  if (lane == 0) wave_stat[wave] = Stat{m, s, u};
+  __syncthreads();
+  s = wave_stat[0].s;
+  u = wave_stat[0].u;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    s += wave_stat[w].s;
+    u += wave_stat[w].u;
+  }
+  return Stat{m, s, u};
+}
+
+// Results of a row from its joined triple and sorted best keys.  Every thread
+// of the workgroup calls it.
+template <class T>
+__device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, Stat t, const uint64_t* best,
+                                          Stat* wave_stat) {
+  const bool far = !(fabsf(t.m) <= kFar);
+  if (far) t = rescan<T>(a.x, row, a.scale, t, wave_stat);
+  const float unit = far ? 1.0f : kLn2;
+  auto logprob_of = [&](float x, float logs) {
+    if (far || fabsf(x * a.scale) > kFar) return (x * a.scale - unit * t.m) - logs;
+    return kLn2 * __builtin_fmaf(x, a.scale2, -t.m) - logs;
+  };
+  const bool empty = t.m == -INFINITY && t.s == 0.0f;  // nothing but masked tokens
+  const float logs = kLn2 * log2_(t.s);
+  const float lse = empty ? -INFINITY : unit * t.m + logs;
+  if (threadIdx.x == 0) {
+    if (a.lse) a.lse[row] = lse;
+    if (a.entropy) a.entropy[row] = empty ? 0.0f : logs - unit * t.u / t.s;
+    if (a.logprob) {
+      const int64_t id = a.ids[row];
+      float lp = 0.0f;  // no token given
+      if (id >= 0 && id < a.x.first[a.x.nranks]) {
+        const int r = rank_of(a.x.first, a.x.nranks, (int)id);
+        const float z = T::widen1(static_cast<const typename T::bits*>(a.x.ptr[r])[row * a.x.stride[r] + (id - a.x.first[r])]);
+        lp = empty ? -INFINITY : logprob_of(z, logs);
+      }
+      a.logprob[row] = lp;
+    }
+  }
+  if ((int)threadIdx.x < a.ntop) {
+    const uint64_t key = best[threadIdx.x];
+    a.top_ids[row * a.ntop + threadIdx.x] = key ? key_id(key) : -1;
+    a.top_logprobs[row * a.ntop + threadIdx.x] = key ? logprob_of(key_logit(key), logs) : -INFINITY;
+  }
+}
+
+template <class T, bool kTop>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobsArgs) {
+  const LogprobsArgs& args = kernel_args<LogprobsArgs>();
+  constexpr int kElems = kVecsPerTile * T::kVec;  // a thread's of one tile
+  constexpr int kTile = tile_elems<T>();
+  __shared__ Stat wave_stat[kWaves];
+  __shared__ std::conditional_t<kTop, Top, int> top_lds;
+  const int64_t row = blockIdx.x / args.splits;
+  const int split = (int)(blockIdx.x - row * args.splits);
+  const int tiles = args.x.tile0[args.x.nranks];
+  const int t0 = (int)((int64_t)tiles * split / args.splits), t1 = (int)((int64_t)tiles * (split + 1) / args.splits);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  Stat st{-INFINITY, 0.0f, 0.0f};
+  float cut = kLowest;  // a candidate's least logit
+  int held = 0;         // candidates in LDS
+  if constexpr (kTop) {
+    if (threadIdx.x == 0) top_lds.count[0] = top_lds.count[1] = top_lds.count[2] = 0;
+    __syncthreads();
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int r = rank_of(args.x.tile0, args.x.nranks, t);
+    const int col0 = (t - args.x.tile0[r]) * kTile;
+    const int width = args.x.first[r + 1] - args.x.first[r];
+    const typename T::bits* src = static_cast<const typename T::bits*>(args.x.ptr[r]) + row * args.x.stride[r];
+    v4u raw[kVecsPerTile];
+#pragma unroll
+    for (int v = 0; v < kVecsPerTile; ++v) {
+      const int c = col0 + (v * kThreads + (int)threadIdx.x) * T::kVec;
+      raw[v] = load_part<T>(src + c, width - c, T::kNegInf);
+    }
+    float x[kElems];
+#pragma unroll
+    for (int v = 0; v < kVecsPerTile; ++v) T::widen(raw[v], x + v * T::kVec);
+    float most = x[0];
+#pragma unroll
+    for (int i = 1; i < kElems; ++i) most = fmaxf(most, x[i]);
+    const float m = fmaxf(st.m, most * args.scale2);
+    shift_to(st, m);
+    const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < kElems; ++i) {
+      const float d = __builtin_fmaf(x[i], args.scale2, -base);
+      const float e = exp2_(d);
+      st.s += e;
+      st.u = __builtin_fmaf(e, fmaxf(d, -200.0f), st.u);  // a masked token adds 0, not 0 * -inf
+    }
+    if constexpr (kTop) {
+      Top& top = top_lds;
+      const int id0 = args.x.first[r] + col0 + (int)threadIdx.x * T::kVec;
+      if (t == t0) {
+        // the k-th largest of a wave's maxima: k tokens at least reach it
+        const float kth = wave_kth(most, args.ntop);
+        if (lane == 0) top.wave_cut[wave] = kth;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) cut = fmaxf(cut, top.wave_cut[w]);
+      }
+      uint32_t* count = &top.count[t % 3];
+      if (__any(most >= cut)) {
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+          if (x[i] >= cut) {
+            const uint32_t at = held + atomicAdd(count, 1u);
+            if (at < (uint32_t)kCandidates)
+              top.key[at] = key_of(x[i], id0 + (i / T::kVec) * kThreads * T::kVec + i % T::kVec);
+          }
+        }
+      }
+      // the next tile's counter: last read two tiles ago, before the last barrier
+      if (threadIdx.x == 0) top.count[(t + 1) % 3] = 0;
+      __syncthreads();
+      int n = held + (int)*count;
+      const bool over = n > kCandidates;
+      if (over) {
+        // More equal logits than the list holds: the best of what it held
+        // before this tile, and the tile's best one by one.
+        select_top(top, held, args.ntop);
+        if ((int)threadIdx.x < args.ntop) top.key[threadIdx.x] = top.best[threadIdx.x];
+        uint64_t last = ~0ull;
+        for (int k = 0; k < args.ntop; ++k) {
+          uint64_t mine = 0;
+#pragma unroll 1
+          for (int i = 0; i < kElems; ++i) {
+            const int c = col0 + ((i / T::kVec) * kThreads + (int)threadIdx.x) * T::kVec + i % T::kVec;
+            if (c >= width) continue;
+            const float f = T::widen1(src[c]);
+            const uint64_t key = key_of(f, args.x.first[r] + c);
+            if (f >= cut && key < last && key > mine) mine = key;
+          }
+          mine = wave_max_key(mine);
+          if (lane == 0) top.wave_best[wave] = mine;
+          __syncthreads();
+          last = 0;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) last = top.wave_best[w] > last ? top.wave_best[w] : last;
+          if (threadIdx.x == 0) top.key[args.ntop + k] = last;
+          __syncthreads();
+        }
+        n = 2 * args.ntop;  // unused places are zero: below every candidate
+      }
+      if (over || n > kCandidates / 2 || (t == t0 && n > args.ntop)) {
+        select_top(top, n, args.ntop);
+        const uint64_t kth = top.best[args.ntop - 1];
+        n = args.ntop;
+        if (kth) cut = above(kth);
+        else
+          for (n = 0; top.best[n];) ++n;
+        if ((int)threadIdx.x < n) top.key[threadIdx.x] = top.best[threadIdx.x];
+        __syncthreads();
+      }
+      held = n;
+    }
+  }
+  st = wave_join(st);
+  if (lane == 0) wave_stat[wave] = st;
+  if constexpr (kTop) select_top(top_lds, held, args.ntop);
+  else __syncthreads();
+  st = wave_stat[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) st = join(st, wave_stat[w]);
+  const uint64_t* best = nullptr;
+  if constexpr (kTop) best = top_lds.best;
+  if (args.splits == 1) {
+    write_row<T>(args, row, st, best, wave_stat);
+    return;
+  }
+  if (threadIdx.x == 0) args.parts[blockIdx.x] = v4f{st.m, st.s, st.u, 0.0f};
+  if constexpr (kTop) {
+    if ((int)threadIdx.x < args.ntop) args.keys[(int64_t)blockIdx.x * args.ntop + threadIdx.x] = best[threadIdx.x];
+  }
+}
+
+// Join a row's parts: one workgroup a row.
+template <class T>
+__global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobsArgs) {
+  const LogprobsArgs& args = kernel_args<LogprobsArgs>();
+  __shared__ Stat wave_stat[kWaves];
+  __shared__ Top top;
+  const int64_t row = blockIdx.x;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  Stat st{-INFINITY, 0.0f, 0.0f};
+  if ((int)threadIdx.x < args.splits) {
+    const v4f p = args.parts[row * args.splits + threadIdx.x];
+    st = Stat{p[0], p[1], p[2]};
+  }
+  st = wave_join(st);
+  if (lane == 0) wave_stat[wave] = st;
+  if (args.ntop) {
+    // Only keys that reach the largest of the parts' k-th keys can be among the best k.
+    const uint64_t* keys = args.keys + row * args.splits * args.ntop;
+    uint64_t least = 0;
+    if ((int)threadIdx.x < args.splits) least = keys[threadIdx.x * args.ntop + args.ntop - 1];
+    least = wave_max_key(least);
+    if (lane == 0) top.wave_best[wave] = least;
+    if (threadIdx.x == 0) top.count[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) least = top.wave_best[w] > least ? top.wave_best[w] : least;
+    for (int i = threadIdx.x; i < args.splits * args.ntop; i += kThreads) {
+      const uint64_t key = keys[i];
+      if (key && key >= least) top.key[atomicAdd(&top.count[0], 1u)] = key;
+    }
+    __syncthreads();
+    select_top(top, (int)top.count[0], args.ntop);
+  } else {
+    __syncthreads();
+  }
+  st = wave_stat[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) st = join(st, wave_stat[w]);
+  write_row<T>(args, row, st, top.best, wave_stat);
+}
+
+struct LogprobsBackwardArgs {
+  Shards x;
+  void* grad[kMaxRanks];
+  int64_t grad_stride[kMaxRanks];
+  int64_t row0;
+  float scale;
+  const int64_t* ids;
+  const float *lse, *entropy, *grad_logprob, *grad_entropy, *grad_lse;
+};
+
+// One tile of one row a workgroup.  With w = l - g - h * entropy the gradient
+// is scale * (p_j (w - h log p_j) + g [j == id]).  Bound by memory: every
+// logit read and every gradient written once.
+template <class T, bool kEntropy>
+__global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(LogprobsBackwardArgs) {
+  const LogprobsBackwardArgs& args = kernel_args<LogprobsBackwardArgs>();
+  constexpr int kTile = tile_elems<T>();
+  const uint32_t tiles = (uint32_t)args.x.tile0[args.x.nranks];
+  const int64_t row = args.row0 + blockIdx.x / tiles;
+  const int t = (int)(blockIdx.x % tiles);
+  const int r = rank_of(args.x.tile0, args.x.nranks, t);
+  const int col0 = (t - args.x.tile0[r]) * kTile;
+  const int width = args.x.first[r + 1] - args.x.first[r];
+  const typename T::bits* src = static_cast<const typename T::bits*>(args.x.ptr[r]) + row * args.x.stride[r];
+  typename T::bits* dst = static_cast<typename T::bits*>(args.grad[r]) + row * args.grad_stride[r];
+  v4u raw[kVecsPerTile];
+#pragma unroll
+  for (int v = 0; v < kVecsPerTile; ++v) {
+    const int c = col0 + (v * kThreads + (int)threadIdx.x) * T::kVec;
+    raw[v] = load_part<T>(src + c, width - c, T::kNegInf);
+  }
+  const float lse = args.lse[row];
+  const bool empty = lse == -INFINITY;
+  const int64_t id = args.ids[row];
+  const bool given = id >= 0 && id < args.x.first[args.x.nranks] && !empty;
+  const float g = given && args.grad_logprob ? args.grad_logprob[row] * args.scale : 0.0f;
+  const float h = kEntropy ? args.grad_entropy[row] * args.scale : 0.0f;
+  float w = -g;
+  if (args.grad_lse) w += args.grad_lse[row] * args.scale;
+  if (kEntropy) w -= h * args.entropy[row];
+  const int64_t at = given ? id - args.x.first[r] : -1;  // this rank's column of the given token
+#pragma unroll
+  for (int v = 0; v < kVecsPerTile; ++v) {
+    const int c = col0 + (v * kThreads + (int)threadIdx.x) * T::kVec;
+    if (c >= width) continue;
+    float x[T::kVec], d[T::kVec];
+    T::widen(raw[v], x);
+#pragma unroll
+    for (int i = 0; i < T::kVec; ++i) {
+      // z rounded first: far out, a fused x * scale - lse is the rounding of lse
+      const float logp = x[i] * args.scale - lse;
+      const float p = exp2_(logp * kLog2e);
+      d[i] = kEntropy ? p * __builtin_fmaf(-h, fmaxf(logp, -150.0f), w) : p * w;
+      if (empty) d[i] = 0.0f;
+    }
+    if (at >= c && at < c + T::kVec) {
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i)
+        if (at == c + i) d[i] += g;
+    }
+    store_part<T>(dst + c, width - c, T::round(d));
+  }
+}
+
+// ---- host -------------------------------------------------------------------
+
+rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* widths, const int64_t* strides,
+                         int nranks, int64_t rows, int dtype) {
+  if (nranks < 1 || nranks > kMaxRanks) return set_error(RAR_INVALID_ARGUMENT, "nranks must be in [1, 64]");
+  if (rar_result_t r = check_float_dtype(dtype)) return r;
+  if (rows < 0 || rows > kMaxRows) return set_error(RAR_INVALID_ARGUMENT, "rows must be in [0, 2^23]");
+  if (!widths) return set_error(RAR_INVALID_ARGUMENT, "widths is NULL");
+  const int tile = dtype == RAR_BFLOAT16 ? tile_elems<BF16>() : tile_elems<F32>();
+  int64_t vocab = 0, tiles = 0;
+  for (int r = 0; r < nranks; ++r) {
+    if (widths[r] < 0 || widths[r] > (int64_t(1) << 30))
+      return set_error(RAR_INVALID_ARGUMENT, "width of rank " + std::to_string(r) + " out of range");
+    s.first[r] = (int32_t)vocab;
+    s.tile0[r] = (int32_t)tiles;
+    vocab += widths[r];
+    tiles += (widths[r] + tile - 1) / tile;
+    if (vocab > (int64_t(1) << 30)) return set_error(RAR_INVALID_ARGUMENT, "the vocabulary must have at most 2^30 tokens");
+    if (strides && strides[r] < widths[r])
+      return set_error(RAR_INVALID_ARGUMENT, "row stride of rank " + std::to_string(r) + " below its width");
+    s.stride[r] = strides ? strides[r] : widths[r];
+  }
+  if (vocab == 0) return set_error(RAR_INVALID_ARGUMENT, "the vocabulary is empty");
+  s.first[nranks] = (int32_t)vocab;
+  s.tile0[nranks] = (int32_t)tiles;
+  s.nranks = nranks;
+  if (rows == 0 || !logits) return RAR_SUCCESS;
+  const size_t es = (size_t)elem_size(dtype);
+  for (int r = 0; r < nranks; ++r) {
+    if (widths[r] == 0) continue;
+    if (rar_result_t e = check_pointer(logits[r], es, "logits of rank " + std::to_string(r))) return e;
+    s.ptr[r] = logits[r];
+  }
+  return RAR_SUCCESS;
+}
+
+// Workgroups a row is split over: enough for about 4 per compute unit.
+int choose_splits(const Shards& s, int64_t rows, int ntop) {
+  const int tiles = s.tile0[s.nranks];
+  int64_t want = rows > 0 ? (1024 + rows - 1) / rows : 1;
+  want = std::min<int64_t>(want, std::min(tiles, kMaxSplits));
+  if (ntop) want = std::min<int64_t>(want, kCandidates / ntop);
+  return (int)std::max<int64_t>(1, want);
+}
+size_t workspace_for(int64_t rows, int splits, int ntop) {
+  return splits == 1 ? 0 : (size_t)rows * splits * (16 + 8 * (size_t)ntop);
+}
+
+rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, const int64_t* strides, int nranks,
+                           int64_t rows, int dtype, float scale, const int64_t* ids, int ntop, float* logprob,
+                           float* entropy, float* lse, int32_t* top_ids, float* top_logprobs, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  LogprobsArgs a{};
+  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype)) return r;
+  if (!(scale > 0.0f) || !std::isfinite(scale) || !std::isfinite(scale * kLog2e))
+    return set_error(RAR_INVALID_ARGUMENT, "scale must be positive and finite");
+  if (ntop < 0 || ntop > kMaxTop) return set_error(RAR_INVALID_ARGUMENT, "ntop must be in [0, 32]");
+  if (rows == 0) return RAR_SUCCESS;
+  if (!logits) return set_error(RAR_INVALID_ARGUMENT, "logits is NULL");
+  if (!logprob && !entropy && !lse && !ntop) return set_error(RAR_INVALID_ARGUMENT, "no output is asked for");
+  const size_t es = (size_t)elem_size(dtype);
+  std::vector<Block> reads, writes;
+  for (int r = 0; r < nranks; ++r)
+    reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits"});
+  auto out = [&](void* p, size_t align, int64_t bytes, const char* what) -> rar_result_t {
+    if (!p) return RAR_SUCCESS;
+    if (rar_result_t r = check_pointer(p, align, what)) return r;
+    writes.push_back({p, 1, bytes, bytes, what});
+    return RAR_SUCCESS;
+  };
+  if (logprob) {
+    if (rar_result_t r = check_pointer(ids, 8, "ids")) return r;
+    reads.push_back({ids, 1, rows * 8, rows * 8, "ids"});
+  }
+  if (ntop) {
+    if (rar_result_t r = check_pointer(top_ids, 4, "top_ids")) return r;
+    if (rar_result_t r = check_pointer(top_logprobs, 4, "top_logprobs")) return r;
+  }
+  if (rar_result_t r = out(logprob, 4, rows * 4, "logprob")) return r;
+  if (rar_result_t r = out(entropy, 4, rows * 4, "entropy")) return r;
+  if (rar_result_t r = out(lse, 4, rows * 4, "lse")) return r;
+  if (ntop) {
+    if (rar_result_t r = out(top_ids, 4, rows * ntop * 4, "top_ids")) return r;
+    if (rar_result_t r = out(top_logprobs, 4, rows * ntop * 4, "top_logprobs")) return r;
+  }
+  a.splits = choose_splits(a.x, rows, ntop);
+  const size_t need = workspace_for(rows, a.splits, ntop);
+  if (need) {
+    if (workspace_bytes < need)
+      return set_error(RAR_INVALID_ARGUMENT, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
+                                                 std::to_string(need) + " needed");
+    if (rar_result_t r = out(workspace, 16, (int64_t)need, "workspace")) return r;
+    if (!workspace) return set_error(RAR_INVALID_ARGUMENT, "workspace is NULL");
+  }
+  if (rar_result_t r = check_blocks(reads, writes, false)) return r;
+  a.rows = rows;
+  a.ntop = ntop;
+  a.scale = scale;
+  a.scale2 = scale * kLog2e;
+  a.ids = ids;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.parts = static_cast<v4f*>(workspace);
+  a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + (size_t)rows * a.splits * 16);
+  const bool bf = dtype == RAR_BFLOAT16;
+  const void* fn = bf ? (ntop ? reinterpret_cast<const void*>(&logprobs_kernel<BF16, true>)
+                              : reinterpret_cast<const void*>(&logprobs_kernel<BF16, false>))
+                      : (ntop ? reinterpret_cast<const void*>(&logprobs_kernel<F32, true>)
+                              : reinterpret_cast<const void*>(&logprobs_kernel<F32, false>));
+  if (rar_result_t r = launch_kernel(fn, dim3((unsigned)(rows * a.splits)), dim3(kThreads), &a, stream)) return r;
+  if (a.splits == 1) return RAR_SUCCESS;
+  const void* join_fn = bf ? reinterpret_cast<const void*>(&logprobs_join_kernel<BF16>)
+                           : reinterpret_cast<const void*>(&logprobs_join_kernel<F32>);
+  return launch_kernel(join_fn, dim3((unsigned)rows), dim3(kThreads), &a, stream);
+}
+
+rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* widths, const int64_t* strides,
+                                    int nranks, int64_t rows, int dtype, float scale, const int64_t* ids,
+                                    const float* lse, const float* entropy, const float* grad_logprob,
+                                    const float* grad_entropy, const float* grad_lse, void* const* grads,
+                                    const int64_t* grad_strides, void* stream) {
+  LogprobsBackwardArgs a{};
+  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype)) return r;
+  if (!(scale > 0.0f) || !std::isfinite(scale))
+    return set_error(RAR_INVALID_ARGUMENT, "scale must be positive and finite");
+  if (rows == 0) return RAR_SUCCESS;
+  if (!logits || !grads) return set_error(RAR_INVALID_ARGUMENT, "logits or grads is NULL");
+  const size_t es = (size_t)elem_size(dtype);
+  std::vector<Block> reads, writes;
+  for (int r = 0; r < nranks; ++r) {
+    reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits of another rank"});
+    a.grad_stride[r] = grad_strides ? grad_strides[r] : widths[r];
+    if (widths[r] == 0) continue;
+    if (rar_result_t e = check_pointer(grads[r], es, "gradient of rank " + std::to_string(r))) return e;
+    if (a.grad_stride[r] < widths[r])
+      return set_error(RAR_INVALID_ARGUMENT, "gradient row stride of rank " + std::to_string(r) + " below its width");
+    a.grad[r] = grads[r];
+    writes.push_back({grads[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.grad_stride[r] * es), "gradient"});
+  }
+  auto in = [&](const void* p, size_t size, const char* what) -> rar_result_t {
+    if (!p) return RAR_SUCCESS;
+    if (rar_result_t r = check_pointer(p, size, what)) return r;
+    reads.push_back({p, 1, (int64_t)(rows * size), (int64_t)(rows * size), what});
+    return RAR_SUCCESS;
+  };
+  if (!ids || !lse) return set_error(RAR_INVALID_ARGUMENT, "ids or lse is NULL");
+  if (!grad_logprob && !grad_entropy && !grad_lse) return set_error(RAR_INVALID_ARGUMENT, "no gradient is given");
+  if (grad_entropy && !entropy) return set_error(RAR_INVALID_ARGUMENT, "entropy is NULL");
+  if (rar_result_t r = in(ids, 8, "ids")) return r;
+  if (rar_result_t r = in(lse, 4, "lse")) return r;
+  if (rar_result_t r = in(grad_entropy ? entropy : nullptr, 4, "entropy")) return r;
+  if (rar_result_t r = in(grad_logprob, 4, "grad_logprob")) return r;
+  if (rar_result_t r = in(grad_entropy, 4, "grad_entropy")) return r;
+  if (rar_result_t r = in(grad_lse, 4, "grad_lse")) return r;
+  if (rar_result_t r = check_blocks(reads, writes, true)) return r;
+  a.scale = scale;
+  a.ids = ids;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.grad_logprob = grad_logprob;
+  a.grad_entropy = grad_entropy;
+  a.grad_lse = grad_lse;
+  const bool bf = dtype == RAR_BFLOAT16;
+  const void* fn = bf ? (grad_entropy ? reinterpret_cast<const void*>(&logprobs_backward_kernel<BF16, true>)
+                                      : reinterpret_cast<const void*>(&logprobs_backward_kernel<BF16, false>))
+                      : (grad_entropy ? reinterpret_cast<const void*>(&logprobs_backward_kernel<F32, true>)
+                                      : reinterpret_cast<const void*>(&logprobs_backward_kernel<F32, false>));
+  // rows that one grid can hold, launch after launch
+  const int64_t tiles = a.x.tile0[nranks];
+  for (int64_t row0 = 0, step = std::max<int64_t>(1, kMaxBlocks / tiles); row0 < rows; row0 += step) {
+    a.row0 = row0;
+    const int64_t blocks = std::min(step, rows - row0) * tiles;
+    if (rar_result_t r = launch_kernel(fn, dim3((unsigned)blocks), dim3(kThreads), &a, stream)) return r;
+  }
+  return RAR_SUCCESS;
+}
+
+}  // namespace
+}  // namespace rar
+
+extern "C" {
+
+rar_result_t rar_logprobs_workspace(const int64_t* widths, int nranks, int64_t rows, rar_dtype_t dtype, int ntop,
+                                    size_t* bytes) {
+  return rar::guarded([&]() -> rar_result_t {
+    rar::Shards s{};
+    if (!bytes) return rar::set_error(RAR_INVALID_ARGUMENT, "bytes is NULL");
+    if (rar_result_t r = rar::fill_shards(s, nullptr, widths, nullptr, nranks, rows, dtype)) return r;
+    if (ntop < 0 || ntop > rar::kMaxTop) return rar::set_error(RAR_INVALID_ARGUMENT, "ntop must be in [0, 32]");
+    *bytes = rar::workspace_for(rows, rar::choose_splits(s, rows, ntop), ntop);
+    return RAR_SUCCESS;
+  });
+}
+
+rar_result_t rar_logprobs(const void* const* logits, const int64_t* widths, const int64_t* strides, int nranks,
+                          int64_t rows, rar_dtype_t dtype, float scale, const int64_t* ids, int ntop, float* logprob,
+                          float* entropy, float* lse, int32_t* top_ids, float* top_logprobs, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  return rar::guarded([&] {
+    return rar::logprobs_call(logits, widths, strides, nranks, rows, dtype, scale, ids, ntop, logprob, entropy, lse,
+                              top_ids, top_logprobs, workspace, workspace_bytes, stream);
+  });
+}
+
+rar_result_t rar_logprobs_backward(const void* const* logits, const int64_t* widths, const int64_t* strides,
+                                   int nranks, int64_t rows, rar_dtype_t dtype, float scale, const int64_t* ids,
+                                   const float* lse, const float* entropy, const float* grad_logprob,
+                                   const float* grad_entropy, const float* grad_lse, void* const* grads,
+                                   const int64_t* grad_strides, void* stream) {
+  return rar::guarded([&] {
+    return rar::logprobs_backward_call(logits, widths, strides, nranks, rows, dtype, scale, ids, lse, entropy,
+                                       grad_logprob, grad_entropy, grad_lse, grads, grad_strides, stream);
+  });
+}
+
+}  // extern "C"

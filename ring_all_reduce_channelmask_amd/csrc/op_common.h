@@ -1,0 +1,202 @@
+// op_common.h -- what the operators around an AllReduce share (dropout.hip,
+// logprobs.hip, adapters.hip): host-side argument checks, the C boundary's
+// exception guard, and the device types and conversions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "capi_internal.h"
+
+namespace rar {
+
+// ---- host -------------------------------------------------------------------
+
+// A rectangle of device memory that a call reads or writes: `rows` rows of
+// `width` bytes, `stride` bytes apart.
+struct Block {
+  const void* ptr;
+  int64_t rows, width, stride;
+  const char* what;
+};
+
+// Whether two rectangles share a byte.  Exact for equal strides (columns of
+// one matrix are disjoint although their address ranges interleave);
+// rectangles of different strides count as sharing where their ranges do.
+inline bool blocks_overlap(const Block& a, const Block& b) {
+  if (a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+  const int64_t pa = (int64_t)(uintptr_t)a.ptr, pb = (int64_t)(uintptr_t)b.ptr;
+  const int64_t ea = pa + (a.rows - 1) * a.stride + a.width, eb = pb + (b.rows - 1) * b.stride + b.width;
+  if (ea <= pb || eb <= pa) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  // A single row takes the other's stride: wider than that, it meets a row.
+  const int64_t stride = a.rows > 1 ? a.stride : b.stride;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  const int64_t d = (((pb - pa) % stride) + stride) % stride;  // b's column in a's rows
+  return d < a.width || d + b.width > stride;
+}
+
+// Outputs share no byte with each other, and with an input only where both
+// are the same rectangle and `in_place` allows it: every element is then
+// read by the thread that writes it, before it writes.
+inline rar_result_t check_blocks(const std::vector<Block>& reads, const std::vector<Block>& writes, bool in_place) {
+  for (size_t i = 0; i < writes.size(); ++i) {
+    for (size_t j = i + 1; j < writes.size(); ++j)
+      if (blocks_overlap(writes[i], writes[j]))
+        return set_error(RAR_INVALID_ARGUMENT, std::string(writes[i].what) + " " + std::to_string(i) + " overlaps " +
+                                                   writes[j].what + " " + std::to_string(j));
+    for (const Block& r : reads) {
+      if (!blocks_overlap(writes[i], r)) continue;
+      const bool same = writes[i].ptr == r.ptr && writes[i].rows == r.rows && writes[i].width == r.width &&
+                        (writes[i].stride == r.stride || r.rows == 1);
+      if (!in_place || !same)
+        return set_error(RAR_INVALID_ARGUMENT, std::string(writes[i].what) + " " + std::to_string(i) + " overlaps " + r.what);
+    }
+  }
+  return RAR_SUCCESS;
+}
+
+inline rar_result_t check_float_dtype(int dtype) {
+  if (dtype != RAR_FLOAT32 && dtype != RAR_BFLOAT16)
+    return set_error(RAR_INVALID_ARGUMENT, "dtype must be float32 or bfloat16");
+  return RAR_SUCCESS;
+}
+
+inline rar_result_t check_pointer(const void* p, size_t align, const std::string& what) {
+  if (!p) return set_error(RAR_INVALID_ARGUMENT, what + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+    return set_error(RAR_INVALID_ARGUMENT, what + " is not aligned to its element size");
+  return RAR_SUCCESS;
+}
+
+// Run the body of a C entry point: no C++ exception leaves it.
+template <class F>
+rar_result_t guarded(F&& body) {
+  try {
+    clear_error();
+    return body();
+  } catch (...) {
+    try {
+      return set_error(RAR_INTERNAL_ERROR, "out of host memory");
+    } catch (...) {
+      return RAR_INTERNAL_ERROR;
+    }
+  }
+}
+
+inline rar_result_t launch_kernel(const void* fn, dim3 grid, dim3 block, void* args, void* stream) {
+  void* params[] = {args};
+  const hipError_t e = hipLaunchKernel(fn, grid, block, params, 0, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return set_error(RAR_HIP_ERROR, std::string("kernel launch failed: ") + hipGetErrorString(e));
+  return RAR_SUCCESS;
+}
+
+// ---- device -----------------------------------------------------------------
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+// Rows and buffers need only element alignment: gfx950 serves unaligned
+// global vector accesses in hardware.
+typedef uint32_t v4u_user __attribute__((ext_vector_type(4), aligned(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ v4u load_nt(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const v4u_user*>(p));
+}
+__device__ __forceinline__ v4u load_16(const void* p) { return *static_cast<const v4u_user*>(p); }
+__device__ __forceinline__ void store_nt(void* p, v4u v) {
+  __builtin_nontemporal_store((v4u_user)v, static_cast<v4u_user*>(p));
+}
+
+// Payload types: how many elements a 16-byte vector holds, widening to fp32
+// (exact) and rounding to nearest even.
+struct F32 {
+  typedef uint32_t bits;
+  static constexpr int kVec = 4;
+  static constexpr uint32_t kNegInf = 0xFF800000u;  // a word of -inf elements
+  static __device__ __forceinline__ void widen(v4u x, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x[i]);
+  }
+  static __device__ __forceinline__ v4u round(const float* f) {
+    v4u r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(f[i]);
+    return r;
+  }
+  static __device__ __forceinline__ float widen1(bits x) { return __uint_as_float(x); }
+  static __device__ __forceinline__ bits round1(float f) { return __float_as_uint(f); }
+};
+struct BF16 {
+  typedef uint16_t bits;
+  static constexpr int kVec = 8;
+  static constexpr uint32_t kNegInf = 0xFF80FF80u;
+  static __device__ __forceinline__ void widen(v4u x, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(x[i] << 16);
+      f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ v4u round(const float* f) {
+    v4u r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{f[2 * i], f[2 * i + 1]}, v2bf));
+    return r;
+  }
+  static __device__ __forceinline__ float widen1(bits x) { return __uint_as_float((uint32_t)x << 16); }
+  static __device__ __forceinline__ bits round1(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+
+// A kernel's arguments (its only parameter, of type A) where the launch put
+// them.  Through the parameter itself a large structure that is indexed at run
+// time may be copied to scratch memory first.
+template <class A>
+__device__ __forceinline__ const A& kernel_args() {
+  typedef const __attribute__((address_space(4))) A* P;
+  return *(const A*)(P)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+// The first `n` (0..kVec) elements at p as a vector, the rest -inf or zero.
+template <class T>
+__device__ __forceinline__ v4u load_part(const typename T::bits* p, int n, uint32_t fill) {
+  if (n >= T::kVec) return load_nt(p);
+  v4u r = {fill, fill, fill, fill};
+#pragma unroll
+  for (int i = 0; i < T::kVec; ++i) {
+    if (i < n) {
+      if constexpr (T::kVec == 4) {
+        r[i] = p[i];
+      } else {
+        const int sh = 16 * (i & 1);
+        r[i / 2] = (r[i / 2] & ~(0xFFFFu << sh)) | ((uint32_t)p[i] << sh);
+      }
+    }
+  }
+  return r;
+}
+template <class T>
+__device__ __forceinline__ void store_part(typename T::bits* p, int n, v4u v) {
+  if (n >= T::kVec) {
+    store_nt(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < T::kVec; ++i) {
+    if (i < n) {
+      if constexpr (T::kVec == 4) p[i] = v[i];
+      else p[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
+}  // namespace rar
