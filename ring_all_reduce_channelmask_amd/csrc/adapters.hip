@@ -24,17 +24,18 @@ namespace {
 
 constexpr int kMaxRank = 128;  // of an adapter
 constexpr int kThreads = 256, kWaves = kThreads / kWaveSize;
+constexpr int kMaxParts = 16;
 
 struct ShrinkArgs {
   const void* x[kMaxRanks];
   int64_t x_stride[kMaxRanks];
   const void* down[kMaxRanks];   // [adapters][rank][width]
   int32_t width[kMaxRanks];
-  int32_t part0[kMaxRanks + 1];  // first part of each rank
+  int32_t step0[kMaxRanks + 1];  // first step of each rank
   const int64_t* ids;
   float* h;                      // [parts][tokens][rank]
   int64_t tokens;
-  int32_t nranks, adapters, rank, part_width, slots;
+  int32_t nranks, adapters, rank, parts, slots;
 };
 struct ExpandArgs {
   const void* partial[kMaxRanks];
@@ -46,9 +47,13 @@ struct ExpandArgs {
   const float* scales;
   const float* h;
   int64_t tokens;
+  int64_t run0;                  // first run of the launch
   int32_t nranks, ncopies, adapters, rank, outer, parts;
-  int32_t tiles_per_block;       // token tiles that a workgroup takes in turn
 };
+
+// A step of the inner dimension: 2 vectors for each of the 4 lane groups.
+template <class T>
+constexpr int step_width() { return 8 * T::kVec; }
 
 // One 16-byte vector of each operand: 32 (bf16) or 16 (fp32) of the inner
 // dimension, lane group g = lane / 16 holding places g * kVec ...
@@ -65,103 +70,188 @@ __device__ __forceinline__ v4f mma(v4u a, v4u b, v4f c) {
   }
 }
 
-// The adapter of the token that this lane's copy of a tile stands for, or -1.
+// The adapter of a token, or -1.
 __device__ __forceinline__ int load_id(const int64_t* ids, int64_t token, int64_t tokens, int adapters) {
   if (token >= tokens) return -1;
   const int64_t id = ids[token];
   return id >= 0 && id < adapters ? (int)id : -1;
 }
 
-// h of 16 tokens and one part of the inner dimension, for the adapters
-// slot, slot + slots, ... of the tile.  The waves split the part between them
-// and their sums meet in LDS.
-template <class T, int kN>  // kN tiles of 16 cover the adapter's rank
+// h of 16 * kM tokens and one part of the inner dimension, for the adapters
+// slot, slot + slots, ... of the tile.  The waves split the part's steps
+// between them and their sums meet in LDS.  kN tiles of 16 cover the
+// adapter's rank.
+template <class T, int kN, int kM>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
   const ShrinkArgs& args = kernel_args<ShrinkArgs>();
-  __shared__ v4f sums[kWaves][kN][kWaveSize];
-  constexpr int kStep = 4 * T::kVec;  // inner places of one vector over the lane groups
+  __shared__ v4f sums[kWaves][kM][kN][kWaveSize];
+  constexpr int kStep = step_width<T>();
+  typedef typename T::bits bits;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
-  const int64_t token0 = (int64_t)blockIdx.x * 16;
-  const int part = blockIdx.y;
-  int r = 0;
-  while (r + 1 < args.nranks && args.part0[r + 1] <= part) ++r;
-  const int width = args.width[r];
-  const int begin = (part - args.part0[r]) * args.part_width;
-  const int end = begin + args.part_width < width ? begin + args.part_width : width;
-  const int id = load_id(args.ids, token0 + at, args.tokens, args.adapters);
-  const typename T::bits* xrow =
-      static_cast<const typename T::bits*>(args.x[r]) + (token0 + at) * args.x_stride[r];
-  uint64_t left = __ballot(id >= 0) & 0xFFFF;
+  const int64_t token0 = (int64_t)blockIdx.x * 16 * kM;
+  const int part = blockIdx.y, steps = args.step0[args.nranks];
+  const int begin = (int)((int64_t)steps * part / args.parts), end = (int)((int64_t)steps * (part + 1) / args.parts);
+  // lane l stands for token l of the tile
+  const int id = lane < 16 * kM ? load_id(args.ids, token0 + lane, args.tokens, args.adapters) : -1;
+  uint64_t left = __ballot(id >= 0);
   for (int k = 0; left; ++k) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const bool mine = id == a;
-    left &= ~__ballot(mine);
+    const uint64_t members = __ballot(id == a);
+    left &= ~members;
     if (k % args.slots != (int)blockIdx.z) continue;
-    const typename T::bits* w =
-        static_cast<const typename T::bits*>(args.down[r]) + (int64_t)a * args.rank * width;
-    v4f acc[kN];
+    v4f acc[kM][kN];
 #pragma unroll
-    for (int n = 0; n < kN; ++n) acc[n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = begin + wave * 2 * kStep; c < end; c += kWaves * 2 * kStep) {
-      // two vectors a lane, side by side: the inner dimension's order within
-      // a step is free as long as both operands take the same
-      v4u xa[2], wb[kN][2];
+    for (int m = 0; m < kM; ++m)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int col = c + (group * 2 + v) * T::kVec;
-        xa[v] = load_part<T>(xrow + col, mine ? end - col : 0, 0);
+      for (int n = 0; n < kN; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int step = begin + wave; step < end; step += kWaves) {
+      int r = 0;
+      while (r + 1 < args.nranks && args.step0[r + 1] <= step) ++r;
+      const int width = args.width[r];
+      const int col0 = (step - args.step0[r]) * kStep;
+      const bits* x = static_cast<const bits*>(args.x[r]);
+      const bits* w = static_cast<const bits*>(args.down[r]) + (int64_t)a * args.rank * width;
+      // Two vectors a lane, side by side: the inner dimension's order within
+      // a step is free as long as both operands take the same.  Rows past the
+      // adapter's rank repeat its last one and are not written.
+      v4u xa[kM][2], wb[kN][2];
+      const int col = col0 + group * 2 * T::kVec;
+      const bool full = col0 + kStep <= width;
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          const int row = n * 16 + at;
-          wb[n][v] = load_part<T>(w + (int64_t)row * width + col, row < args.rank ? end - col : 0, 0);
+      for (int n = 0; n < kN; ++n) {
+        const int row = n * 16 + at < args.rank ? n * 16 + at : args.rank - 1;
+        const bits* p = w + (int64_t)row * width + col;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          wb[n][v] = full ? load_16(p + v * T::kVec) : load_part<T>(p + v * T::kVec, width - col - v * T::kVec, 0);
+      }
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const bool mine = members >> (m * 16 + at) & 1;
+        const bits* p = x + (token0 + m * 16 + at) * args.x_stride[r] + col;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          xa[m][v] = v4u{0, 0, 0, 0};
+          if (mine) xa[m][v] = full ? load_16(p + v * T::kVec) : load_part<T>(p + v * T::kVec, width - col - v * T::kVec, 0);
         }
       }
 #pragma unroll
       for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int n = 0; n < kN; ++n) acc[n] = mma<T>(xa[v], wb[n][v], acc[n]);
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int n = 0; n < kN; ++n) acc[m][n] = mma<T>(xa[m][v], wb[n][v], acc[m][n]);
     }
     __syncthreads();  // the previous adapter's sums have been read
 #pragma unroll
-    for (int n = 0; n < kN; ++n) sums[wave][n][lane] = acc[n];
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) sums[wave][m][n][lane] = acc[m][n];
     __syncthreads();
     // lane: column (place in the adapter's rank) `at`, rows (tokens) 4 * group + i
-    for (int n = wave; n < kN; n += kWaves) {
-      v4f s = sums[0][n][lane];
+    for (int q = wave; q < kM * kN; q += kWaves) {
+      const int m = q / kN, n = q % kN;
+      v4f s = sums[0][m][n][lane];
 #pragma unroll
-      for (int o = 1; o < kWaves; ++o) s += sums[o][n][lane];
+      for (int o = 1; o < kWaves; ++o) s += sums[o][m][n][lane];
       const int col = n * 16 + at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 4 * group + i;
-        const int id_of_row = __builtin_amdgcn_ds_bpermute(row * 4, id);  // with every lane active
-        if (col < args.rank && id_of_row == a)
+        const int row = m * 16 + 4 * group + i;
+        if (col < args.rank && (members >> row & 1))
           args.h[((int64_t)part * args.tokens + token0 + row) * args.rank + col] = s[i];
       }
     }
   }
 }
 
-// y of 16 tokens x 64 columns a wave, for `tiles_per_block` token tiles in
-// turn.  The columns are the MFMA's rows: row m of tile j is column
-// (m / 4) * 16 + j * 4 + m % 4, so that a lane's results over the four tiles
-// are 16 neighbouring columns of one token.
-template <class T, int kR>  // kR vectors of each lane group cover the adapter's rank
+// Place q of h of a token: its parts' sum.  The loads of 8 parts are issued
+// together.
+__device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int parts) {
+  float s = 0.0f;
+  for (int p0 = 0; p0 < parts; p0 += 8) {
+    float f[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) f[p] = p0 + p < parts ? h[(int64_t)(p0 + p) * stride] : 0.0f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) s += f[p];
+  }
+  return s;
+}
+
+// y of a run of kTiles * 16 tokens x 64 columns a wave.  The columns are the
+// MFMA's rows, dealt so that a lane's results over the four tiles are whole
+// 16-byte vectors of one token and the four lane groups' vectors are
+// neighbours: a store of half lines costs more than one of whole ones.  The run's h is laid out in LDS first, for bf16 as two bf16 numbers
+// whose sum has 16 bits of it.
+template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
 __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
+  constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts
+  constexpr int kForms = T::kVec == 8 ? 2 : 1;
+  constexpr int kPer = T::kVec / 4;     // tiles that make up a vector
   typedef typename T::bits bits;
+  __shared__ v4u hs[kForms][kTiles * 16][kRowVecs];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
+  const int64_t run0 = (args.run0 + blockIdx.y) * kTiles * 16;
+  constexpr int kQuads = kR * kStep / 4;  // of a token's h
+#pragma unroll 4
+  for (int i = threadIdx.x; i < kTiles * 16 * kQuads; i += kThreads) {
+    const int t = i / kQuads, q = i % kQuads * 4;
+    const int64_t token = run0 + t;
+    const int id = load_id(args.ids, token, args.tokens, args.adapters);
+    const int places = id >= 0 ? args.rank - q : 0;
+    float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p0 = 0; p0 < args.parts; p0 += 4) {
+      float f[4][4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        load4<F32>(reinterpret_cast<const uint32_t*>(args.h + ((p0 + p) * args.tokens + token) * args.rank + q),
+                   p0 + p < args.parts ? places : 0, f[p]);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] += f[p][j];
+    }
+    const float scale = id >= 0 && args.scales ? args.scales[id] : 1.0f;
+    float low[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] *= scale;
+      low[j] = h[j] - T::widen1(T::round1(h[j]));
+    }
+    store4<T>(reinterpret_cast<bits*>(hs[0][t]) + q, 4, h);
+    if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
+  }
+  __syncthreads();
   const int col0 = ((int)blockIdx.x * kWaves + wave) * 64;
-  const int col = col0 + group * 16;
+  const int col = col0 + group * T::kVec;  // of vector v: + v * kStep
   if (col0 >= args.outer) return;
+  const bool full = col0 + 64 <= args.outer;
   int held = -1;  // the adapter whose weights are in registers
   v4u w[4][kR];
-  for (int tile = 0; tile < args.tiles_per_block; ++tile) {
-    const int64_t token0 = ((int64_t)blockIdx.y * args.tiles_per_block + tile) * 16;
+  for (int tile = 0; tile < kTiles; ++tile) {
+    const int64_t token0 = run0 + tile * 16;
     if (token0 >= args.tokens) return;
     const int64_t token = token0 + at;
+    const bool live = token < args.tokens;
     const int id = load_id(args.ids, token, args.tokens, args.adapters);
+    float y[16];
+    v4u p[kBatch][kVecs];
+    auto load_partials = [&](int r0) {
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r) {
+        if (r0 + r < args.nranks) {
+          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) +
+                            (live ? token : token0) * args.partial_stride[r0 + r] + col;
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v)
+            p[r][v] = full ? load_nt(src + v * kStep) : load_part<T>(src + v * kStep, args.outer - col - v * kStep, 0);
+        }
+      }
+    };
+    load_partials(0);  // in flight during the products
     v4f sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -173,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
       if (a != held) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int d = col0 + (at >> 2) * 16 + j * 4 + (at & 3);
+          const int d = col0 + j / kPer * kStep + (at >> 2) * T::kVec + j % kPer * 4 + (at & 3);
           const bits* row = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + d) * args.rank;
 #pragma unroll
           for (int c = 0; c < kR; ++c) {
@@ -183,54 +273,22 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
         }
         held = a;
       }
-      const float scale = args.scales ? args.scales[a] : 1.0f;
       v4f acc[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < kR; ++c) {
-        const int q = c * kStep + group * T::kVec;
-        float h[T::kVec];
+      for (int c = 0; c < kR; ++c)
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) h[i] = 0.0f;
-        if (mine) {
-          for (int p = 0; p < args.parts; ++p) {
-            const float* src = args.h + ((int64_t)p * args.tokens + token) * args.rank + q;
+        for (int f = 0; f < kForms; ++f) {
+          const v4u h = hs[f][tile * 16 + at][c * 4 + group];
 #pragma unroll
-            for (int i = 0; i < T::kVec; ++i)
-              if (q + i < args.rank) h[i] += src[i];
-          }
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) h[i] *= scale;
+          for (int j = 0; j < 4; ++j) acc[j] = mma<T>(w[j][c], h, acc[j]);
         }
-        const v4u high = T::round(h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = mma<T>(w[j][c], high, acc[j]);
-        if constexpr (T::kVec == 8) {
-          float back[8];
-          T::widen(high, back);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] -= back[i];
-          const v4u low = T::round(h);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = mma<T>(w[j][c], low, acc[j]);
-        }
-      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum[j] = mine ? acc[j] : sum[j];
     }
-    if (token >= args.tokens) continue;
-    float y[16];
     for (int r0 = 0; r0 < args.nranks; r0 += kBatch) {
-      v4u p[kBatch][kVecs];
-#pragma unroll
-      for (int r = 0; r < kBatch; ++r) {
-        if (r0 + r < args.nranks) {
-          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + token * args.partial_stride[r0 + r] + col;
-#pragma unroll
-          for (int v = 0; v < kVecs; ++v) p[r][v] = load_part<T>(src + v * T::kVec, args.outer - col - v * T::kVec, 0);
-        }
-      }
+      if (r0) load_partials(r0);
 #pragma unroll
       for (int r = 0; r < kBatch; ++r) {
         if (r0 + r < args.nranks) {
@@ -244,47 +302,146 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) y[i] += sum[i / 4][i % 4];
-    for (int k = 0; k < args.ncopies; ++k) {
-      bits* dst = static_cast<bits*>(args.out[k]) + token * args.out_stride[k] + col;
+    if (live) {
+      for (int k = 0; k < args.ncopies; ++k) {
+        bits* dst = static_cast<bits*>(args.out[k]) + token * args.out_stride[k] + col;
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v)
-        store_part<T>(dst + v * T::kVec, args.outer - col - v * T::kVec, T::round(y + v * T::kVec));
+        for (int v = 0; v < kVecs; ++v) {
+          const v4u o = T::round(y + v * T::kVec);
+          if (full) store_nt(dst + v * kStep, o);
+          else store_part<T>(dst + v * kStep, args.outer - col - v * kStep, o);
+        }
+      }
     }
   }
 }
 
-template <class T>
-const void* pick_shrink(int rank) {
-  if (rank <= 16) return reinterpret_cast<const void*>(&shrink_kernel<T, 1>);
-  if (rank <= 32) return reinterpret_cast<const void*>(&shrink_kernel<T, 2>);
-  if (rank <= 64) return reinterpret_cast<const void*>(&shrink_kernel<T, 4>);
-  return reinterpret_cast<const void*>(&shrink_kernel<T, 8>);
-}
-template <class T>
-const void* pick_expand(int rank) {
-  if (rank <= 4 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 1>);
-  if (rank <= 8 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 2>);
-  if (rank <= 16 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 4>);
-  return reinterpret_cast<const void*>(&expand_kernel<T, 8>);
+// y of one token x kCols columns: for few tokens, which have few neighbours
+// with the same adapter.  kLanes lanes take a row of the adapter's weights, a
+// vector each, so that a wave reads neighbouring rows whole.
+constexpr int kCols = 1024;
+template <class T, int kLanes>
+__global__ void __launch_bounds__(kThreads) expand_token_kernel(ExpandArgs) {
+  const ExpandArgs& args = kernel_args<ExpandArgs>();
+  typedef typename T::bits bits;
+  constexpr int kRows = kThreads / kLanes, kBatch = 4;
+  __shared__ float hs[kLanes * T::kVec];
+  __shared__ float delta[kCols];
+  const int64_t token = blockIdx.y;
+  const int col0 = blockIdx.x * kCols, tid = threadIdx.x;
+  const int cols = args.outer - col0 < kCols ? args.outer - col0 : kCols;
+  const int mine = cols - tid * 4;  // of this thread's four neighbouring columns
+  const int a = load_id(args.ids, token, args.tokens, args.adapters);  // uniform
+  float p[kBatch][4];
+  auto load_partials = [&](int r0) {
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) {
+      if (r0 + r < args.nranks) {
+        const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + token * args.partial_stride[r0 + r] + col0 + tid * 4;
+        load4<T>(src, mine, p[r]);
+      }
+    }
+  };
+  load_partials(0);
+  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a >= 0) {
+    if (tid < kLanes * T::kVec)
+      hs[tid] = tid < args.rank ? sum_parts(args.h + token * args.rank + tid, args.tokens * args.rank, args.parts) *
+                                      (args.scales ? args.scales[a] : 1.0f)
+                                : 0.0f;
+    __syncthreads();
+    const int q = tid % kLanes * T::kVec;
+    float h[T::kVec];
+#pragma unroll
+    for (int i = 0; i < T::kVec; ++i) h[i] = hs[q + i];
+    const bits* up = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + col0) * args.rank + q;
+#pragma unroll 8
+    for (int row0 = 0; row0 < kCols; row0 += kRows) {
+      const int row = row0 + tid / kLanes;
+      const v4u v = load_part<T>(up + (int64_t)row * args.rank, row < cols ? args.rank - q : 0, 0);
+      float f[T::kVec], s = 0.0f;
+      T::widen(v, f);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) s = __builtin_fmaf(f[i], h[i], s);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor(s, o);
+      if (tid % kLanes == 0) delta[row] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = delta[tid * 4 + i];
+  }
+  float y[4];
+  for (int r0 = 0; r0 < args.nranks; r0 += kBatch) {
+    if (r0) load_partials(r0);
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r)
+      if (r0 + r < args.nranks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = r0 + r == 0 ? p[r][i] : y[i] + p[r][i];
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] += d[i];
+  for (int k = 0; k < args.ncopies; ++k)
+    store4<T>(static_cast<bits*>(args.out[k]) + token * args.out_stride[k] + col0 + tid * 4, mine, y);
 }
 
-// How the inner dimension is cut: parts of `width` that do not cross ranks.
-struct Parts {
-  int width = 0;
-  int first[kMaxRanks + 1] = {};
+template <class T, int kM>
+const void* pick_shrink(int rank) {
+  if (rank <= 16) return reinterpret_cast<const void*>(&shrink_kernel<T, 1, kM>);
+  if (rank <= 32) return reinterpret_cast<const void*>(&shrink_kernel<T, 2, kM>);
+  if (rank <= 64) return reinterpret_cast<const void*>(&shrink_kernel<T, 4, kM>);
+  return reinterpret_cast<const void*>(&shrink_kernel<T, 8, kM>);
+}
+// Token tiles of a run: its h takes at most 36 KB of LDS.
+constexpr int kRunTiles = 8;
+template <class T>
+const void* pick_expand(int rank, int* tiles) {
+  *tiles = kRunTiles;
+  if (rank <= 4 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 1, kRunTiles>);
+  if (rank <= 8 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 2, kRunTiles>);
+  if constexpr (T::kVec == 8) {
+    *tiles = kRunTiles / 2;
+    return reinterpret_cast<const void*>(&expand_kernel<T, 4, kRunTiles / 2>);
+  } else {
+    if (rank <= 16 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 4, kRunTiles>);
+    *tiles = kRunTiles / 2;
+    return reinterpret_cast<const void*>(&expand_kernel<T, 8, kRunTiles / 2>);
+  }
+}
+template <class T>
+const void* pick_expand_token(int rank) {
+  if (rank <= T::kVec) return reinterpret_cast<const void*>(&expand_token_kernel<T, 1>);
+  if (rank <= 2 * T::kVec) return reinterpret_cast<const void*>(&expand_token_kernel<T, 2>);
+  if (rank <= 4 * T::kVec) return reinterpret_cast<const void*>(&expand_token_kernel<T, 4>);
+  if (rank <= 8 * T::kVec) return reinterpret_cast<const void*>(&expand_token_kernel<T, 8>);
+  if constexpr (T::kVec == 4)
+    if (rank > 16 * T::kVec) return reinterpret_cast<const void*>(&expand_token_kernel<T, 32>);
+  return reinterpret_cast<const void*>(&expand_token_kernel<T, 16>);
+}
+
+// How a call is cut: token tiles and parts of the inner dimension's steps.
+struct Cut {
+  int m;       // 16-token tiles that a shrink workgroup takes together
+  int tiles;   // of 16 * m tokens
+  int slots;   // workgroups over which a tile's adapters are dealt
+  int parts;   // of the inner dimension
+  bool by_token;
+  int step0[kMaxRanks + 1];
 };
-Parts cut_parts(const int64_t* widths, int nranks, int64_t tokens, int dtype) {
-  Parts p;
-  int64_t inner = 0;
-  for (int r = 0; r < nranks; ++r) inner += widths[r];
-  // Workgroups for every compute unit twice over, no part below one step of
-  // the four waves, and few parts: expand reads each part's h again.
-  const int64_t tiles = std::max<int64_t>(1, (tokens + 15) / 16);
-  const int64_t least = kWaves * 8 * (16 / elem_size(dtype));
-  const int64_t want = std::max<int64_t>(1, 512 / tiles);
-  p.width = (int)std::max<int64_t>(least, ((inner + want - 1) / want + least - 1) / least * least);
-  for (int r = 0; r < nranks; ++r) p.first[r + 1] = p.first[r] + (int)((widths[r] + p.width - 1) / p.width);
-  return p;
+Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int rank) {
+  Cut c{};
+  const int step = dtype == RAR_BFLOAT16 ? step_width<BF16>() : step_width<F32>();
+  for (int r = 0; r < nranks; ++r) c.step0[r + 1] = c.step0[r] + (int)((widths[r] + step - 1) / step);
+  // Few tokens: each may have an adapter of its own.
+  c.by_token = tokens * rank <= 16384;
+  c.m = c.by_token ? 1 : 2;
+  c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));
+  c.slots = c.by_token ? 16 : 1;
+  const int want = std::max(1, 512 / c.tiles);
+  c.parts = std::min({want, kMaxParts, (c.step0[nranks] + kWaves - 1) / kWaves});
+  return c;
 }
 
 rar_result_t check_adapters(const int64_t* widths, int nranks, int64_t tokens, int dtype, int64_t adapters, int rank) {
@@ -351,8 +508,8 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
     if (rar_result_t q = check_pointer(scales, 4, "scales")) return q;
     reads.push_back(flat(scales, adapters * 4, "scales"));
   }
-  const Parts parts = cut_parts(widths, nranks, tokens, dtype);
-  const size_t need = (size_t)parts.first[nranks] * tokens * rank * 4;
+  const Cut cut = cut_call(widths, nranks, tokens, dtype, rank);
+  const size_t need = (size_t)cut.parts * tokens * rank * 4;
   if (workspace_bytes < need)
     return set_error(RAR_INVALID_ARGUMENT, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                                std::to_string(need) + " needed");
@@ -364,7 +521,7 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   if (rar_result_t q = check_blocks(reads, writes, false)) return q;
   if (rar_result_t q = check_blocks(partial_reads, writes, true)) return q;
   if (rar_result_t q = check_blocks(partial_reads, scratch, false)) return q;
-  for (int r = 0; r <= nranks; ++r) s.part0[r] = parts.first[r];
+  for (int r = 0; r <= nranks; ++r) s.step0[r] = cut.step0[r];
   s.ids = e.ids = ids;
   s.h = static_cast<float*>(workspace);
   e.h = s.h;
@@ -372,26 +529,32 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   s.nranks = e.nranks = nranks;
   s.adapters = e.adapters = (int32_t)adapters;
   s.rank = e.rank = rank;
-  s.part_width = parts.width;
+  s.parts = e.parts = cut.parts;
+  s.slots = cut.slots;
   e.up = up;
   e.scales = scales;
   e.ncopies = ncopies;
   e.outer = (int32_t)outer;
-  e.parts = parts.first[nranks];
-  const int64_t tiles = (tokens + 15) / 16;
   const bool bf = dtype == RAR_BFLOAT16;
-  if (e.parts) {
-    // Few tiles: a workgroup for every adapter a tile can hold.
-    s.slots = tiles <= 16 ? 16 : 1;
-    const void* fn = bf ? pick_shrink<BF16>(rank) : pick_shrink<F32>(rank);
-    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)tiles, (unsigned)e.parts, (unsigned)s.slots), dim3(kThreads), &s, stream))
+  if (cut.parts) {
+    const void* fn = cut.m == 1 ? (bf ? pick_shrink<BF16, 1>(rank) : pick_shrink<F32, 1>(rank))
+                                : (bf ? pick_shrink<BF16, 2>(rank) : pick_shrink<F32, 2>(rank));
+    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cut.tiles, (unsigned)cut.parts, (unsigned)cut.slots), dim3(kThreads), &s, stream))
       return q;
   }
-  const int64_t cols = (outer + 64 * kWaves - 1) / (64 * kWaves);
-  e.tiles_per_block = (int32_t)std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(8, tiles * cols / 2048));
-  const void* fn = bf ? pick_expand<BF16>(rank) : pick_expand<F32>(rank);
-  return launch_kernel(fn, dim3((unsigned)cols, (unsigned)((tiles + e.tiles_per_block - 1) / e.tiles_per_block)), dim3(kThreads), &e,
-                       stream);
+  if (cut.by_token)
+    return launch_kernel(bf ? pick_expand_token<BF16>(rank) : pick_expand_token<F32>(rank),
+                         dim3((unsigned)((outer + kCols - 1) / kCols), (unsigned)tokens), dim3(kThreads), &e, stream);
+  int tiles = 0;
+  const void* fn = bf ? pick_expand<BF16>(rank, &tiles) : pick_expand<F32>(rank, &tiles);
+  const int64_t runs = (tokens + 16 * tiles - 1) / (16 * tiles), cols = (outer + 64 * kWaves - 1) / (64 * kWaves);
+  // a grid's second dimension holds 65535 workgroups
+  for (int64_t run0 = 0; run0 < runs; run0 += 65535) {
+    e.run0 = run0;
+    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, runs - run0)), dim3(kThreads), &e, stream))
+      return q;
+  }
+  return RAR_SUCCESS;
 }
 
 }  // namespace
@@ -404,7 +567,7 @@ rar_result_t rar_adapter_workspace(const int64_t* widths, int nranks, int64_t to
   return rar::guarded([&]() -> rar_result_t {
     if (!bytes) return rar::set_error(RAR_INVALID_ARGUMENT, "bytes is NULL");
     if (rar_result_t r = rar::check_adapters(widths, nranks, tokens, dtype, 1, rank)) return r;
-    *bytes = (size_t)rar::cut_parts(widths, nranks, tokens, dtype).first[nranks] * tokens * rank * 4;
+    *bytes = (size_t)rar::cut_call(widths, nranks, tokens, dtype, rank).parts * tokens * rank * 4;
     return RAR_SUCCESS;
   });
 }

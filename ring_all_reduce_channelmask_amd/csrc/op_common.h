@@ -199,4 +199,43 @@ __device__ __forceinline__ void store_part(typename T::bits* p, int n, v4u v) {
   }
 }
 
+// Four neighbouring elements, `n` of them there, as fp32.
+template <class T>
+__device__ __forceinline__ void load4(const typename T::bits* p, int n, float* f) {
+  typedef uint32_t v2u_user __attribute__((ext_vector_type(2), aligned(2)));
+  if (n >= 4) {
+    if constexpr (T::kVec == 4) {
+      T::widen(load_16(p), f);
+    } else {
+      const v2u v = *reinterpret_cast<const v2u_user*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = T::widen1((uint16_t)(v[i / 2] >> (16 * (i & 1))));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = 0.0f;
+      if (i < n) f[i] = T::widen1(p[i]);
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ void store4(typename T::bits* p, int n, const float* f) {
+  typedef uint32_t v2u_user __attribute__((ext_vector_type(2), aligned(2)));
+  if (n >= 4) {
+    if constexpr (T::kVec == 4) {
+      *reinterpret_cast<v4u_user*>(p) = T::round(f);
+    } else {
+      v2u v;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = (uint32_t)T::round1(f[2 * i]) | (uint32_t)T::round1(f[2 * i + 1]) << 16;
+      *reinterpret_cast<v2u_user*>(p) = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = T::round1(f[i]);
+  }
+}
+
 }  // namespace rar
