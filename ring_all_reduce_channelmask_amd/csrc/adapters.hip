@@ -25,6 +25,7 @@ namespace {
 constexpr int kMaxRank = 128;  // of an adapter
 constexpr int kThreads = 256, kWaves = kThreads / kWaveSize;
 constexpr int kMaxParts = 16;
+constexpr int kExpandThreads = 256, kExpandWaves = kExpandThreads / kWaveSize;
 
 struct ShrinkArgs {
   const void* x[kMaxRanks];
@@ -48,7 +49,7 @@ struct ExpandArgs {
   const float* h;
   int64_t tokens;
   int64_t run0;                  // first run of the launch
-  int32_t nranks, ncopies, adapters, rank, outer, parts;
+  int32_t nranks, ncopies, adapters, rank, outer, parts, run_tiles;
 };
 
 // A step of the inner dimension: 2 vectors for each of the 4 lane groups.
@@ -77,16 +78,33 @@ __device__ __forceinline__ int load_id(const int64_t* ids, int64_t token, int64_
   return id >= 0 && id < adapters ? (int)id : -1;
 }
 
+// Between a wave's stores to LDS and its own loads: LDS keeps a wave's order,
+// so only the compiler has to.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // h of 16 * kM tokens and one part of the inner dimension, for the adapters
 // slot, slot + slots, ... of the tile.  The waves split the part's steps
 // between them and their sums meet in LDS.  kN tiles of 16 cover the
 // adapter's rank.
+//
+// Each wave stages a step's operands, 128 bytes of every row, in LDS: a load
+// there takes 8 whole lines, while in the MFMA's own layout, where
+// neighbouring lanes are different rows, it takes 45 accesses to the cache
+// (4096 tokens of 7168, rank 64: 45 us, staged @@ us).
 template <class T, int kN, int kM>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
   const ShrinkArgs& args = kernel_args<ShrinkArgs>();
-  __shared__ v4f sums[kWaves][kM][kN][kWaveSize];
   constexpr int kStep = step_width<T>();
+  constexpr int kLoads = 2 * (kM + kN);  // of 8 rows each
   typedef typename T::bits bits;
+  union Lds {
+    v4u rows[kWaves][16 * (kM + kN)][9];  // 128 bytes and 16 against bank conflicts
+    v4f sums[kWaves][kM][kN][kWaveSize];
+  };
+  __shared__ Lds lds;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
   const int64_t token0 = (int64_t)blockIdx.x * 16 * kM;
   const int part = blockIdx.y, steps = args.step0[args.nranks];
@@ -104,56 +122,67 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int n = 0; n < kN; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int step = begin + wave; step < end; step += kWaves) {
+    // One step's operands: rows 0 .. 16 kM - 1 are tokens (those of other
+    // adapters zero), the rest rows of the adapter's weights (those past its
+    // rank repeat the last one and are not written).
+    v4u next[kLoads];
+    auto load = [&](int step) {
       int r = 0;
       while (r + 1 < args.nranks && args.step0[r + 1] <= step) ++r;
       const int width = args.width[r];
-      const int col0 = (step - args.step0[r]) * kStep;
-      const bits* x = static_cast<const bits*>(args.x[r]);
-      const bits* w = static_cast<const bits*>(args.down[r]) + (int64_t)a * args.rank * width;
-      // Two vectors a lane, side by side: the inner dimension's order within
-      // a step is free as long as both operands take the same.  Rows past the
-      // adapter's rank repeat its last one and are not written.
-      v4u xa[kM][2], wb[kN][2];
-      const int col = col0 + group * 2 * T::kVec;
+      const int col0 = (step - args.step0[r]) * kStep, col = col0 + lane % 8 * T::kVec;
       const bool full = col0 + kStep <= width;
+      const bits* x = static_cast<const bits*>(args.x[r]) + token0 * args.x_stride[r] + col;
+      const bits* w = static_cast<const bits*>(args.down[r]) + (int64_t)a * args.rank * width + col;
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        const int row = n * 16 + at < args.rank ? n * 16 + at : args.rank - 1;
-        const bits* p = w + (int64_t)row * width + col;
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-          wb[n][v] = full ? load_16(p + v * T::kVec) : load_part<T>(p + v * T::kVec, width - col - v * T::kVec, 0);
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = i * 8 + lane / 8;
+        const bits* p;
+        bool there = true;
+        if (i < 2 * kM) {
+          p = x + row * args.x_stride[r];
+          there = members >> row & 1;
+        } else {
+          const int n = row - 16 * kM;
+          p = w + (int64_t)(n < args.rank ? n : args.rank - 1) * width;
+        }
+        next[i] = v4u{0, 0, 0, 0};
+        if (there) next[i] = full ? load_16(p) : load_part<T>(p, width - col, 0);
       }
+    };
+    __syncthreads();  // the previous adapter's sums have been read
+    if (begin + wave < end) load(begin + wave);
+    for (int step = begin + wave; step < end; step += kWaves) {
 #pragma unroll
-      for (int m = 0; m < kM; ++m) {
-        const bool mine = members >> (m * 16 + at) & 1;
-        const bits* p = x + (token0 + m * 16 + at) * args.x_stride[r] + col;
+      for (int i = 0; i < kLoads; ++i) lds.rows[wave][i * 8 + lane / 8][lane % 8] = next[i];
+      wave_lds_fence();
+      if (step + kWaves < end) load(step + kWaves);  // in flight during the products
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          xa[m][v] = v4u{0, 0, 0, 0};
-          if (mine) xa[m][v] = full ? load_16(p + v * T::kVec) : load_part<T>(p + v * T::kVec, width - col - v * T::kVec, 0);
+      for (int v = 0; v < 2; ++v) {
+        v4u x[kM];
+#pragma unroll
+        for (int m = 0; m < kM; ++m) x[m] = lds.rows[wave][m * 16 + at][v * 4 + group];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const v4u w = lds.rows[wave][(kM + n) * 16 + at][v * 4 + group];
+#pragma unroll
+          for (int m = 0; m < kM; ++m) acc[m][n] = mma<T>(x[m], w, acc[m][n]);
         }
       }
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int n = 0; n < kN; ++n) acc[m][n] = mma<T>(xa[m][v], wb[n][v], acc[m][n]);
+      wave_lds_fence();
     }
-    __syncthreads();  // the previous adapter's sums have been read
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < kM; ++m)
 #pragma unroll
-      for (int n = 0; n < kN; ++n) sums[wave][m][n][lane] = acc[m][n];
+      for (int n = 0; n < kN; ++n) lds.sums[wave][m][n][lane] = acc[m][n];
     __syncthreads();
     // lane: column (place in the adapter's rank) `at`, rows (tokens) 4 * group + i
     for (int q = wave; q < kM * kN; q += kWaves) {
       const int m = q / kN, n = q % kN;
-      v4f s = sums[0][m][n][lane];
+      v4f s = lds.sums[0][m][n][lane];
 #pragma unroll
-      for (int o = 1; o < kWaves; ++o) s += sums[o][m][n][lane];
+      for (int o = 1; o < kWaves; ++o) s += lds.sums[o][m][n][lane];
       const int col = n * 16 + at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -179,25 +208,28 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
   return s;
 }
 
-// y of a run of kTiles * 16 tokens x 64 columns a wave.  The columns are the
-// MFMA's rows, dealt so that a lane's results over the four tiles are whole
-// 16-byte vectors of one token and the four lane groups' vectors are
-// neighbours: a store of half lines costs more than one of whole ones.  The run's h is laid out in LDS first, for bf16 as two bf16 numbers
-// whose sum has 16 bits of it.
+// y of a run of at most kTiles * 16 tokens x 64 columns a wave, a tile of 16
+// tokens at a time.  The run's h is laid out in LDS first, for bf16 as two bf16
+// numbers whose sum has 16 bits of it.  In the products the columns are the
+// MFMA's rows and the tokens its columns; the result passes through LDS so
+// that the partials and y move in whole 128-byte lines (a lane's own results
+// would make 64-byte pieces of them: 4096 x 7168, 4 ranks, 150 us against
+// @@ without any adapter).
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
-__global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
   constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts
   constexpr int kForms = T::kVec == 8 ? 2 : 1;
-  constexpr int kPer = T::kVec / 4;     // tiles that make up a vector
+  constexpr int kRowLanes = 64 / T::kVec;  // lanes that move a token's 64 columns, kVec tokens at a time
   typedef typename T::bits bits;
   __shared__ v4u hs[kForms][kTiles * 16][kRowVecs];
+  __shared__ v4f turn[kExpandWaves][16][17];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
-  const int64_t run0 = (args.run0 + blockIdx.y) * kTiles * 16;
+  const int64_t run0 = (args.run0 + blockIdx.y) * args.run_tiles * 16;
   constexpr int kQuads = kR * kStep / 4;  // of a token's h
 #pragma unroll 4
-  for (int i = threadIdx.x; i < kTiles * 16 * kQuads; i += kThreads) {
+  for (int i = threadIdx.x; i < args.run_tiles * 16 * kQuads; i += kExpandThreads) {
     const int t = i / kQuads, q = i % kQuads * 4;
     const int64_t token = run0 + t;
     const int id = load_id(args.ids, token, args.tokens, args.adapters);
@@ -225,37 +257,40 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
     if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
   }
   __syncthreads();
-  const int col0 = ((int)blockIdx.x * kWaves + wave) * 64;
-  const int col = col0 + group * T::kVec;  // of vector v: + v * kStep
+  const int col0 = ((int)blockIdx.x * kExpandWaves + wave) * 64;
   if (col0 >= args.outer) return;
   const bool full = col0 + 64 <= args.outer;
+  const int col = col0 + lane % kRowLanes * T::kVec;  // of this lane's vectors
   int held = -1;  // the adapter whose weights are in registers
   v4u w[4][kR];
-  for (int tile = 0; tile < kTiles; ++tile) {
+  for (int tile = 0; tile < args.run_tiles; ++tile) {
     const int64_t token0 = run0 + tile * 16;
     if (token0 >= args.tokens) return;
-    const int64_t token = token0 + at;
-    const bool live = token < args.tokens;
-    const int id = load_id(args.ids, token, args.tokens, args.adapters);
-    float y[16];
+    const int64_t row0 = token0 + lane / kRowLanes;  // token of vector v: + v * kVec
+    const bool whole = full && token0 + 16 <= args.tokens;
     v4u p[kBatch][kVecs];
     auto load_partials = [&](int r0) {
 #pragma unroll
       for (int r = 0; r < kBatch; ++r) {
         if (r0 + r < args.nranks) {
-          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) +
-                            (live ? token : token0) * args.partial_stride[r0 + r] + col;
+          const int64_t stride = args.partial_stride[r0 + r];
+          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + row0 * stride + col;
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v)
-            p[r][v] = full ? load_nt(src + v * kStep) : load_part<T>(src + v * kStep, args.outer - col - v * kStep, 0);
+          for (int v = 0; v < kVecs; ++v) {
+            if (whole) p[r][v] = load_nt(src + v * T::kVec * stride);
+            else p[r][v] = load_part<T>(src + v * T::kVec * stride, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, 0);
+          }
         }
       }
     };
     load_partials(0);  // in flight during the products
-    v4f sum[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const int id = load_id(args.ids, token0 + at, args.tokens, args.adapters);
     uint64_t left = __ballot(id >= 0) & 0xFFFF;
+    const bool any = left != 0;
+    if (any && id < 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) turn[wave][at][j * 4 + group] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     while (left) {
       const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
       const bool mine = id == a;
@@ -263,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
       if (a != held) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int d = col0 + j / kPer * kStep + (at >> 2) * T::kVec + j % kPer * 4 + (at & 3);
+          const int d = col0 + j * 16 + at;
           const bits* row = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + d) * args.rank;
 #pragma unroll
           for (int c = 0; c < kR; ++c) {
@@ -284,9 +319,14 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = mma<T>(w[j][c], h, acc[j]);
         }
+      // from (token `at`, columns j * 16 + 4 * group ..) to the lanes' vectors;
+      // the wave's own part of LDS, and LDS keeps a wave's order
+      if (mine) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] = mine ? acc[j] : sum[j];
+        for (int j = 0; j < 4; ++j) turn[wave][at][j * 4 + group] = acc[j];
+      }
     }
+    float y[16];
     for (int r0 = 0; r0 < args.nranks; r0 += kBatch) {
       if (r0) load_partials(r0);
 #pragma unroll
@@ -300,17 +340,26 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
         }
       }
     }
+    if (any) {
+      wave_lds_fence();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] += sum[i / 4][i % 4];
-    if (live) {
-      for (int k = 0; k < args.ncopies; ++k) {
-        bits* dst = static_cast<bits*>(args.out[k]) + token * args.out_stride[k] + col;
+      for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-          const v4u o = T::round(y + v * T::kVec);
-          if (full) store_nt(dst + v * kStep, o);
-          else store_part<T>(dst + v * kStep, args.outer - col - v * kStep, o);
+        for (int q = 0; q < T::kVec / 4; ++q) {
+          const v4f d = turn[wave][lane / kRowLanes + v * T::kVec][lane % kRowLanes * (T::kVec / 4) + q];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[v * T::kVec + q * 4 + i] += d[i];
         }
+      wave_lds_fence();
+    }
+    for (int k = 0; k < args.ncopies; ++k) {
+      const int64_t stride = args.out_stride[k];
+      bits* dst = static_cast<bits*>(args.out[k]) + row0 * stride + col;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const v4u o = T::round(y + v * T::kVec);
+        if (whole) store_nt(dst + v * T::kVec * stride, o);
+        else store_part<T>(dst + v * T::kVec * stride, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, o);
       }
     }
   }
@@ -395,7 +444,7 @@ const void* pick_shrink(int rank) {
   return reinterpret_cast<const void*>(&shrink_kernel<T, 8, kM>);
 }
 // Token tiles of a run: its h takes at most 36 KB of LDS.
-constexpr int kRunTiles = 8;
+constexpr int kRunTiles = 4;
 template <class T>
 const void* pick_expand(int rank, int* tiles) {
   *tiles = kRunTiles;
@@ -547,11 +596,16 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
                          dim3((unsigned)((outer + kCols - 1) / kCols), (unsigned)tokens), dim3(kThreads), &e, stream);
   int tiles = 0;
   const void* fn = bf ? pick_expand<BF16>(rank, &tiles) : pick_expand<F32>(rank, &tiles);
-  const int64_t runs = (tokens + 16 * tiles - 1) / (16 * tiles), cols = (outer + 64 * kWaves - 1) / (64 * kWaves);
+  // The longer a run, the fewer times weights are loaded, but 4 workgroups for
+  // each compute unit come first.
+  const int64_t cols = (outer + 64 * kExpandWaves - 1) / (64 * kExpandWaves);
+  while (tiles > 1 && cols * ((tokens + 16 * tiles - 1) / (16 * tiles)) < 1024) tiles /= 2;
+  const int64_t runs = (tokens + 16 * tiles - 1) / (16 * tiles);
+  e.run_tiles = tiles;
   // a grid's second dimension holds 65535 workgroups
   for (int64_t run0 = 0; run0 < runs; run0 += 65535) {
     e.run0 = run0;
-    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, runs - run0)), dim3(kThreads), &e, stream))
+    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, runs - run0)), dim3(kExpandThreads), &e, stream))
       return q;
   }
   return RAR_SUCCESS;
