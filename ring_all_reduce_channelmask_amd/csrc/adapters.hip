@@ -78,13 +78,6 @@ __device__ __forceinline__ int load_id(const int64_t* ids, int64_t token, int64_
   return id >= 0 && id < adapters ? (int)id : -1;
 }
 
-// Between a wave's stores to LDS and its own loads: LDS keeps a wave's order,
-// so only the compiler has to.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // h of 16 * kM tokens and one part of the inner dimension, for the adapters
 // slot, slot + slots, ... of the tile.  The waves split the part's steps
 // between them and their sums meet in LDS.  kN tiles of 16 cover the

@@ -14,10 +14,10 @@
 // join the same way.  Then lse = ln 2 (M + log2 s) and entropy = ln 2
 // (log2 s - u / s).  All of it is fp32.
 //
-// The logits are cut into tiles that do not cross ranks; a workgroup takes a
-// run of consecutive tiles of one row.  Where there are few rows a row is
-// split over several workgroups, which leave (M, s, u) and their best tokens
-// in the workspace for a second kernel to join.
+// The logits are cut into tiles that do not cross ranks, one for a wave at a
+// time; a workgroup takes a run of consecutive tiles of one row.  Where there
+// are few rows a row is split over several workgroups, which leave (M, s, u)
+// and their best tokens in the workspace for a second kernel to join.
 #include "op_common.h"
 
 #include <cmath>
@@ -26,6 +26,7 @@ namespace rar {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWaveSize;
+constexpr int kMaxWgWaves = 16;
 constexpr int kVecsPerTile = 4;  // 16-byte vectors of a tile per thread
 constexpr int kMaxTop = 32;
 constexpr int kCandidates = 1024;  // best-token candidates a workgroup holds
@@ -55,8 +56,11 @@ struct LogprobsArgs {
   uint64_t* keys;                  // [rows][splits][ntop]
 };
 
+// Forward: a wave's tile; gradient: a workgroup's.
 template <class T>
-constexpr int tile_elems() { return kThreads * kVecsPerTile * T::kVec; }
+constexpr int wave_tile() { return kWaveSize * kVecsPerTile * T::kVec; }
+template <class T>
+constexpr int block_tile() { return kThreads * kVecsPerTile * T::kVec; }
 
 // The rank that holds tile t (or id v, from `first`).  Uniform: scalar code.
 __device__ __forceinline__ int rank_of(const int32_t* starts, int nranks, int at) {
@@ -100,38 +104,60 @@ __device__ __forceinline__ void shift_to(Stat& a, float m) {
   a.s = f > 0.0f || a.s != a.s ? f * a.s : 0.0f;
   a.m = m;
 }
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  shift_to(a, m);
-  shift_to(b, m);
-  return Stat{m, a.s + b.s, a.u + b.u};
+
+// Reductions over a wave with lane shifts inside the vector unit (shifts by 1,
+// 2, 4, 8 within a row of 16 lanes, then row 15 -> next row, rows 0-1 -> rows
+// 2-3): lane 63 ends with the whole, which every lane gets.  `none` is what
+// lanes without a source take.
+template <class Op>
+__device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
+#define RAR_STEP(ctrl, rows)                                                                                  \
+  v = op(v, __uint_as_float(__builtin_amdgcn_update_dpp((int)__float_as_uint(none), (int)__float_as_uint(v), ctrl, rows, 0xF, false)))
+  RAR_STEP(0x111, 0xF);
+  RAR_STEP(0x112, 0xF);
+  RAR_STEP(0x114, 0xF);
+  RAR_STEP(0x118, 0xF);
+  RAR_STEP(0x142, 0xA);
+  RAR_STEP(0x143, 0xC);
+#undef RAR_STEP
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return wave_reduce(v, 0.0f, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ Stat wave_join(Stat a) {
-#pragma unroll
-  for (int d = 1; d < kWaveSize; d <<= 1) {
-    Stat b{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.u, d)};
-    a = join(a, b);
-  }
-  return a;
+  shift_to(a, wave_max(a.m));
+  return Stat{a.m, wave_sum(a.s), wave_sum(a.u)};
+}
+// The join of `n` <= 64 triples in LDS, in every wave.
+__device__ __forceinline__ Stat join_all(const Stat* stats, int n) {
+  const int lane = threadIdx.x & 63;
+  return wave_join(lane < n ? stats[lane] : Stat{-INFINITY, 0.0f, 0.0f});
 }
 
 // Candidates for the most probable tokens, in LDS.
 struct Top {
   uint64_t key[kCandidates];
   uint64_t best[kMaxTop];
-  uint32_t count[3];  // appended in tile t: count[t % 3]
-  float wave_cut[kWaves];
-  uint64_t wave_best[kWaves];
+  uint32_t count[3];  // appended in round t: count[t % 3]
+  float group_most[kWaveSize];
+  uint64_t wave_best[kMaxWgWaves];
 };
 
-// Keep the `k` largest of the n <= kCandidates keys (all different), sorted,
-// in `best`, unused places zero.  Every thread of the workgroup calls it.
+// Keep the `k` largest of the n <= kCandidates keys (all different but for
+// zeros), sorted, in `best`, unused places zero.  Every thread of the
+// workgroup calls it.
 __device__ __forceinline__ void select_top(Top& top, int n, int k) {
-  for (int i = threadIdx.x; i < k; i += kThreads) top.best[i] = 0;
+  const int threads = blockDim.x;
+  if ((int)threadIdx.x < k) top.best[threadIdx.x] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += threads) {
     const uint64_t mine = top.key[i];
     int above_me = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) above_me += top.key[j] > mine;
     if (above_me < k) top.best[above_me] = mine;
   }
@@ -147,21 +173,17 @@ __device__ __forceinline__ uint64_t wave_max_key(uint64_t a) {
   return a;
 }
 
-// The k-th largest of the wave's 64 values (NaN counts as -inf): bitonic sort
-// across lanes, descending.
+// A bound that at least k of the wave's 64 values reach, to the upper 16 bits
+// of the k-th largest: bit by bit from the top.  NaN where there is none.
 __device__ __forceinline__ float wave_kth(float v, int k) {
-  const int lane = threadIdx.x & 63;
-  v = fmaxf(v, -INFINITY);
+  const uint32_t mine = v == v ? (uint32_t)(key_of(v, 0) >> 48) : 0u;
+  uint32_t bound = 0;
 #pragma unroll
-  for (int size = 2; size <= 64; size <<= 1) {
-#pragma unroll
-    for (int d = size / 2; d > 0; d >>= 1) {
-      const float o = __shfl_xor(v, d);
-      const bool larger = ((lane & size) == 0) == ((lane & d) == 0);
-      v = larger ? fmaxf(v, o) : fminf(v, o);
-    }
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t t = bound | 1u << bit;
+    if (__popcll(__ballot(mine >= t)) >= k) bound = t;
   }
-  return __shfl(v, k - 1);
+  return key_logit((uint64_t)bound << 48);
 }
 
 // A row whose largest logit is so far out that d_j = fma(x_j, scale2, -M) says
@@ -173,46 +195,34 @@ __device__ __forceinline__ float wave_kth(float v, int k) {
 constexpr float kFar = 268435456.0f;  // 2^28
 template <class T>
 __device__ __forceinline__ Stat rescan(const Shards& x, int64_t row, float scale, Stat seen, Stat* wave_stat) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, threads = blockDim.x, waves = threads / kWaveSize;
   float m = -INFINITY;
   for (int r = 0; r < x.nranks; ++r) {
     const typename T::bits* src = static_cast<const typename T::bits*>(x.ptr[r]) + row * x.stride[r];
-    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += kThreads) m = fmaxf(m, T::widen1(src[c]) * scale);
+    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += threads) m = fmaxf(m, T::widen1(src[c]) * scale);
   }
-#pragma unroll
-  for (int d = 1; d < kWaveSize; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  m = wave_max(m);
   __syncthreads();
   if (lane == 0) wave_stat[wave].m = m;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, wave_stat[w].m);
+  m = wave_max(lane < waves ? wave_stat[lane].m : -INFINITY);
   if (m == -INFINITY) return Stat{m, seen.s, 0.0f};
   float s = 0.0f, u = 0.0f;
   for (int r = 0; r < x.nranks; ++r) {
     const typename T::bits* src = static_cast<const typename T::bits*>(x.ptr[r]) + row * x.stride[r];
-    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += kThreads) {
+    for (int c = threadIdx.x; c < x.first[r + 1] - x.first[r]; c += threads) {
       const float d = T::widen1(src[c]) * scale - m;
       const float e = exp2_(d * kLog2e);
       s += e;
       u = __builtin_fmaf(e, fmaxf(d, -200.0f), u);
     }
   }
-#pragma unroll
-  for (int d = 1; d < kWaveSize; d <<= 1) {
-    s += __shfl_xor(s, d);
-    u += __shfl_xor(u, d);
-  }
+  s = wave_sum(s);
+  u = wave_sum(u);
   __syncthreads();
   if (lane == 0) wave_stat[wave] = Stat{m, s, u};
   __syncthreads();
-  s = wave_stat[0].s;
-  u = wave_stat[0].u;
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) {
-    s += wave_stat[w].s;
-    u += wave_stat[w].u;
-  }
-  return Stat{m, s, u};
+  return Stat{m, wave_sum(lane < waves ? wave_stat[lane].s : 0.0f), wave_sum(lane < waves ? wave_stat[lane].u : 0.0f)};
 }
 
 // Results of a row from its joined triple and sorted best keys.  Every thread
@@ -251,90 +261,153 @@ __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, St
   }
 }
 
-template <class T, bool kTop>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobsArgs) {
+// Each lane's maximum over its group of n = 4, 8 or 16 lanes.
+template <int n>
+__device__ __forceinline__ float group_max(float v) {
+#define RAR_STEP(ctrl) \
+  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xF, 0xF, true)))
+  RAR_STEP(0xB1);                      // lane ^ 1
+  RAR_STEP(0x4E);                      // lane ^ 2
+  if constexpr (n > 4) RAR_STEP(0x141);  // mirrored within 8
+  if constexpr (n > 8) RAR_STEP(0x140);  // mirrored within 16
+#undef RAR_STEP
+  return v;
+}
+
+template <class T, bool kTop, int kWgWaves>
+__global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(LogprobsArgs) {
   const LogprobsArgs& args = kernel_args<LogprobsArgs>();
   constexpr int kElems = kVecsPerTile * T::kVec;  // a thread's of one tile
-  constexpr int kTile = tile_elems<T>();
-  __shared__ Stat wave_stat[kWaves];
+  constexpr int kTile = wave_tile<T>();
+  __shared__ Stat wave_stat[kWgWaves];
   __shared__ std::conditional_t<kTop, Top, int> top_lds;
-  const int64_t row = blockIdx.x / args.splits;
-  const int split = (int)(blockIdx.x - row * args.splits);
+  const int64_t row = blockIdx.x / (uint32_t)args.splits;
+  const int split = (int)(blockIdx.x % (uint32_t)args.splits);
   const int tiles = args.x.tile0[args.x.nranks];
   const int t0 = (int)((int64_t)tiles * split / args.splits), t1 = (int)((int64_t)tiles * (split + 1) / args.splits);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Stat st{-INFINITY, 0.0f, 0.0f};
+  bool masked = false;  // -inf has been met
   float cut = kLowest;  // a candidate's least logit
   int held = 0;         // candidates in LDS
+  bool sorted = false;  // the best of them are in top.best
   if constexpr (kTop) {
-    if (threadIdx.x == 0) top_lds.count[0] = top_lds.count[1] = top_lds.count[2] = 0;
+    if (threadIdx.x < 3) top_lds.count[threadIdx.x] = 0;
     __syncthreads();
   }
-  for (int t = t0; t < t1; ++t) {
-    const int r = rank_of(args.x.tile0, args.x.nranks, t);
-    const int col0 = (t - args.x.tile0[r]) * kTile;
-    const int width = args.x.first[r + 1] - args.x.first[r];
+  // element i of this thread: column col0 + column(i)
+  auto column = [&](int i) { return (i / T::kVec * kWaveSize + lane) * T::kVec + i % T::kVec; };
+  int round = 0;
+  for (int base = t0; base < t1; base += kWgWaves, ++round) {
+    const int t = base + wave;
+    const bool live = t < t1;
+    const int r = rank_of(args.x.tile0, args.x.nranks, live ? t : t0);
+    const int col0 = (t - args.x.tile0[r]) * kTile, width = args.x.first[r + 1] - args.x.first[r];
     const typename T::bits* src = static_cast<const typename T::bits*>(args.x.ptr[r]) + row * args.x.stride[r];
     v4u raw[kVecsPerTile];
+    float most = -INFINITY, vec_most[kVecsPerTile];
+    if (live) {
+      const bool full = col0 + kTile <= width;
 #pragma unroll
-    for (int v = 0; v < kVecsPerTile; ++v) {
-      const int c = col0 + (v * kThreads + (int)threadIdx.x) * T::kVec;
-      raw[v] = load_part<T>(src + c, width - c, T::kNegInf);
-    }
-    float x[kElems];
+      for (int v = 0; v < kVecsPerTile; ++v) {
+        const int c = col0 + column(v * T::kVec);
+        raw[v] = full ? load_nt(src + c) : load_part<T>(src + c, width - c, T::kNegInf);
+      }
+      float x[kElems];
 #pragma unroll
-    for (int v = 0; v < kVecsPerTile; ++v) T::widen(raw[v], x + v * T::kVec);
-    float most = x[0];
+      for (int v = 0; v < kVecsPerTile; ++v) T::widen(raw[v], x + v * T::kVec);
 #pragma unroll
-    for (int i = 1; i < kElems; ++i) most = fmaxf(most, x[i]);
-    const float m = fmaxf(st.m, most * args.scale2);
-    shift_to(st, m);
-    const float base = m == -INFINITY ? 0.0f : m;
+      for (int v = 0; v < kVecsPerTile; ++v) {
+        vec_most[v] = x[v * T::kVec];
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) {
-      const float d = __builtin_fmaf(x[i], args.scale2, -base);
-      const float e = exp2_(d);
-      st.s += e;
-      st.u = __builtin_fmaf(e, fmaxf(d, -200.0f), st.u);  // a masked token adds 0, not 0 * -inf
+        for (int i = 1; i < T::kVec; ++i) vec_most[v] = fmaxf(vec_most[v], x[v * T::kVec + i]);
+        most = fmaxf(most, vec_most[v]);
+      }
+      shift_to(st, fmaxf(st.m, most * args.scale2));
+      const float from = st.m == -INFINITY ? 0.0f : st.m;
+      // A masked token adds e * d = 0 * -inf to u: from the first one on, d is
+      // bounded for u, which costs one operation of seven for each logit.
+      masked = masked || !full;
+      if (!masked) {
+        float s = st.s, u = st.u;
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+          const float d = __builtin_fmaf(x[i], args.scale2, -from);
+          const float e = exp2_(d);
+          s += e;
+          u = __builtin_fmaf(e, d, u);
+        }
+        masked = __any(u != u);
+        if (!masked) st = Stat{st.m, s, u};
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+          const float d = __builtin_fmaf(x[i], args.scale2, -from);
+          const float e = exp2_(d);
+          st.s += e;
+          st.u = __builtin_fmaf(e, fmaxf(d, -200.0f), st.u);
+        }
+      }
     }
     if constexpr (kTop) {
       Top& top = top_lds;
-      const int id0 = args.x.first[r] + col0 + (int)threadIdx.x * T::kVec;
-      if (t == t0) {
-        // the k-th largest of a wave's maxima: k tokens at least reach it
-        const float kth = wave_kth(most, args.ntop);
-        if (lane == 0) top.wave_cut[wave] = kth;
+      if (round == 0) {
+        // The k-th largest of 64 groups' maxima over the workgroup: k tokens at
+        // least reach it, and seldom many more.
+        const float group = group_max<kWgWaves>(most);
+        if (lane % kWgWaves == 0) top.group_most[wave * (kWaveSize / kWgWaves) + lane / kWgWaves] = group;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) cut = fmaxf(cut, top.wave_cut[w]);
+        cut = fmaxf(cut, wave_kth(top.group_most[lane], args.ntop));
       }
-      uint32_t* count = &top.count[t % 3];
-      if (__any(most >= cut)) {
+      uint32_t* count = &top.count[round % 3];
+      if (live && __any(most >= cut)) {
+        // one reservation for the wave; few of its elements are candidates
+        int mine = 0;
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) {
-          if (x[i] >= cut) {
-            const uint32_t at = held + atomicAdd(count, 1u);
-            if (at < (uint32_t)kCandidates)
-              top.key[at] = key_of(x[i], id0 + (i / T::kVec) * kThreads * T::kVec + i % T::kVec);
+        for (int v = 0; v < kVecsPerTile; ++v) {
+          if (!__any(vec_most[v] >= cut)) continue;
+          float x[T::kVec];
+          T::widen(raw[v], x);
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) mine += __popcll(__ballot(x[i] >= cut));
+        }
+        int at = 0;
+        if (lane == 0) at = (int)atomicAdd(count, (uint32_t)mine);
+        at = held + __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int v = 0; v < kVecsPerTile; ++v) {
+          if (!__any(vec_most[v] >= cut)) continue;
+          float x[T::kVec];
+          T::widen(raw[v], x);
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) {
+            const uint64_t takers = __ballot(x[i] >= cut);
+            if (takers) {
+              const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(takers >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)takers, 0));
+              if (x[i] >= cut && to < kCandidates) top.key[to] = key_of(x[i], args.x.first[r] + col0 + column(v * T::kVec + i));
+              at += __popcll(takers);
+            }
           }
         }
       }
-      // the next tile's counter: last read two tiles ago, before the last barrier
-      if (threadIdx.x == 0) top.count[(t + 1) % 3] = 0;
+      // the next round's counter: last read two rounds ago, before the last barrier
+      if (threadIdx.x == 0) top.count[(round + 1) % 3] = 0;
       __syncthreads();
       int n = held + (int)*count;
       const bool over = n > kCandidates;
+      sorted = sorted && n == held;
       if (over) {
         // More equal logits than the list holds: the best of what it held
-        // before this tile, and the tile's best one by one.
+        // before this round, and the round's best one by one.
         select_top(top, held, args.ntop);
         if ((int)threadIdx.x < args.ntop) top.key[threadIdx.x] = top.best[threadIdx.x];
         uint64_t last = ~0ull;
         for (int k = 0; k < args.ntop; ++k) {
           uint64_t mine = 0;
 #pragma unroll 1
-          for (int i = 0; i < kElems; ++i) {
-            const int c = col0 + ((i / T::kVec) * kThreads + (int)threadIdx.x) * T::kVec + i % T::kVec;
+          for (int i = 0; i < kElems && live; ++i) {
+            const int c = col0 + column(i);
             if (c >= width) continue;
             const float f = T::widen1(src[c]);
             const uint64_t key = key_of(f, args.x.first[r] + c);
@@ -343,22 +416,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobsArgs) {
           mine = wave_max_key(mine);
           if (lane == 0) top.wave_best[wave] = mine;
           __syncthreads();
-          last = 0;
-#pragma unroll
-          for (int w = 0; w < kWaves; ++w) last = top.wave_best[w] > last ? top.wave_best[w] : last;
+          last = wave_max_key(lane < kWgWaves ? top.wave_best[lane] : 0);
           if (threadIdx.x == 0) top.key[args.ntop + k] = last;
           __syncthreads();
         }
         n = 2 * args.ntop;  // unused places are zero: below every candidate
       }
-      if (over || n > kCandidates / 2 || (t == t0 && n > args.ntop)) {
+      if (over || n > kCandidates / 2 || (round == 0 && n > args.ntop)) {
         select_top(top, n, args.ntop);
         const uint64_t kth = top.best[args.ntop - 1];
         n = args.ntop;
+        // a later round's ids are higher: an equal logit no longer counts
         if (kth) cut = above(kth);
         else
           for (n = 0; top.best[n];) ++n;
         if ((int)threadIdx.x < n) top.key[threadIdx.x] = top.best[threadIdx.x];
+        sorted = true;
         __syncthreads();
       }
       held = n;
@@ -366,13 +439,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobsArgs) {
   }
   st = wave_join(st);
   if (lane == 0) wave_stat[wave] = st;
-  if constexpr (kTop) select_top(top_lds, held, args.ntop);
-  else __syncthreads();
-  st = wave_stat[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) st = join(st, wave_stat[w]);
+  __syncthreads();
+  st = join_all(wave_stat, kWgWaves);
   const uint64_t* best = nullptr;
-  if constexpr (kTop) best = top_lds.best;
+  if constexpr (kTop) {
+    if (!sorted) select_top(top_lds, held, args.ntop);
+    best = top_lds.best;
+  }
   if (args.splits == 1) {
     write_row<T>(args, row, st, best, wave_stat);
     return;
@@ -407,8 +480,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobsArgs) {
     if (lane == 0) top.wave_best[wave] = least;
     if (threadIdx.x == 0) top.count[0] = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) least = top.wave_best[w] > least ? top.wave_best[w] : least;
+    least = wave_max_key(lane < kWaves ? top.wave_best[lane] : 0);
     for (int i = threadIdx.x; i < args.splits * args.ntop; i += kThreads) {
       const uint64_t key = keys[i];
       if (key && key >= least) top.key[atomicAdd(&top.count[0], 1u)] = key;
@@ -418,10 +490,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobsArgs) {
   } else {
     __syncthreads();
   }
-  st = wave_stat[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) st = join(st, wave_stat[w]);
-  write_row<T>(args, row, st, top.best, wave_stat);
+  write_row<T>(args, row, join_all(wave_stat, kWaves), top.best, wave_stat);
 }
 
 struct LogprobsBackwardArgs {
@@ -440,7 +509,7 @@ struct LogprobsBackwardArgs {
 template <class T, bool kEntropy>
 __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(LogprobsBackwardArgs) {
   const LogprobsBackwardArgs& args = kernel_args<LogprobsBackwardArgs>();
-  constexpr int kTile = tile_elems<T>();
+  constexpr int kTile = block_tile<T>();
   const uint32_t tiles = (uint32_t)args.x.tile0[args.x.nranks];
   const int64_t row = args.row0 + blockIdx.x / tiles;
   const int t = (int)(blockIdx.x % tiles);
@@ -491,12 +560,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(LogprobsBac
 // ---- host -------------------------------------------------------------------
 
 rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* widths, const int64_t* strides,
-                         int nranks, int64_t rows, int dtype) {
+                         int nranks, int64_t rows, int dtype, bool backward) {
   if (nranks < 1 || nranks > kMaxRanks) return set_error(RAR_INVALID_ARGUMENT, "nranks must be in [1, 64]");
   if (rar_result_t r = check_float_dtype(dtype)) return r;
   if (rows < 0 || rows > kMaxRows) return set_error(RAR_INVALID_ARGUMENT, "rows must be in [0, 2^23]");
   if (!widths) return set_error(RAR_INVALID_ARGUMENT, "widths is NULL");
-  const int tile = dtype == RAR_BFLOAT16 ? tile_elems<BF16>() : tile_elems<F32>();
+  const int tile = dtype == RAR_BFLOAT16 ? (backward ? block_tile<BF16>() : wave_tile<BF16>())
+                                         : (backward ? block_tile<F32>() : wave_tile<F32>());
   int64_t vocab = 0, tiles = 0;
   for (int r = 0; r < nranks; ++r) {
     if (widths[r] < 0 || widths[r] > (int64_t(1) << 30))
@@ -524,16 +594,37 @@ rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* wi
   return RAR_SUCCESS;
 }
 
-// Workgroups a row is split over: enough for about 4 per compute unit.
-int choose_splits(const Shards& s, int64_t rows, int ntop) {
+// How a row is cut: waves of a workgroup, and workgroups.
+struct Cut {
+  int waves, splits;
+};
+Cut choose_cut(const Shards& s, int64_t rows, int ntop) {
   const int tiles = s.tile0[s.nranks];
-  int64_t want = rows > 0 ? (1024 + rows - 1) / rows : 1;
-  want = std::min<int64_t>(want, std::min(tiles, kMaxSplits));
-  if (ntop) want = std::min<int64_t>(want, kCandidates / ntop);
-  return (int)std::max<int64_t>(1, want);
+  // 16 waves for each of 256 compute units, at most one for each tile
+  const int64_t want = std::min<int64_t>(tiles, 4096 / std::max<int64_t>(1, rows));
+  Cut c{want > 8 ? 16 : want > 4 ? 8 : 4, 1};
+  if (want > 16) {
+    c.waves = 8;
+    int64_t splits = std::min<int64_t>((want + 7) / 8, kMaxSplits);
+    if (ntop) splits = std::min<int64_t>(splits, kCandidates / ntop);
+    c.splits = (int)splits;
+  }
+  return c;
 }
 size_t workspace_for(int64_t rows, int splits, int ntop) {
   return splits == 1 ? 0 : (size_t)rows * splits * (16 + 8 * (size_t)ntop);
+}
+
+template <class T>
+const void* pick_logprobs(bool top, int waves) {
+  if (waves == 16)
+    return top ? reinterpret_cast<const void*>(&logprobs_kernel<T, true, 16>)
+               : reinterpret_cast<const void*>(&logprobs_kernel<T, false, 16>);
+  if (waves == 8)
+    return top ? reinterpret_cast<const void*>(&logprobs_kernel<T, true, 8>)
+               : reinterpret_cast<const void*>(&logprobs_kernel<T, false, 8>);
+  return top ? reinterpret_cast<const void*>(&logprobs_kernel<T, true, 4>)
+             : reinterpret_cast<const void*>(&logprobs_kernel<T, false, 4>);
 }
 
 rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, const int64_t* strides, int nranks,
@@ -541,7 +632,7 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
                            float* entropy, float* lse, int32_t* top_ids, float* top_logprobs, void* workspace,
                            size_t workspace_bytes, void* stream) {
   LogprobsArgs a{};
-  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype)) return r;
+  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype, false)) return r;
   if (!(scale > 0.0f) || !std::isfinite(scale) || !std::isfinite(scale * kLog2e))
     return set_error(RAR_INVALID_ARGUMENT, "scale must be positive and finite");
   if (ntop < 0 || ntop > kMaxTop) return set_error(RAR_INVALID_ARGUMENT, "ntop must be in [0, 32]");
@@ -573,7 +664,8 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
     if (rar_result_t r = out(top_ids, 4, rows * ntop * 4, "top_ids")) return r;
     if (rar_result_t r = out(top_logprobs, 4, rows * ntop * 4, "top_logprobs")) return r;
   }
-  a.splits = choose_splits(a.x, rows, ntop);
+  const Cut cut = choose_cut(a.x, rows, ntop);
+  a.splits = cut.splits;
   const size_t need = workspace_for(rows, a.splits, ntop);
   if (need) {
     if (workspace_bytes < need)
@@ -596,11 +688,8 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
   a.parts = static_cast<v4f*>(workspace);
   a.keys = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + (size_t)rows * a.splits * 16);
   const bool bf = dtype == RAR_BFLOAT16;
-  const void* fn = bf ? (ntop ? reinterpret_cast<const void*>(&logprobs_kernel<BF16, true>)
-                              : reinterpret_cast<const void*>(&logprobs_kernel<BF16, false>))
-                      : (ntop ? reinterpret_cast<const void*>(&logprobs_kernel<F32, true>)
-                              : reinterpret_cast<const void*>(&logprobs_kernel<F32, false>));
-  if (rar_result_t r = launch_kernel(fn, dim3((unsigned)(rows * a.splits)), dim3(kThreads), &a, stream)) return r;
+  const void* fn = bf ? pick_logprobs<BF16>(ntop > 0, cut.waves) : pick_logprobs<F32>(ntop > 0, cut.waves);
+  if (rar_result_t r = launch_kernel(fn, dim3((unsigned)(rows * a.splits)), dim3(cut.waves * kWaveSize), &a, stream)) return r;
   if (a.splits == 1) return RAR_SUCCESS;
   const void* join_fn = bf ? reinterpret_cast<const void*>(&logprobs_join_kernel<BF16>)
                            : reinterpret_cast<const void*>(&logprobs_join_kernel<F32>);
@@ -613,7 +702,7 @@ rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* wi
                                     const float* grad_entropy, const float* grad_lse, void* const* grads,
                                     const int64_t* grad_strides, void* stream) {
   LogprobsBackwardArgs a{};
-  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype)) return r;
+  if (rar_result_t r = fill_shards(a.x, logits, widths, strides, nranks, rows, dtype, true)) return r;
   if (!(scale > 0.0f) || !std::isfinite(scale))
     return set_error(RAR_INVALID_ARGUMENT, "scale must be positive and finite");
   if (rows == 0) return RAR_SUCCESS;
@@ -678,9 +767,9 @@ rar_result_t rar_logprobs_workspace(const int64_t* widths, int nranks, int64_t r
   return rar::guarded([&]() -> rar_result_t {
     rar::Shards s{};
     if (!bytes) return rar::set_error(RAR_INVALID_ARGUMENT, "bytes is NULL");
-    if (rar_result_t r = rar::fill_shards(s, nullptr, widths, nullptr, nranks, rows, dtype)) return r;
+    if (rar_result_t r = rar::fill_shards(s, nullptr, widths, nullptr, nranks, rows, dtype, false)) return r;
     if (ntop < 0 || ntop > rar::kMaxTop) return rar::set_error(RAR_INVALID_ARGUMENT, "ntop must be in [0, 32]");
-    *bytes = rar::workspace_for(rows, rar::choose_splits(s, rows, ntop), ntop);
+    *bytes = rar::workspace_for(rows, rar::choose_cut(s, rows, ntop).splits, ntop);
     return RAR_SUCCESS;
   });
 }

@@ -199,6 +199,13 @@ __device__ __forceinline__ void store_part(typename T::bits* p, int n, v4u v) {
   }
 }
 
+// Between a wave's stores to LDS and its own loads: LDS keeps a wave's order,
+// so only the compiler has to.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Four neighbouring elements, `n` of them there, as fp32.
 template <class T>
 __device__ __forceinline__ void load4(const typename T::bits* p, int n, float* f) {
