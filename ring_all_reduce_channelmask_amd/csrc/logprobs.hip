@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(Logprobs
         }
         n = 2 * args.ntop;  // unused places are zero: below every candidate
       }
-      if (over || n > kCandidates / 2 || (round == 0 && n > args.ntop)) {
+      if (over || n > args.ntop + 16 || (round == 0 && n > args.ntop)) {
         select_top(top, n, args.ntop);
         const uint64_t kth = top.best[args.ntop - 1];
         n = args.ntop;

@@ -8,6 +8,7 @@ row-parallel projection.  Tensors are on one device; what a call allocates
 """
 import collections
 import ctypes
+import functools
 
 from . import _lib
 
@@ -19,98 +20,114 @@ LogProbs.__doc__ = """Of each row: the given token's log probability, the entrop
 sum of exponentials (all fp32 [rows]) and the most probable tokens (int32 ids
 and fp32 log probabilities, [rows, ntop])."""
 
-_DTYPE = None
+_torch = None
+_DTYPE = {}
 
 
-def _dtype(t):
-    global _DTYPE
-    if _DTYPE is None:
+def _start(ts, what):
+    """The list's first tensor, its dtype code and device index."""
+    global _torch
+    if _torch is None:
         import torch
-        _DTYPE = {torch.float32: _lib.DTYPE["float32"], torch.bfloat16: _lib.DTYPE["bfloat16"]}
-    if t.dtype not in _DTYPE:
-        raise TypeError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
-    return _DTYPE[t.dtype]
+        _DTYPE.update({torch.float32: _lib.DTYPE["float32"], torch.bfloat16: _lib.DTYPE["bfloat16"]})
+        _torch = torch
+    if not isinstance(ts, (list, tuple)) or not ts:
+        raise ValueError(f"{what} must be a list of tensors")
+    like = ts[0]
+    dt = _DTYPE.get(like.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {like.dtype}: float32 or bfloat16")
+    dev = like.get_device()
+    if dev < 0:
+        raise ValueError(f"{what} must be device tensors")
+    return like, dt, dev
 
 
-def _on(like, stream):
-    """The stream handle of a call, and the stream if it is not the current one."""
-    import torch
-    current = torch.cuda.current_stream(like.device)
-    if stream is None or stream == current:
-        return current.cuda_stream, None
+def _on(dev, stream):
+    """The stream handle of a call, and the stream if one was given."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev), None
     return stream.cuda_stream, stream
 
 
 def _new(stream, make):
     if stream is None:
         return make()
-    import torch
-    with torch.cuda.stream(stream):
+    with _torch.cuda.stream(stream):
         return make()
-
-
-def _check_list(ts, what):
-    if not isinstance(ts, (list, tuple)) or not ts:
-        raise ValueError(f"{what} must be a list of tensors")
-
-
-def _same(t, like, what):
-    if t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{what} must be on {like.device} with dtype {like.dtype}")
 
 
 def _pointers(ts):
     return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
 
 
-def _rows(ts, rows, what, like):
-    """Widths and row strides of [rows, width] tensors with unit column stride."""
+@functools.lru_cache(maxsize=1024)
+def _longs(values):
+    """A host array of int64, read only: kept for the next call of that shape."""
+    return (ctypes.c_int64 * len(values))(*values)
+
+
+def _rows(ts, rows, dtype, dev, what):
+    """Widths and row strides (tuples) of [rows, width] tensors with unit column stride."""
+    if not isinstance(ts, (list, tuple)) or not ts:
+        raise ValueError(f"{what} must be a list of tensors")
     widths, strides = [], []
     for t in ts:
-        _same(t, like, what)
-        if t.dim() != 2 or t.shape[0] != rows:
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise ValueError(f"{what} must be on cuda:{dev} with dtype {dtype}")
+        if t.dim() != 2 or t.size(0) != rows:
             raise ValueError(f"{what} must be [{rows}, width] tensors")
-        w = t.shape[1]
-        if w > 1 and t.stride(1) != 1:
+        w = t.size(1)
+        s, unit = t.stride()
+        if unit != 1 and w > 1:
             raise ValueError(f"{what} must have unit column stride")
-        s = t.stride(0)
-        if rows > 1 and s < w:
-            raise ValueError(f"{what} must not have overlapping rows")
+        if s < w:
+            if rows > 1:
+                raise ValueError(f"{what} must not have overlapping rows")
+            s = w
         widths.append(w)
-        strides.append(s if s > w else w)
-    n = len(ts)
-    return (ctypes.c_int64 * n)(*widths), (ctypes.c_int64 * n)(*strides), widths
+        strides.append(s)
+    return tuple(widths), tuple(strides)
 
 
-def _vector(t, n, dtype, like, what):
-    if t.dtype != dtype or t.device != like.device or t.dim() != 1 or t.shape[0] != n or \
+def _vector(t, n, dtype, dev, what):
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 1 or t.size(0) != n or \
             (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous [{n}] {dtype} tensor on {like.device}")
+        raise ValueError(f"{what} must be a contiguous [{n}] {dtype} tensor on cuda:{dev}")
     return t.data_ptr()
 
 
-def _flat(ts, count, like, what):
+def _flat(ts, count, dtype, dev, what):
+    if not isinstance(ts, (list, tuple)) or not ts:
+        raise ValueError(f"{what} must be a list of tensors")
     for t in ts:
-        _same(t, like, what)
-        if t.numel() != count or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous with {count} elements each")
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() != count or \
+                not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous on cuda:{dev}, with {count} elements of "
+                             f"{dtype} each")
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(entry, *shape):
+    """Bytes of workspace that calls of a shape need."""
+    need = ctypes.c_size_t()
+    _lib.check(getattr(_lib.load(), entry)(_longs(shape[0]), len(shape[0]), *shape[1:],
+                                           ctypes.byref(need)))
+    return need.value
 
 
 def _dropout(fn, ins, outs, extra, p, rng, call, stream):
-    import torch
-    _check_list(ins, "the inputs")
-    _check_list(outs, "the outputs")
-    like = ins[0]
-    dt, count = _dtype(like), like.numel()
-    _flat(ins, count, like, "the inputs")
-    _flat(outs, count, like, "the outputs")
+    like, dt, dev = _start(ins, "the inputs")
+    dtype, count = like.dtype, like.numel()
+    _flat(ins, count, dtype, dev, "the inputs")
+    _flat(outs, count, dtype, dev, "the outputs")
     if extra is not None:
-        _flat([extra], count, like, "the residual or its gradient")
-    rng_ptr = _vector(rng, 2, torch.int64, like, "rng")
-    handle, _ = _on(like, stream)
-    _lib.check(fn(_pointers(ins), len(ins), _pointers(outs), len(outs),
-                  None if extra is None else extra.data_ptr(), count, dt, p, rng_ptr, call,
-                  handle))
+        _flat((extra,), count, dtype, dev, "the residual or its gradient")
+        extra = extra.data_ptr()
+    rng_ptr = _vector(rng, 2, _torch.int64, dev, "rng")
+    handle, _ = _on(dev, stream)
+    _lib.check(fn(_pointers(ins), len(ins), _pointers(outs), len(outs), extra, count, dt, p,
+                  rng_ptr, call, handle))
 
 
 def dropout_allreduce(sends, recvs, p, rng, call=0, residual=None, stream=None):
@@ -134,37 +151,34 @@ def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
     under the logits ``shards`` (one [rows, width] tensor per rank, the
     vocabulary in rank order), with the entropy and the ``ntop`` most probable
     tokens.  Returns a LogProbs, written into ``out`` if one is given."""
-    import torch
-    _check_list(shards, "shards")
-    like = shards[0]
-    dt, rows = _dtype(like), like.shape[0]
-    widths, strides, _ = _rows(shards, rows, "shards", like)
-    n, lib = len(shards), _lib.load()
-    handle, other = _on(like, stream)
-    ids_ptr = _vector(ids, rows, torch.int64, like, "ids")
-    need = ctypes.c_size_t()
-    _lib.check(lib.rar_logprobs_workspace(widths, n, rows, dt, ntop, ctypes.byref(need)))
+    like, dt, dev = _start(shards, "shards")
+    dtype, rows, n = like.dtype, like.size(0), len(shards)
+    widths, strides = _rows(shards, rows, dtype, dev, "shards")
+    handle, other = _on(dev, stream)
+    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids")
+    need = _workspace("rar_logprobs_workspace", widths, rows, dt, ntop)
+    f32, i32, device = _torch.float32, _torch.int32, like.device
     if out is None:
         def make():
-            f = torch.empty((3, rows), dtype=torch.float32, device=like.device).unbind(0)
-            top = (torch.empty((rows, ntop), dtype=torch.int32, device=like.device),
-                   torch.empty((rows, ntop), dtype=torch.float32, device=like.device))
-            return LogProbs(*f, *top)
+            return LogProbs(*_torch.empty((3, rows), dtype=f32, device=device).unbind(0),
+                            _torch.empty((rows, ntop), dtype=i32, device=device),
+                            _torch.empty((rows, ntop), dtype=f32, device=device))
         out = _new(other, make)
     else:
         for t, what in zip(out[:3], ("logprob", "entropy", "lse")):
-            _vector(t, rows, torch.float32, like, what)
-        for t, d in ((out.top_ids, torch.int32), (out.top_logprobs, torch.float32)):
-            if t.dtype != d or t.device != like.device or tuple(t.shape) != (rows, ntop) or \
+            _vector(t, rows, f32, dev, what)
+        for t, d in ((out.top_ids, i32), (out.top_logprobs, f32)):
+            if t.dtype is not d or t.get_device() != dev or tuple(t.shape) != (rows, ntop) or \
                     not t.is_contiguous():
                 raise ValueError(f"the alternatives must be contiguous [{rows}, {ntop}] tensors")
-    work = _new(other, lambda: torch.empty(need.value, dtype=torch.uint8, device=like.device)) \
-        if need.value else None
-    _lib.check(lib.rar_logprobs(
-        _pointers(shards), widths, strides, n, rows, dt, scale, ids_ptr, ntop,
+    work = None
+    if need:
+        work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=device))
+    _lib.check(_lib.load().rar_logprobs(
+        _pointers(shards), _longs(widths), _longs(strides), n, rows, dt, scale, ids_ptr, ntop,
         out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
         out.top_ids.data_ptr(), out.top_logprobs.data_ptr(),
-        work.data_ptr() if work is not None else None, need.value, handle))
+        work.data_ptr() if need else None, need, handle))
     return out
 
 
@@ -174,28 +188,26 @@ def logprobs_backward(shards, ids, lse, entropy, grad_logprob, grad_entropy=None
     lse (fp32 [rows]; None for zero).  ``lse`` and ``entropy`` are those that
     logprobs returned (``entropy`` may be None without ``grad_entropy``).
     Writes into ``grads`` if given, which may be ``shards`` (in place)."""
-    import torch
-    _check_list(shards, "shards")
-    like = shards[0]
-    dt, rows = _dtype(like), like.shape[0]
-    widths, strides, w = _rows(shards, rows, "shards", like)
-    handle, other = _on(like, stream)
+    like, dt, dev = _start(shards, "shards")
+    dtype, rows = like.dtype, like.size(0)
+    widths, strides = _rows(shards, rows, dtype, dev, "shards")
+    handle, other = _on(dev, stream)
     if grads is None:
-        grads = _new(other, lambda: [torch.empty((rows, k), dtype=like.dtype, device=like.device)
-                                     for k in w])
-    _check_list(grads, "grads")
-    gwidths, gstrides, gw = _rows(grads, rows, "grads", like)
-    if gw != w:
+        grads = _new(other, lambda: [_torch.empty((rows, k), dtype=dtype, device=like.device)
+                                     for k in widths])
+    gwidths, gstrides = _rows(grads, rows, dtype, dev, "grads")
+    if gwidths != widths:
         raise ValueError("grads must have the widths of shards")
+    f32 = _torch.float32
 
     def vec(t, what):
-        return None if t is None else _vector(t, rows, torch.float32, like, what)
-    ids_ptr = _vector(ids, rows, torch.int64, like, "ids")
+        return None if t is None else _vector(t, rows, f32, dev, what)
+    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids")
     _lib.check(_lib.load().rar_logprobs_backward(
-        _pointers(shards), widths, strides, len(shards), rows, dt, scale, ids_ptr,
+        _pointers(shards), _longs(widths), _longs(strides), len(shards), rows, dt, scale, ids_ptr,
         vec(lse, "lse"), vec(entropy, "entropy"), vec(grad_logprob, "grad_logprob"),
-        vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads), gstrides,
-        handle))
+        vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads),
+        _longs(gstrides), handle))
     return grads
 
 
@@ -207,36 +219,28 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
     [tokens, outer]; ``downs``: a [adapters, rank, width] tensor per rank;
     ``up``: [adapters, outer, rank]; ``scales``: fp32 [adapters].  An output
     may be one of the partials."""
-    import torch
-    for ts, what in ((xs, "xs"), (partials, "partials"), (recvs, "recvs"), (downs, "downs")):
-        _check_list(ts, what)
-    n, like = len(xs), xs[0]
-    dt, tokens = _dtype(like), like.shape[0]
-    if len(partials) != n or len(downs) != n:
-        raise ValueError("xs, partials and downs need one tensor per rank")
-    if up.dim() != 3:
-        raise ValueError("up must be [adapters, outer, rank]")
+    like, dt, dev = _start(xs, "xs")
+    dtype, tokens, n = like.dtype, like.size(0), len(xs)
+    widths, x_strides = _rows(xs, tokens, dtype, dev, "xs")
+    outers, p_strides = _rows(partials, tokens, dtype, dev, "partials")
+    recv_outers, r_strides = _rows(recvs, tokens, dtype, dev, "recvs")
+    if up.dim() != 3 or up.dtype is not dtype or up.get_device() != dev or not up.is_contiguous():
+        raise ValueError("up must be a contiguous [adapters, outer, rank] tensor like xs")
     adapters, outer, rank = up.shape
-    widths, x_strides, w = _rows(xs, tokens, "xs", like)
-    _, p_strides, pw = _rows(partials, tokens, "partials", like)
-    _, r_strides, rw = _rows(recvs, tokens, "recvs", like)
-    if any(k != outer for k in pw + rw):
-        raise ValueError(f"partials and recvs must be [{tokens}, {outer}] tensors")
-    for t, k in zip(downs, w):
-        _same(t, like, "downs")
-        if tuple(t.shape) != (adapters, rank, k) or not t.is_contiguous():
-            raise ValueError(f"downs must be contiguous [{adapters}, {rank}, width] tensors")
-    _same(up, like, "up")
-    if not up.is_contiguous():
-        raise ValueError("up must be contiguous")
-    handle, other = _on(like, stream)
-    lib = _lib.load()
-    need = ctypes.c_size_t()
-    _lib.check(lib.rar_adapter_workspace(widths, n, tokens, dt, rank, ctypes.byref(need)))
-    work = _new(other, lambda: torch.empty(need.value, dtype=torch.uint8, device=like.device))
-    _lib.check(lib.rar_adapter_allreduce(
-        _pointers(xs), widths, x_strides, _pointers(partials), p_strides, n, _pointers(recvs),
-        r_strides, len(recvs), tokens, outer, dt, _pointers(downs), up.data_ptr(), adapters, rank,
-        _vector(ids, tokens, torch.int64, like, "ids"),
-        None if scales is None else _vector(scales, adapters, torch.float32, like, "scales"),
-        work.data_ptr(), need.value, handle))
+    if outers != (outer,) * n or recv_outers != (outer,) * len(recvs):
+        raise ValueError(f"partials (one per rank) and recvs must be [{tokens}, {outer}] tensors")
+    if not isinstance(downs, (list, tuple)) or len(downs) != n:
+        raise ValueError("downs needs one tensor per rank")
+    for t, k in zip(downs, widths):
+        if t.dtype is not dtype or t.get_device() != dev or t.shape != (adapters, rank, k) or \
+                not t.is_contiguous():
+            raise ValueError(f"downs must be contiguous [{adapters}, {rank}, width] tensors like xs")
+    handle, other = _on(dev, stream)
+    need = _workspace("rar_adapter_workspace", widths, tokens, dt, rank)
+    work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
+    _lib.check(_lib.load().rar_adapter_allreduce(
+        _pointers(xs), _longs(widths), _longs(x_strides), _pointers(partials), _longs(p_strides),
+        n, _pointers(recvs), _longs(r_strides), len(recvs), tokens, outer, dt, _pointers(downs),
+        up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids"),
+        None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
+        work.data_ptr(), need, handle))
