@@ -115,9 +115,12 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
     for (int m = 0; m < kM; ++m)
 #pragma unroll
       for (int n = 0; n < kN; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    // One step's operands: rows 0 .. 16 kM - 1 are tokens (those of other
-    // adapters zero), the rest rows of the adapter's weights (those past its
-    // rank repeat the last one and are not written).
+    // One step's operands: rows 0 .. 16 kM - 1 are tokens, the rest rows of the
+    // adapter's weights.  In the place of other adapters' tokens and of rows
+    // past the rank a row that is there is repeated; its results are not
+    // written.  So all loads are issued together: each with a condition of its
+    // own, they would wait for each other.
+    const int first = __builtin_ctzll(members);
     v4u next[kLoads];
     auto load = [&](int step) {
       int r = 0;
@@ -127,20 +130,18 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
       const bool full = col0 + kStep <= width;
       const bits* x = static_cast<const bits*>(args.x[r]) + token0 * args.x_stride[r] + col;
       const bits* w = static_cast<const bits*>(args.down[r]) + (int64_t)a * args.rank * width + col;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
+      auto row_at = [&](int i) {
         const int row = i * 8 + lane / 8;
-        const bits* p;
-        bool there = true;
-        if (i < 2 * kM) {
-          p = x + row * args.x_stride[r];
-          there = members >> row & 1;
-        } else {
-          const int n = row - 16 * kM;
-          p = w + (int64_t)(n < args.rank ? n : args.rank - 1) * width;
-        }
-        next[i] = v4u{0, 0, 0, 0};
-        if (there) next[i] = full ? load_16(p) : load_part<T>(p, width - col, 0);
+        if (i < 2 * kM) return x + (members >> row & 1 ? row : first) * args.x_stride[r];
+        const int n = row - 16 * kM;
+        return w + (int64_t)(n < args.rank ? n : args.rank - 1) * width;
+      };
+      if (full) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) next[i] = load_16(row_at(i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) next[i] = load_part<T>(row_at(i), width - col, 0);
       }
     };
     __syncthreads();  // the previous adapter's sums have been read
@@ -220,6 +221,30 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
   __shared__ v4f turn[kExpandWaves][16][17];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
   const int64_t run0 = (args.run0 + blockIdx.y) * args.run_tiles * 16;
+  const int col0 = ((int)blockIdx.x * kExpandWaves + wave) * 64;
+  const bool full = col0 + 64 <= args.outer;
+  const int col = col0 + lane % kRowLanes * T::kVec;  // of this lane's vectors
+  // vector v of a tile: token row0 + v * kVec
+  v4u p[kBatch][kVecs];
+  auto load_partials = [&](int64_t token0, int r0) {
+    const bool whole = full && token0 + 16 <= args.tokens;
+    const int64_t row0 = token0 + lane / kRowLanes;
+    auto each = [&](auto load) {
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r) {
+        if (r0 + r < args.nranks) {
+          const int64_t stride = args.partial_stride[r0 + r];
+          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + row0 * stride + col;
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) p[r][v] = load(src + v * T::kVec * stride, v);
+        }
+      }
+    };
+    if (whole) each([](const bits* q, int) { return load_nt(q); });
+    else each([&](const bits* q, int v) { return load_part<T>(q, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, 0); });
+  };
+  // A tile's partials are in flight from the end of the tile before.
+  load_partials(run0, 0);
   constexpr int kQuads = kR * kStep / 4;  // of a token's h
 #pragma unroll 4
   for (int i = threadIdx.x; i < args.run_tiles * 16 * kQuads; i += kExpandThreads) {
@@ -250,33 +275,14 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
     if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
   }
   __syncthreads();
-  const int col0 = ((int)blockIdx.x * kExpandWaves + wave) * 64;
   if (col0 >= args.outer) return;
-  const bool full = col0 + 64 <= args.outer;
-  const int col = col0 + lane % kRowLanes * T::kVec;  // of this lane's vectors
   int held = -1;  // the adapter whose weights are in registers
   v4u w[4][kR];
   for (int tile = 0; tile < args.run_tiles; ++tile) {
     const int64_t token0 = run0 + tile * 16;
     if (token0 >= args.tokens) return;
-    const int64_t row0 = token0 + lane / kRowLanes;  // token of vector v: + v * kVec
+    const int64_t row0 = token0 + lane / kRowLanes;
     const bool whole = full && token0 + 16 <= args.tokens;
-    v4u p[kBatch][kVecs];
-    auto load_partials = [&](int r0) {
-#pragma unroll
-      for (int r = 0; r < kBatch; ++r) {
-        if (r0 + r < args.nranks) {
-          const int64_t stride = args.partial_stride[r0 + r];
-          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + row0 * stride + col;
-#pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            if (whole) p[r][v] = load_nt(src + v * T::kVec * stride);
-            else p[r][v] = load_part<T>(src + v * T::kVec * stride, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, 0);
-          }
-        }
-      }
-    };
-    load_partials(0);  // in flight during the products
     const int id = load_id(args.ids, token0 + at, args.tokens, args.adapters);
     uint64_t left = __ballot(id >= 0) & 0xFFFF;
     const bool any = left != 0;
@@ -289,15 +295,19 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
       const bool mine = id == a;
       left &= ~__ballot(mine);
       if (a != held) {
+        const bits* up = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + col0 + at) * args.rank + group * T::kVec;
+        if (full && args.rank == kR * kStep) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int d = col0 + j * 16 + at;
-          const bits* row = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + d) * args.rank;
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < kR; ++c) {
-            const int q = c * kStep + group * T::kVec;
-            w[j][c] = load_part<T>(row + q, d < args.outer ? args.rank - q : 0, 0);
-          }
+            for (int c = 0; c < kR; ++c) w[j][c] = load_16(up + j * 16 * args.rank + c * kStep);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < kR; ++c)
+              w[j][c] = load_part<T>(up + j * 16 * args.rank + c * kStep,
+                                     col0 + j * 16 + at < args.outer ? args.rank - c * kStep - group * T::kVec : 0, 0);
         }
         held = a;
       }
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
     }
     float y[16];
     for (int r0 = 0; r0 < args.nranks; r0 += kBatch) {
-      if (r0) load_partials(r0);
+      if (r0) load_partials(token0, r0);
 #pragma unroll
       for (int r = 0; r < kBatch; ++r) {
         if (r0 + r < args.nranks) {
@@ -333,6 +343,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
         }
       }
     }
+    if (tile + 1 < args.run_tiles) load_partials(token0 + 16, 0);
     if (any) {
       wave_lds_fence();
 #pragma unroll
@@ -397,17 +408,30 @@ __global__ void __launch_bounds__(kThreads) expand_token_kernel(ExpandArgs) {
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) h[i] = hs[q + i];
     const bits* up = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + col0) * args.rank + q;
-#pragma unroll 8
-    for (int row0 = 0; row0 < kCols; row0 += kRows) {
-      const int row = row0 + tid / kLanes;
-      const v4u v = load_part<T>(up + (int64_t)row * args.rank, row < cols ? args.rank - q : 0, 0);
+    auto dot = [&](int row, v4u v) {
       float f[T::kVec], s = 0.0f;
       T::widen(v, f);
 #pragma unroll
       for (int i = 0; i < T::kVec; ++i) s = __builtin_fmaf(f[i], h[i], s);
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor(s, o);
+      s = group_reduce<kLanes>(s, [](float a, float b) { return a + b; });
       if (tid % kLanes == 0) delta[row] = s;
+    };
+    if (args.rank == kLanes * T::kVec) {
+      // no part vectors: 8 loads in flight (rows past the last repeat it)
+      constexpr int kBunch = kCols / kRows < 8 ? kCols / kRows : 8;
+      for (int row0 = tid / kLanes; row0 < kCols; row0 += kBunch * kRows) {
+        v4u v[kBunch];
+#pragma unroll
+        for (int i = 0; i < kBunch; ++i) {
+          const int row = row0 + i * kRows;
+          v[i] = load_16(up + (int64_t)(row < cols ? row : cols - 1) * args.rank);
+        }
+#pragma unroll
+        for (int i = 0; i < kBunch; ++i) dot(row0 + i * kRows, v[i]);
+      }
+    } else {
+      for (int row = tid / kLanes; row < kCols; row += kRows)
+        dot(row, load_part<T>(up + (int64_t)row * args.rank, row < cols ? args.rank - q : 0, 0));
     }
     __syncthreads();
 #pragma unroll
@@ -480,9 +504,10 @@ Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int r
   c.by_token = tokens * rank <= 16384;
   c.m = c.by_token ? 1 : 2;
   c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));
-  c.slots = c.by_token ? 16 : 1;
   const int want = std::max(1, 512 / c.tiles);
   c.parts = std::min({want, kMaxParts, (c.step0[nranks] + kWaves - 1) / kWaves});
+  // A workgroup without an adapter ends at once.
+  c.slots = c.by_token ? 16 : std::max(1, std::min(16, 2048 / std::max(1, c.tiles * c.parts)));
   return c;
 }
 

@@ -62,6 +62,22 @@ constexpr int wave_tile() { return kWaveSize * kVecsPerTile * T::kVec; }
 template <class T>
 constexpr int block_tile() { return kThreads * kVecsPerTile * T::kVec; }
 
+// A tile's vectors of one thread, those of kStride threads side by side; `left`
+// columns are there, the rest is -inf.
+template <class T, int kStride>
+__device__ __forceinline__ void load_vecs(v4u* raw, const typename T::bits* src, int left, int thread, bool full) {
+  if (full) {
+#pragma unroll
+    for (int v = 0; v < kVecsPerTile; ++v) raw[v] = load_nt(src + (v * kStride + thread) * T::kVec);
+  } else {
+#pragma unroll
+    for (int v = 0; v < kVecsPerTile; ++v) {
+      const int c = (v * kStride + thread) * T::kVec;
+      raw[v] = load_part<T>(src + c, left - c, T::kNegInf);
+    }
+  }
+}
+
 // The rank that holds tile t (or id v, from `first`).  Uniform: scalar code.
 __device__ __forceinline__ int rank_of(const int32_t* starts, int nranks, int at) {
   int r = 0;
@@ -261,19 +277,6 @@ __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, St
   }
 }
 
-// Each lane's maximum over its group of n = 4, 8 or 16 lanes.
-template <int n>
-__device__ __forceinline__ float group_max(float v) {
-#define RAR_STEP(ctrl) \
-  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xF, 0xF, true)))
-  RAR_STEP(0xB1);                      // lane ^ 1
-  RAR_STEP(0x4E);                      // lane ^ 2
-  if constexpr (n > 4) RAR_STEP(0x141);  // mirrored within 8
-  if constexpr (n > 8) RAR_STEP(0x140);  // mirrored within 16
-#undef RAR_STEP
-  return v;
-}
-
 template <class T, bool kTop, int kWgWaves>
 __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(LogprobsArgs) {
   const LogprobsArgs& args = kernel_args<LogprobsArgs>();
@@ -308,11 +311,7 @@ __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(Logprobs
     float most = -INFINITY, vec_most[kVecsPerTile];
     if (live) {
       const bool full = col0 + kTile <= width;
-#pragma unroll
-      for (int v = 0; v < kVecsPerTile; ++v) {
-        const int c = col0 + column(v * T::kVec);
-        raw[v] = full ? load_nt(src + c) : load_part<T>(src + c, width - c, T::kNegInf);
-      }
+      load_vecs<T, kWaveSize>(raw, src + col0, width - col0, lane, full);
       float x[kElems];
 #pragma unroll
       for (int v = 0; v < kVecsPerTile; ++v) T::widen(raw[v], x + v * T::kVec);
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(Logprobs
       if (round == 0) {
         // The k-th largest of 64 groups' maxima over the workgroup: k tokens at
         // least reach it, and seldom many more.
-        const float group = group_max<kWgWaves>(most);
+        const float group = group_reduce<kWgWaves>(most, [](float a, float b) { return fmaxf(a, b); });
         if (lane % kWgWaves == 0) top.group_most[wave * (kWaveSize / kWgWaves) + lane / kWgWaves] = group;
         __syncthreads();
         cut = fmaxf(cut, wave_kth(top.group_most[lane], args.ntop));
@@ -519,11 +518,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(LogprobsBac
   const typename T::bits* src = static_cast<const typename T::bits*>(args.x.ptr[r]) + row * args.x.stride[r];
   typename T::bits* dst = static_cast<typename T::bits*>(args.grad[r]) + row * args.grad_stride[r];
   v4u raw[kVecsPerTile];
-#pragma unroll
-  for (int v = 0; v < kVecsPerTile; ++v) {
-    const int c = col0 + (v * kThreads + (int)threadIdx.x) * T::kVec;
-    raw[v] = load_part<T>(src + c, width - c, T::kNegInf);
-  }
+  load_vecs<T, kThreads>(raw, src + col0, width - col0, threadIdx.x, col0 + kTile <= width);
   const float lse = args.lse[row];
   const bool empty = lse == -INFINITY;
   const int64_t id = args.ids[row];

@@ -199,6 +199,21 @@ __device__ __forceinline__ void store_part(typename T::bits* p, int n, v4u v) {
   }
 }
 
+// Combine each lane's value over its group of n = 1, 2, 4 ... 32 lanes, with
+// lane moves inside the vector unit up to 16.
+template <int n, class Op>
+__device__ __forceinline__ float group_reduce(float v, Op op) {
+#define RAR_STEP(ctrl) \
+  v = op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), ctrl, 0xF, 0xF, true)))
+  if constexpr (n > 1) RAR_STEP(0xB1);   // lane ^ 1
+  if constexpr (n > 2) RAR_STEP(0x4E);   // lane ^ 2
+  if constexpr (n > 4) RAR_STEP(0x141);  // mirrored within 8
+  if constexpr (n > 8) RAR_STEP(0x140);  // mirrored within 16
+#undef RAR_STEP
+  if constexpr (n > 16) v = op(v, __shfl_xor(v, 16));
+  return v;
+}
+
 // Between a wave's stores to LDS and its own loads: LDS keeps a wave's order,
 // so only the compiler has to.
 __device__ __forceinline__ void wave_lds_fence() {
