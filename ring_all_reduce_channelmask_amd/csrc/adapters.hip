@@ -25,7 +25,7 @@ namespace {
 constexpr int kMaxRank = 128;  // of an adapter
 constexpr int kThreads = 256, kWaves = kThreads / kWaveSize;
 constexpr int kMaxParts = 16;
-constexpr int kExpandThreads = 256, kExpandWaves = kExpandThreads / kWaveSize;
+constexpr int kRunCols = 64 * kWaves;  // columns of an expand workgroup
 
 struct ShrinkArgs {
   const void* x[kMaxRanks];
@@ -202,101 +202,125 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
   return s;
 }
 
-// y of a run of at most kTiles * 16 tokens x 64 columns a wave, a tile of 16
-// tokens at a time.  The run's h is laid out in LDS first, for bf16 as two bf16
-// numbers whose sum has 16 bits of it.  In the products the columns are the
-// MFMA's rows and the tokens its columns; the result passes through LDS so
-// that the partials and y move in whole 128-byte lines (a lane's own results
-// would make 64-byte pieces of them: 4096 x 7168, 4 ranks, 150 us against
-// @@ without any adapter).
+// y of a run of at most kTiles * 16 tokens x 256 columns, a tile of 16 tokens
+// at a time.  The run's h is laid out in LDS first, for bf16 as two bf16
+// numbers whose sum has 16 bits of it.  In the products a wave takes 64
+// columns, which are the MFMA's rows, and the tokens are its columns.  The
+// result passes through LDS, so that the partials and y move in pieces of 256
+// neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
+// adapter: in the products' own layout, 64 bytes a piece, 150 us; 64 columns a
+// piece 104 us; 256 columns @@ us).
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
-__global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
+__global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
   constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts
   constexpr int kForms = T::kVec == 8 ? 2 : 1;
-  constexpr int kRowLanes = 64 / T::kVec;  // lanes that move a token's 64 columns, kVec tokens at a time
+  constexpr int kRowLanes = kRunCols / T::kVec;      // threads that move a token's columns
+  constexpr int kRows = kWaveSize * T::kVec / kRunCols > 0 ? kWaveSize * T::kVec / kRunCols : 1;  // tokens a wave's vector covers
+  static_assert(kRows * kVecs * kWaves == 16, "four waves move a tile");
   typedef typename T::bits bits;
   __shared__ v4u hs[kForms][kTiles * 16][kRowVecs];
-  __shared__ v4f turn[kExpandWaves][16][17];
+  __shared__ v4f turn[16][kRunCols / 4 + 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, group = lane >> 4, at = lane & 15;
   const int64_t run0 = (args.run0 + blockIdx.y) * args.run_tiles * 16;
-  const int col0 = ((int)blockIdx.x * kExpandWaves + wave) * 64;
-  const bool full = col0 + 64 <= args.outer;
-  const int col = col0 + lane % kRowLanes * T::kVec;  // of this lane's vectors
-  // vector v of a tile: token row0 + v * kVec
+  const int first = (int)blockIdx.x * kRunCols;
+  const bool full = first + kRunCols <= args.outer;
+  const int left_cols = args.outer - first;
+  // vector v of a tile: token row + v * kRows, columns col ..
+  const int row = wave * kRows * kVecs + lane / kRowLanes, col = lane % kRowLanes * T::kVec;
   v4u p[kBatch][kVecs];
   auto load_partials = [&](int64_t token0, int r0) {
     const bool whole = full && token0 + 16 <= args.tokens;
-    const int64_t row0 = token0 + lane / kRowLanes;
     auto each = [&](auto load) {
 #pragma unroll
       for (int r = 0; r < kBatch; ++r) {
         if (r0 + r < args.nranks) {
           const int64_t stride = args.partial_stride[r0 + r];
-          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + row0 * stride + col;
+          const bits* src = static_cast<const bits*>(args.partial[r0 + r]) + token0 * stride + first;
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) p[r][v] = load(src + v * T::kVec * stride, v);
+          for (int v = 0; v < kVecs; ++v) p[r][v] = load(src, row + v * kRows, stride);
         }
       }
     };
-    if (whole) each([](const bits* q, int) { return load_nt(q); });
-    else each([&](const bits* q, int v) { return load_part<T>(q, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, 0); });
+    const int64_t rows = args.tokens - token0;
+    if (whole) {
+      each([&](const bits* src, int at_row, int64_t stride) { return load_nt(src + at_row * stride + col); });
+    } else if (left_cols >= T::kVec) {
+      // Rows and vectors past the end repeat the last ones, which is not used
+      // of them but for the part of a vector that is there.
+      const int c = col < left_cols - T::kVec ? col : left_cols - T::kVec;
+      each([&](const bits* src, int at_row, int64_t stride) {
+        return load_nt(src + (at_row < rows ? at_row : 0) * stride + c);
+      });
+#pragma unroll
+      for (int r = 0; r < kBatch; ++r)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) p[r][v] = shift_elements<T>(p[r][v], col - c);
+    } else {
+      each([&](const bits* src, int at_row, int64_t stride) {
+        return load_part<T>(src + at_row * stride + col, at_row < rows ? left_cols - col : 0, 0);
+      });
+    }
   };
   // A tile's partials are in flight from the end of the tile before.
   load_partials(run0, 0);
   constexpr int kQuads = kR * kStep / 4;  // of a token's h
-#pragma unroll 4
-  for (int i = threadIdx.x; i < args.run_tiles * 16 * kQuads; i += kExpandThreads) {
+#pragma unroll 2
+  for (int i = threadIdx.x; i < args.run_tiles * 16 * kQuads; i += kThreads) {
     const int t = i / kQuads, q = i % kQuads * 4;
-    const int64_t token = run0 + t;
-    const int id = load_id(args.ids, token, args.tokens, args.adapters);
-    const int places = id >= 0 ? args.rank - q : 0;
+    const int64_t token = run0 + t < args.tokens ? run0 + t : args.tokens - 1;
+    const int64_t id = args.ids[token];
+    const bool there = run0 + t < args.tokens && id >= 0 && id < args.adapters;
     float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p0 = 0; p0 < args.parts; p0 += 4) {
-      float f[4][4];
+    if (args.rank % 4 == 0) {
+      const float* src = args.h + token * args.rank + (q < args.rank ? q : 0);
+      for (int p0 = 0; p0 < args.parts; p0 += 4) {
+        v4u f[4];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        load4<F32>(reinterpret_cast<const uint32_t*>(args.h + ((p0 + p) * args.tokens + token) * args.rank + q),
-                   p0 + p < args.parts ? places : 0, f[p]);
+        for (int j = 0; j < 4; ++j)
+          f[j] = load_16(src + (p0 + j < args.parts ? p0 + j : 0) * args.tokens * args.rank);
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] += f[p][j];
+          for (int e = 0; e < 4; ++e) h[e] += p0 + j < args.parts ? __uint_as_float(f[j][e]) : 0.0f;
+      }
+    } else {
+      for (int e = 0; e < 4; ++e)
+        if (there && q + e < args.rank) h[e] = sum_parts(args.h + token * args.rank + q + e, args.tokens * args.rank, args.parts);
     }
-    const float scale = id >= 0 && args.scales ? args.scales[id] : 1.0f;
+    const float scale = there && args.scales ? args.scales[id] : 1.0f;
     float low[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] *= scale;
-      low[j] = h[j] - T::widen1(T::round1(h[j]));
+    for (int e = 0; e < 4; ++e) {
+      h[e] = there && q + e < args.rank ? h[e] * scale : 0.0f;
+      low[e] = h[e] - T::widen1(T::round1(h[e]));
     }
     store4<T>(reinterpret_cast<bits*>(hs[0][t]) + q, 4, h);
     if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
   }
-  __syncthreads();
-  if (col0 >= args.outer) return;
-  int held = -1;  // the adapter whose weights are in registers
+  const int col0 = first + wave * 64;  // of the wave's products
+  int held = -1;                       // the adapter whose weights are in registers
   v4u w[4][kR];
   for (int tile = 0; tile < args.run_tiles; ++tile) {
     const int64_t token0 = run0 + tile * 16;
     if (token0 >= args.tokens) return;
-    const int64_t row0 = token0 + lane / kRowLanes;
-    const bool whole = full && token0 + 16 <= args.tokens;
+    __syncthreads();  // h is there, and the tile before has been read from `turn`
     const int id = load_id(args.ids, token0 + at, args.tokens, args.adapters);
     uint64_t left = __ballot(id >= 0) & 0xFFFF;
     const bool any = left != 0;
     if (any && id < 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) turn[wave][at][j * 4 + group] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < 4; ++j) turn[at][wave * 16 + j * 4 + group] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
     while (left) {
       const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
       const bool mine = id == a;
       left &= ~__ballot(mine);
+      if (col0 >= args.outer) continue;
       if (a != held) {
         const bits* up = static_cast<const bits*>(args.up) + ((int64_t)a * args.outer + col0 + at) * args.rank + group * T::kVec;
-        if (full && args.rank == kR * kStep) {
+        if (col0 + 64 <= args.outer && args.rank == kR * kStep) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -322,13 +346,13 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = mma<T>(w[j][c], h, acc[j]);
         }
-      // from (token `at`, columns j * 16 + 4 * group ..) to the lanes' vectors;
-      // the wave's own part of LDS, and LDS keeps a wave's order
+      // token `at`, columns col0 + j * 16 + 4 * group ..
       if (mine) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) turn[wave][at][j * 4 + group] = acc[j];
+        for (int j = 0; j < 4; ++j) turn[at][wave * 16 + j * 4 + group] = acc[j];
       }
     }
+    __syncthreads();
     float y[16];
     for (int r0 = 0; r0 < args.nranks; r0 += kBatch) {
       if (r0) load_partials(token0, r0);
@@ -343,27 +367,26 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(ExpandArgs) {
         }
       }
     }
-    if (tile + 1 < args.run_tiles) load_partials(token0 + 16, 0);
+    if (tile + 1 < args.run_tiles) load_partials(token0 + 16 < args.tokens ? token0 + 16 : token0, 0);
     if (any) {
-      wave_lds_fence();
 #pragma unroll
       for (int v = 0; v < kVecs; ++v)
 #pragma unroll
         for (int q = 0; q < T::kVec / 4; ++q) {
-          const v4f d = turn[wave][lane / kRowLanes + v * T::kVec][lane % kRowLanes * (T::kVec / 4) + q];
+          const v4f d = turn[row + v * kRows][col / 4 + q];
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[v * T::kVec + q * 4 + i] += d[i];
         }
-      wave_lds_fence();
     }
+    const bool whole = full && token0 + 16 <= args.tokens;
     for (int k = 0; k < args.ncopies; ++k) {
       const int64_t stride = args.out_stride[k];
-      bits* dst = static_cast<bits*>(args.out[k]) + row0 * stride + col;
+      bits* dst = static_cast<bits*>(args.out[k]) + (token0 + row) * stride + first + col;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
         const v4u o = T::round(y + v * T::kVec);
-        if (whole) store_nt(dst + v * T::kVec * stride, o);
-        else store_part<T>(dst + v * T::kVec * stride, row0 + v * T::kVec < args.tokens ? args.outer - col : 0, o);
+        if (whole) store_nt(dst + v * kRows * stride, o);
+        else store_part<T>(dst + v * kRows * stride, token0 + row + v * kRows < args.tokens ? left_cols - col : 0, o);
       }
     }
   }
@@ -505,7 +528,9 @@ Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int r
   c.m = c.by_token ? 1 : 2;
   c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));
   const int want = std::max(1, 512 / c.tiles);
-  c.parts = std::min({want, kMaxParts, (c.step0[nranks] + kWaves - 1) / kWaves});
+  // (expand_kernel's workgroups read every part again: 1024 x 7168, rank 64, 50
+  // us with 16 parts, 45 with 8)
+  c.parts = std::min({want, c.by_token ? kMaxParts : kMaxParts / 2, (c.step0[nranks] + kWaves - 1) / kWaves});
   // A workgroup without an adapter ends at once.
   c.slots = c.by_token ? 16 : std::max(1, std::min(16, 2048 / std::max(1, c.tiles * c.parts)));
   return c;
@@ -616,14 +641,14 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   const void* fn = bf ? pick_expand<BF16>(rank, &tiles) : pick_expand<F32>(rank, &tiles);
   // The longer a run, the fewer times weights are loaded, but 4 workgroups for
   // each compute unit come first.
-  const int64_t cols = (outer + 64 * kExpandWaves - 1) / (64 * kExpandWaves);
+  const int64_t cols = (outer + kRunCols - 1) / kRunCols;
   while (tiles > 1 && cols * ((tokens + 16 * tiles - 1) / (16 * tiles)) < 1024) tiles /= 2;
   const int64_t runs = (tokens + 16 * tiles - 1) / (16 * tiles);
   e.run_tiles = tiles;
   // a grid's second dimension holds 65535 workgroups
   for (int64_t run0 = 0; run0 < runs; run0 += 65535) {
     e.run0 = run0;
-    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, runs - run0)), dim3(kExpandThreads), &e, stream))
+    if (rar_result_t q = launch_kernel(fn, dim3((unsigned)cols, (unsigned)std::min<int64_t>(65535, runs - run0)), dim3(kThreads), &e, stream))
       return q;
   }
   return RAR_SUCCESS;

@@ -221,6 +221,18 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A vector without its first n (0 or more) elements, zeros behind.
+template <class T>
+__device__ __forceinline__ v4u shift_elements(v4u v, int n) {
+  const int bits = n * (128 / T::kVec);
+  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+  if (bits >= 64) lo = hi, hi = 0;
+  const int b = bits & 63;
+  lo = b ? lo >> b | hi << (64 - b) : lo;
+  hi >>= b;
+  return bits >= 128 ? v4u{0, 0, 0, 0} : v4u{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // Four neighbouring elements, `n` of them there, as fp32.
 template <class T>
 __device__ __forceinline__ void load4(const typename T::bits* p, int n, float* f) {
