@@ -86,7 +86,8 @@ __device__ __forceinline__ int load_id(const int64_t* ids, int64_t token, int64_
 // Each wave stages a step's operands, 128 bytes of every row, in LDS: a load
 // there takes 8 whole lines, while in the MFMA's own layout, where
 // neighbouring lanes are different rows, it takes 45 accesses to the cache
-// (4096 tokens of 7168, rank 64: 45 us, staged @@ us).
+// (4096 tokens of 7168, rank 64: 45 us,
+// staged 34 us, with all of a step's loads issued together 30 us).
 template <class T, int kN, int kM>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
   const ShrinkArgs& args = kernel_args<ShrinkArgs>();
@@ -209,9 +210,13 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
 // result passes through LDS, so that the partials and y move in pieces of 256
 // neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
 // adapter: in the products' own layout, 64 bytes a piece, 150 us; 64 columns a
-// piece 104 us; 256 columns @@ us).
+// piece 104 us, 256 columns 107 us; 1000 x 5001, whose rows are not aligned: 64
+// columns a piece 41 us, 256 columns 30 us).
+// In bf16 the registers are held to 128, four workgroups a compute unit, for
+// ranks up to 64 (rank 16: 124 -> 117 us in all, rank 64: 144 -> 141); fp32
+// would spill.
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
-__global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs) {
+__global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR <= 2 ? 4 : 1) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
   constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts

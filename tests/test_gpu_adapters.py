@@ -84,6 +84,56 @@ def test_forward(dtype, tokens, widths, outer, rank, adapters):
             _check(y, want, f"ids {k}")
 
 
+# tokens * rank over 16384: the tokens go 16 at a time
+TILED = [
+    (150, [70, 61], 300, 128, 5),
+    (257, [129], 257, 64, 4),
+    (263, [33, 0, 100], 5, 65, 3),
+    (300, [64] * 5, 1025, 100, 30),
+    (529, [40, 41], 516, 32, 3),
+    (700, [17], 63, 33, 200),
+    (1100, [130, 126], 777, 16, 6),
+    (2100, [31], 40, 9, 4),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,widths,outer,rank,adapters", TILED, ids=[f"t{c[0]}-i{sum(c[1])}-o{c[2]}-r{c[3]}-a{c[4]}" for c in TILED])
+def test_tiles_of_tokens(dtype, tokens, widths, outer, rank, adapters):
+    r = np.random.default_rng(tokens)
+    spread = r.integers(-1, adapters, tokens)
+    runs = np.sort(r.integers(-1, adapters, tokens))
+    for k, ids in enumerate((spread, runs)):
+        dev, want = _case(dtype, tokens, widths, outer, rank, adapters, ids, tokens + k, pad=3 * k, skip=k)
+        for y in _run(dev, copies=1 + 2 * k):
+            _check(y, want, f"ids {k}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_tiles_with_more_than_four_ranks_in_place(dtype):
+    ids = np.arange(700) // 50 % 5 - 1
+    dev, want = _case(dtype, 700, [20, 21, 22, 23, 24, 25, 26], 333, 32, 4, ids, 11, pad=1, skip=1)
+    got = _run(dev, recvs=[dev["partials"][6], dev["partials"][2]])
+    for y in got:
+        _check(y, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_tiles_keep_a_broken_adapter_apart(dtype):
+    import torch
+    tokens = 600
+    ids = [i % 4 for i in range(tokens)]
+    dev, want = _case(dtype, tokens, [200, 100], 330, 32, 4, ids, 6)
+    dev["downs"][0][1, 3, 7] = float("nan")
+    dev["up"][2, 5, 2] = float("inf")
+    dev["xs"][0][12, :] = float("inf")
+    got = _run(dev)[0]
+    clean = [t for t in range(tokens) if ids[t] in (0, 3) and t != 12]
+    y, bound = want
+    _check(got[clean], (y[clean], bound[clean]))
+    assert not torch.isfinite(got[[1, 2]]).all(dim=1).any()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_many_tokens(dtype):
     """Enough token tiles that workgroups take several in turn."""

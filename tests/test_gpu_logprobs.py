@@ -99,6 +99,27 @@ def test_many_rows_take_one_workgroup_each(dtype, ntop):
         _close(got.top_logprobs[rows_checked], want["top_logprobs"], want["top_bound"], "top_logprobs")
 
 
+@pytest.mark.parametrize("rows", [2, 60, 300, 600])
+def test_every_cut_of_a_row(rows):
+    """Few rows are split over workgroups; more take 16, 8 and 4 waves each.
+    The first and last rows and the rows with many equal logits are checked."""
+    import ring_all_reduce_channelmask_amd as rar
+    widths = [33000, 1, 30011]
+    x = np.random.default_rng(rows).standard_normal((rows, sum(widths))).astype(np.float32) * 3
+    x[0] = np.floor(x[0])
+    x[-1, 1000:] = -np.inf
+    shards, exact = _shards(x, widths, "bfloat16")
+    ids = [(i * 7919) % sum(widths) for i in range(rows)]
+    at = sorted({0, 1, rows // 2, rows - 1})
+    for ntop in (0, 1, 20, 32):
+        got = rar.logprobs(shards, _ids(ids), ntop=ntop)
+        want = model_ops.logprobs(exact[at], [ids[i] for i in at], 1.0, ntop)
+        for name in ("lse", "entropy", "logprob"):
+            _close(getattr(got, name)[at], want[name], want[name + "_bound"], name)
+        assert np.array_equal(got.top_ids.cpu().numpy()[at], want["top_ids"])
+        _close(got.top_logprobs[at], want["top_logprobs"], want["top_bound"], "top_logprobs")
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("ntop", [0, 2, 32])
 def test_masks_infinities_and_nan(dtype, ntop):
