@@ -16,7 +16,12 @@
 // In bf16, h enters expand as the sum of two bf16 numbers (16 bits of it).
 //
 // Bound by memory: x, the partials and y move once; 2 * rank flops for each
-// element of x and y are far below the matrix rate.
+// element of x and y are far below the matrix rate.  Measured (kernels, 4
+// ranks, 7168 x 7168, bf16): 4096 tokens of 7 requests, rank 64: shrink 30 us
+// (59 MB of x and 40 MB of weights past the L2), expand 111 us (470 MB, 4.2
+// TB/s; the one-shot AllReduce moves as much in 88); 104 tokens with 64
+// adapters of rank 16: 10 + 8.5 us; 1 token 4.6 + 5.6 us, the time that two
+// dependent launches and their chains of loads take.
 #include "op_common.h"
 
 namespace rar {
@@ -528,7 +533,10 @@ Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int r
   Cut c{};
   const int step = dtype == RAR_BFLOAT16 ? step_width<BF16>() : step_width<F32>();
   for (int r = 0; r < nranks; ++r) c.step0[r + 1] = c.step0[r] + (int)((widths[r] + step - 1) / step);
-  // Few tokens: each may have an adapter of its own.
+  // Few tokens: each may have an adapter of its own.  By token the adapter's
+  // second matrix is read for every token, tiled for every adapter of a tile:
+  // 256 tokens, rank 64, one adapter each 79 us by token; 512 tokens 143 us
+  // tiled; of 4 requests 256 tokens 30 us by token, 300 tokens 24 us tiled.
   c.by_token = tokens * rank <= 16384;
   c.m = c.by_token ? 1 : 2;
   c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));
@@ -568,32 +576,34 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   const size_t es = (size_t)elem_size(dtype);
   ShrinkArgs s{};
   ExpandArgs e{};
-  std::vector<Block> reads, partial_reads, writes, scratch;
+  std::vector<Block> reads, partial_reads, writes;
+  reads.reserve(2 * nranks + 3);
+  partial_reads.reserve(nranks);
+  writes.reserve(ncopies + 1);
   auto flat = [](const void* p, int64_t bytes, const char* what) { return Block{p, 1, bytes, bytes, what}; };
   for (int r = 0; r < nranks; ++r) {
-    const std::string of = " of rank " + std::to_string(r);
     s.width[r] = (int32_t)widths[r];
     s.x_stride[r] = x_strides ? x_strides[r] : widths[r];
-    if (s.x_stride[r] < widths[r]) return set_error(RAR_INVALID_ARGUMENT, "input row stride" + of + " below its width");
+    if (s.x_stride[r] < widths[r]) return argument_error("input row stride of rank", r, "is below its width");
     if (widths[r]) {
-      if (rar_result_t q = check_pointer(xs[r], es, "input" + of)) return q;
-      if (rar_result_t q = check_pointer(downs[r], es, "down weights" + of)) return q;
+      if (rar_result_t q = check_pointer(xs[r], es, "input of rank", r)) return q;
+      if (rar_result_t q = check_pointer(downs[r], es, "down weights of rank", r)) return q;
       reads.push_back({xs[r], tokens, (int64_t)(widths[r] * es), (int64_t)(s.x_stride[r] * es), "an input"});
       reads.push_back(flat(downs[r], adapters * rank * widths[r] * (int64_t)es, "down weights"));
     }
     s.x[r] = xs[r];
     s.down[r] = downs[r];
     e.partial_stride[r] = partial_strides ? partial_strides[r] : outer;
-    if (e.partial_stride[r] < outer) return set_error(RAR_INVALID_ARGUMENT, "partial row stride" + of + " below its width");
-    if (rar_result_t q = check_pointer(partials[r], es, "partial" + of)) return q;
+    if (e.partial_stride[r] < outer) return argument_error("partial row stride of rank", r, "is below its width");
+    if (rar_result_t q = check_pointer(partials[r], es, "partial of rank", r)) return q;
     e.partial[r] = partials[r];
     partial_reads.push_back({partials[r], tokens, (int64_t)(outer * es), (int64_t)(e.partial_stride[r] * es), "a partial"});
   }
   for (int k = 0; k < ncopies; ++k) {
     e.out_stride[k] = out_strides ? out_strides[k] : outer;
     if (e.out_stride[k] < outer)
-      return set_error(RAR_INVALID_ARGUMENT, "output row stride " + std::to_string(k) + " below its width");
-    if (rar_result_t q = check_pointer(outs[k], es, "output " + std::to_string(k))) return q;
+      return argument_error("row stride of output", k, "is below its width");
+    if (rar_result_t q = check_pointer(outs[k], es, "output", k)) return q;
     e.out[k] = outs[k];
     writes.push_back({outs[k], tokens, (int64_t)(outer * es), (int64_t)(e.out_stride[k] * es), "output"});
   }
@@ -612,11 +622,14 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
                                                std::to_string(need) + " needed");
   if (need) {
     if (rar_result_t q = check_pointer(workspace, 16, "workspace")) return q;
-    writes.push_back(flat(workspace, (int64_t)need, "workspace"));
-    scratch.push_back(writes.back());
+    reads.push_back(flat(workspace, (int64_t)need, "workspace"));
   }
   if (rar_result_t q = check_blocks(reads, writes, false)) return q;
   if (rar_result_t q = check_blocks(partial_reads, writes, true)) return q;
+  // the workspace is written while the inputs and partials are still to be read
+  const std::vector<Block> scratch(reads.end() - (need ? 1 : 0), reads.end());
+  reads.resize(reads.size() - scratch.size());
+  if (rar_result_t q = check_blocks(reads, scratch, false)) return q;
   if (rar_result_t q = check_blocks(partial_reads, scratch, false)) return q;
   for (int r = 0; r <= nranks; ++r) s.step0[r] = cut.step0[r];
   s.ids = e.ids = ids;

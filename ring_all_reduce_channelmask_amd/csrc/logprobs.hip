@@ -18,6 +18,16 @@
 // time; a workgroup takes a run of consecutive tiles of one row.  Where there
 // are few rows a row is split over several workgroups, which leave (M, s, u)
 // and their best tokens in the workspace for a second kernel to join.
+//
+// Bound: in bf16 the vector units and memory alike.  A logit costs 5.5 plain
+// operations and an exp2 at a quarter of their rate, 38 cycles for a wave's 64:
+// 7.8 TB/s on all units at 2.4 GHz.  Measured (kernel): 4096 rows of 131072
+// bf16 without alternatives 167 us = 6.4 TB/s; 104 masked rows of 131075 with
+// 5 alternatives 17.6 us and 5 us for the join; 1 row of 32003 with 20
+// alternatives 9.9 us, of which the alternatives are 4 us (one threshold, one
+// list, one sort of about 25 keys).  The gradient is bound by memory: 4096
+// rows of 131072 bf16 338 us = 6.4 TB/s; 333 rows of 32003 fp32 with an
+// entropy gradient 17.6 us = 4.8 TB/s.
 #include "op_common.h"
 
 #include <cmath>
@@ -422,6 +432,8 @@ __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(Logprobs
         }
         n = 2 * args.ntop;  // unused places are zero: below every candidate
       }
+      // Sorting often keeps the bound close (4096 rows of 131072, 20
+      // alternatives: when 512 are held 272 us, from 16 beyond k on 218).
       if (over || n > args.ntop + 16 || (round == 0 && n > args.ntop)) {
         select_top(top, n, args.ntop);
         const uint64_t kth = top.best[args.ntop - 1];
@@ -584,7 +596,7 @@ rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* wi
   const size_t es = (size_t)elem_size(dtype);
   for (int r = 0; r < nranks; ++r) {
     if (widths[r] == 0) continue;
-    if (rar_result_t e = check_pointer(logits[r], es, "logits of rank " + std::to_string(r))) return e;
+    if (rar_result_t e = check_pointer(logits[r], es, "logits of rank", r)) return e;
     s.ptr[r] = logits[r];
   }
   return RAR_SUCCESS;
@@ -594,9 +606,14 @@ rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* wi
 struct Cut {
   int waves, splits;
 };
+// 16 waves for each of 256 compute units, at most one for each tile: one
+// workgroup of 4, 8 or 16 waves a row where that is enough, else several of 8
+// and a join.  Measured (us, by waves x workgroups a row; 131072 tokens bf16,
+// none / 20 alternatives): 1 row 16x1 11.5 / 25.6, 8x8 6.5 / 13.0; 256 rows
+// 16x1 14.9 / 30.5, 8x2 16.9 / 32.9, 4x1 18.1 / 36; 512 rows 8x1 25.4 / 45.5,
+// 16x1 28.4 / 56, 4x1 27.6 / 53; 4096 rows 4x1 171 / 218, 16x1 194 / 414.
 Cut choose_cut(const Shards& s, int64_t rows, int ntop) {
   const int tiles = s.tile0[s.nranks];
-  // 16 waves for each of 256 compute units, at most one for each tile
   const int64_t want = std::min<int64_t>(tiles, 4096 / std::max<int64_t>(1, rows));
   Cut c{want > 8 ? 16 : want > 4 ? 8 : 4, 1};
   if (want > 16) {
@@ -637,6 +654,8 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
   if (!logprob && !entropy && !lse && !ntop) return set_error(RAR_INVALID_ARGUMENT, "no output is asked for");
   const size_t es = (size_t)elem_size(dtype);
   std::vector<Block> reads, writes;
+  reads.reserve(nranks + 6);
+  writes.reserve(nranks + 6);
   for (int r = 0; r < nranks; ++r)
     reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits"});
   auto out = [&](void* p, size_t align, int64_t bytes, const char* what) -> rar_result_t {
@@ -705,11 +724,13 @@ rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* wi
   if (!logits || !grads) return set_error(RAR_INVALID_ARGUMENT, "logits or grads is NULL");
   const size_t es = (size_t)elem_size(dtype);
   std::vector<Block> reads, writes;
+  reads.reserve(nranks + 6);
+  writes.reserve(nranks + 6);
   for (int r = 0; r < nranks; ++r) {
     reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits of another rank"});
     a.grad_stride[r] = grad_strides ? grad_strides[r] : widths[r];
     if (widths[r] == 0) continue;
-    if (rar_result_t e = check_pointer(grads[r], es, "gradient of rank " + std::to_string(r))) return e;
+    if (rar_result_t e = check_pointer(grads[r], es, "gradient of rank", r)) return e;
     if (a.grad_stride[r] < widths[r])
       return set_error(RAR_INVALID_ARGUMENT, "gradient row stride of rank " + std::to_string(r) + " below its width");
     a.grad[r] = grads[r];

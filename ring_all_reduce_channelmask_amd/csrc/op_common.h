@@ -68,10 +68,13 @@ inline rar_result_t check_float_dtype(int dtype) {
   return RAR_SUCCESS;
 }
 
-inline rar_result_t check_pointer(const void* p, size_t align, const std::string& what) {
-  if (!p) return set_error(RAR_INVALID_ARGUMENT, what + " is NULL");
-  if (reinterpret_cast<uintptr_t>(p) & (align - 1))
-    return set_error(RAR_INVALID_ARGUMENT, what + " is not aligned to its element size");
+// `index` >= 0 names one of several; the message is made only on failure.
+inline rar_result_t argument_error(const char* what, int index, const char* why) {
+  return set_error(RAR_INVALID_ARGUMENT, what + (index < 0 ? std::string() : " " + std::to_string(index)) + " " + why);
+}
+inline rar_result_t check_pointer(const void* p, size_t align, const char* what, int index = -1) {
+  if (!p) return argument_error(what, index, "is NULL");
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1)) return argument_error(what, index, "is not aligned to its element size");
   return RAR_SUCCESS;
 }
 

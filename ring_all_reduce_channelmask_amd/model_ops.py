@@ -57,8 +57,14 @@ def _new(stream, make):
         return make()
 
 
+_ARRAYS = [ctypes.c_void_p * n for n in range(65)]  # of as many pointers
+
+
 def _pointers(ts):
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+    n = len(ts)
+    if n > 64:
+        raise ValueError("at most 64 tensors of a kind")
+    return _ARRAYS[n](*[t.data_ptr() for t in ts])
 
 
 @functools.lru_cache(maxsize=1024)
@@ -75,9 +81,10 @@ def _rows(ts, rows, dtype, dev, what):
     for t in ts:
         if t.dtype is not dtype or t.get_device() != dev:
             raise ValueError(f"{what} must be on cuda:{dev} with dtype {dtype}")
-        if t.dim() != 2 or t.size(0) != rows:
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != rows:
             raise ValueError(f"{what} must be [{rows}, width] tensors")
-        w = t.size(1)
+        w = shape[1]
         s, unit = t.stride()
         if unit != 1 and w > 1:
             raise ValueError(f"{what} must have unit column stride")
@@ -91,8 +98,8 @@ def _rows(ts, rows, dtype, dev, what):
 
 
 def _vector(t, n, dtype, dev, what):
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 1 or t.size(0) != n or \
-            (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or \
+            not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{n}] {dtype} tensor on cuda:{dev}")
     return t.data_ptr()
 
