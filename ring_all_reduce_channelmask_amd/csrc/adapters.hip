@@ -534,10 +534,14 @@ Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int r
   const int step = dtype == RAR_BFLOAT16 ? step_width<BF16>() : step_width<F32>();
   for (int r = 0; r < nranks; ++r) c.step0[r + 1] = c.step0[r] + (int)((widths[r] + step - 1) / step);
   // Few tokens: each may have an adapter of its own.  By token the adapter's
-  // second matrix is read for every token, tiled for every adapter of a tile:
-  // 256 tokens, rank 64, one adapter each 79 us by token; 512 tokens 143 us
-  // tiled; of 4 requests 256 tokens 30 us by token, 300 tokens 24 us tiled.
-  c.by_token = tokens * rank <= 16384;
+  // second matrix is read for every token; in tiles, for every adapter of a
+  // tile.  7168 x 7168, 4 ranks, by token / in tiles, us:
+  //            rank 16, one adapter each, of 4 requests; rank 64, each, of 4
+  //   64 tokens          15 / 37         10 / 14          27 / 36   16 / 18
+  //   128                21 / 42         13 / 14          44 / 44   20 / 19
+  //   512                56 / 67         29 / 24         143 / 131  47 / 30
+  //   1024               92 / 117        45 / 38         255 / 237  80 / 47
+  c.by_token = tokens * rank <= 8192;
   c.m = c.by_token ? 1 : 2;
   c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));
   const int want = std::max(1, 512 / c.tiles);

@@ -609,9 +609,10 @@ struct Cut {
 // 16 waves for each of 256 compute units, at most one for each tile: one
 // workgroup of 4, 8 or 16 waves a row where that is enough, else several of 8
 // and a join.  Measured (us, by waves x workgroups a row; 131072 tokens bf16,
-// none / 20 alternatives): 1 row 16x1 11.5 / 25.6, 8x8 6.5 / 13.0; 256 rows
-// 16x1 14.9 / 30.5, 8x2 16.9 / 32.9, 4x1 18.1 / 36; 512 rows 8x1 25.4 / 45.5,
-// 16x1 28.4 / 56, 4x1 27.6 / 53; 4096 rows 4x1 171 / 218, 16x1 194 / 414.
+// no / 20 alternatives): 1 row 8x8 6.6 / 13.3, 16x4 7.4 / 14.1; 104 rows 8x4
+// 11.3 / 21.1, 16x1 11.7 / 23.8; 256 rows 16x1 14.1 / 25.5, 8x1 16.2 / 33;
+// 512 rows 8x1 24 / 40, 16x1 26 / 47; 4096 rows 4x1 176 / 215, 8x1 173 / 222,
+// 16x1 185 / 343.
 Cut choose_cut(const Shards& s, int64_t rows, int ntop) {
   const int tiles = s.tile0[s.nranks];
   const int64_t want = std::min<int64_t>(tiles, 4096 / std::max<int64_t>(1, rows));
