@@ -457,8 +457,8 @@ rar_result_t rar_dropout_allreduce_backward(const void* const* grads, int ngrads
  *              do not matter before or after the call.
  * Masked tokens are -inf: they have probability 0 and are not alternatives
  * (places left over hold id -1 and -inf).  A row masked entirely gives lse
- * and logprob -inf, entropy 0.  A NaN or +inf gives NaN in its row's logprob
- * and entropy; NaN is no alternative. */
+ * and logprob -inf, entropy 0.  A NaN or +inf gives NaN in its row's lse,
+ * logprob and entropy; NaN is no alternative. */
 rar_result_t rar_logprobs(const void* const* logits, const int64_t* widths,
                           const int64_t* strides, int nranks, int64_t rows, rar_dtype_t dtype,
                           float scale, const int64_t* ids, int ntop, float* logprob,

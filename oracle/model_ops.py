@@ -16,11 +16,11 @@ U = 2.0 ** -24
 ROUND = {"float32": U, "bfloat16": 2.0 ** -8}
 
 
-def philox_fields(seed, offset, count):
-    """16 random bits of every element: Philox4x32 with 7 rounds (Salmon,
+def philox_fields(seed, offset, count, start=0):
+    """16 random bits of the elements from `start` (a multiple of 8) on: Philox4x32 with 7 rounds (Salmon,
     Moraes, Dror and Shaw, 2011), key = seed, counter = (element // 8, offset)."""
     out = []
-    for n in range((count + 7) // 8):
+    for n in range(start // 8, start // 8 + (count + 7) // 8):
         c = [n & 0xFFFFFFFF, n >> 32, offset & 0xFFFFFFFF, (offset >> 32) & 0xFFFFFFFF]
         k = [seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF]
         for _ in range(7):

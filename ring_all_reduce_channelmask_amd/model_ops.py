@@ -21,14 +21,18 @@ sum of exponentials (all fp32 [rows]) and the most probable tokens (int32 ids
 and fp32 log probabilities, [rows, ntop])."""
 
 _torch = None
+_raw_stream = None
 _DTYPE = {}
 
 
 def _start(ts, what):
     """The list's first tensor, its dtype code and device index."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        # the handle without a Stream object around it, where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
         _DTYPE.update({torch.float32: _lib.DTYPE["float32"], torch.bfloat16: _lib.DTYPE["bfloat16"]})
         _torch = torch
     if not isinstance(ts, (list, tuple)) or not ts:
@@ -46,7 +50,7 @@ def _start(ts, what):
 def _on(dev, stream):
     """The stream handle of a call, and the stream if one was given."""
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev), None
+        return _raw_stream(dev), None
     return stream.cuda_stream, stream
 
 

@@ -226,6 +226,38 @@ def test_streams_and_graph_replays():
         assert torch.equal(a, b), step
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_ranks_without_columns(dtype):
+    """No rank has a column of the input: the adapters add nothing."""
+    import torch
+    for tokens in (5, 600):
+        dev, want = _case(dtype, tokens, [0, 0], 70, 16, 3, [t % 4 - 1 for t in range(tokens)], 9)
+        _check(_run(dev)[0], want)
+
+
+def test_more_than_2_31_elements_between_rows():
+    """Row offsets beyond 32 bits in every strided operand, of few tokens and
+    of tiles of them."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    for tokens, stride in ((40, 60_000_001), (600, 3_700_001)):
+        dev, want = _case("bfloat16", tokens, [65, 64], 131, 16, 3, [t % 4 - 1 for t in range(tokens)], 10)
+        held = torch.empty(tokens * stride, dtype=torch.bfloat16, device="cuda")
+        assert held.numel() > 1 << 31
+        column = 0
+
+        def far(t):
+            nonlocal column
+            view = held.as_strided(t.shape, (stride, 1), column)
+            column += t.shape[1] + 3
+            return view.copy_(t)
+        for k in ("xs", "partials"):
+            dev[k] = [far(t) for t in dev[k]]
+        out = held.as_strided((tokens, 131), (stride, 1), column)
+        _check(_run(dev, recvs=[out])[0], want, f"{tokens} tokens")
+        del held, out, dev
+
+
 def test_no_tokens():
     import torch
     import ring_all_reduce_channelmask_amd as rar

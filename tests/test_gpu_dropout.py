@@ -163,6 +163,23 @@ def test_offset_carries_into_its_high_word():
     assert np.array_equal(out.cpu().numpy(), want.astype(np.float32))
 
 
+def test_more_than_2_31_elements():
+    """Indexes beyond 32 bits, of elements and of bytes."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    n, tail = (1 << 31) + 1029, 1029
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = torch.arange(tail, device="cuda") % 100 + 1
+    out = torch.empty_like(x)
+    rar.dropout_allreduce([x], [out], 0.5, _rng())
+    factor = (model_ops.philox_fields(SEED, OFFSET, tail, start=1 << 31) >= 32768) * 2.0
+    assert np.array_equal(out[-tail:].double().cpu().numpy(), factor * (np.arange(tail) % 100 + 1))
+    first = model_ops.keep_factor(SEED, OFFSET, 1024, 0.5)
+    assert np.array_equal(out[:1024].double().cpu().numpy(), first)
+    share = (out[:1 << 30] != 0).double().mean().item()
+    assert abs(share - 0.5) < 4 * 0.5 / (1 << 15)
+
+
 def test_streams_and_graph_replays():
     import torch
     import ring_all_reduce_channelmask_amd as rar

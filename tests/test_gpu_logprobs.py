@@ -288,6 +288,35 @@ def test_streams_and_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(list(c) + cg, list(e) + eg)), step
 
 
+def test_more_than_2_31_logits():
+    """Offsets beyond 32 bits in a shard, and gradients over them in place."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    rows, widths = 17000, [130003, 37]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    shards = []
+    for w in widths:
+        t = torch.empty((rows, w), dtype=torch.bfloat16, device="cuda")
+        for r0 in range(0, rows, 1000):
+            t[r0:r0 + 1000] = torch.randn((1000, w), generator=g, device="cuda") * 3
+        shards.append(t)
+    assert shards[0].numel() > 1 << 31
+    ids = torch.randint(0, sum(widths), (rows,), generator=g, device="cuda")
+    at = [0, 8000, 16520, 16999]  # before and behind element 2^31 of the first shard
+    exact = torch.cat([s[at].double() for s in shards], 1).cpu().numpy()
+    own = ids[at].tolist()
+    got = rar.logprobs(shards, ids, ntop=3)
+    want = model_ops.logprobs(exact, own, 1.0, 3)
+    for name in ("lse", "entropy", "logprob"):
+        _close(getattr(got, name)[at], want[name], want[name + "_bound"], name)
+    assert np.array_equal(got.top_ids[at].cpu().numpy(), want["top_ids"])
+    ones = torch.ones(rows, device="cuda")
+    rar.logprobs_backward(shards, ids, got.lse, None, ones, grads=shards)
+    grad, bound = model_ops.logprobs_backward(exact, own, got.lse[at].double().cpu().numpy(), np.zeros(4), np.ones(4), np.zeros(4),
+                                              np.zeros(4), 1.0, "bfloat16")
+    _close(torch.cat([s[at] for s in shards], 1), grad, bound, "gradient")
+
+
 def test_no_rows():
     import torch
     import ring_all_reduce_channelmask_amd as rar
