@@ -18,8 +18,8 @@
 // Bound by memory: x, the partials and y move once; 2 * rank flops for each
 // element of x and y are far below the matrix rate.  Measured (kernels, 4
 // ranks, 7168 x 7168, bf16): 4096 tokens of 7 requests, rank 64: shrink 30 us
-// (59 MB of x and 40 MB of weights past the L2), expand 111 us (470 MB, 4.2
-// TB/s; the one-shot AllReduce moves as much in 88); 104 tokens with 64
+// (59 MB of x and 40 MB of weights past the L2), expand 105 us (470 MB, 4.5
+// TB/s; the one-shot AllReduce moves 512 MiB in 88); 104 tokens with 64
 // adapters of rank 16: 10 + 8.5 us; 1 token 4.6 + 5.6 us, the time that two
 // dependent launches and their chains of loads take.
 #include "op_common.h"
@@ -218,7 +218,8 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
 // piece 104 us, 256 columns 107 us; 1000 x 5001, whose rows are not aligned: 64
 // columns a piece 41 us, 256 columns 30 us).
 // In bf16 the registers are held to 128, four workgroups a compute unit, for
-// ranks up to 64 (rank 16: 124 -> 117 us in all, rank 64: 144 -> 141); fp32
+// ranks up to 64 (runs of 4 tiles, rank 16: 124 -> 117 us in all, rank 64: 144
+// -> 141); fp32
 // would spill.
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
 __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR <= 2 ? 4 : 1) expand_kernel(ExpandArgs) {
@@ -493,21 +494,17 @@ const void* pick_shrink(int rank) {
   if (rank <= 64) return reinterpret_cast<const void*>(&shrink_kernel<T, 4, kM>);
   return reinterpret_cast<const void*>(&shrink_kernel<T, 8, kM>);
 }
-// Token tiles of a run: its h takes at most 36 KB of LDS.
-constexpr int kRunTiles = 4;
+// Token tiles of a run: one follows the other's loads, and more would take the
+// place of workgroups (their h is in LDS; 8192 tokens of 7168, rank 64: runs
+// of 4 tiles 250 us in all, of 2 242).
+constexpr int kRunTiles = 2;
 template <class T>
-const void* pick_expand(int rank, int* tiles) {
-  *tiles = kRunTiles;
+const void* pick_expand(int rank) {
   if (rank <= 4 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 1, kRunTiles>);
   if (rank <= 8 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 2, kRunTiles>);
-  if constexpr (T::kVec == 8) {
-    *tiles = kRunTiles / 2;
-    return reinterpret_cast<const void*>(&expand_kernel<T, 4, kRunTiles / 2>);
-  } else {
-    if (rank <= 16 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 4, kRunTiles>);
-    *tiles = kRunTiles / 2;
-    return reinterpret_cast<const void*>(&expand_kernel<T, 8, kRunTiles / 2>);
-  }
+  if constexpr (T::kVec == 4)
+    if (rank > 16 * T::kVec) return reinterpret_cast<const void*>(&expand_kernel<T, 8, kRunTiles>);
+  return reinterpret_cast<const void*>(&expand_kernel<T, 4, kRunTiles>);
 }
 template <class T>
 const void* pick_expand_token(int rank) {
@@ -659,12 +656,12 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   if (cut.by_token)
     return launch_kernel(bf ? pick_expand_token<BF16>(rank) : pick_expand_token<F32>(rank),
                          dim3((unsigned)((outer + kCols - 1) / kCols), (unsigned)tokens), dim3(kThreads), &e, stream);
-  int tiles = 0;
-  const void* fn = bf ? pick_expand<BF16>(rank, &tiles) : pick_expand<F32>(rank, &tiles);
-  // The longer a run, the fewer times weights are loaded, but 4 workgroups for
-  // each compute unit come first.
+  const void* fn = bf ? pick_expand<BF16>(rank) : pick_expand<F32>(rank);
+  // The longer a run, the fewer times weights are loaded, but 8 workgroups for
+  // each compute unit come first (4096 tokens: runs of 1 tile 141 us, of 2 133,
+  // of 4 140).
   const int64_t cols = (outer + kRunCols - 1) / kRunCols;
-  while (tiles > 1 && cols * ((tokens + 16 * tiles - 1) / (16 * tiles)) < 1024) tiles /= 2;
+  const int tiles = cols * ((tokens + 16 * kRunTiles - 1) / (16 * kRunTiles)) < 2048 ? 1 : kRunTiles;
   const int64_t runs = (tokens + 16 * tiles - 1) / (16 * tiles);
   e.run_tiles = tiles;
   // a grid's second dimension holds 65535 workgroups
