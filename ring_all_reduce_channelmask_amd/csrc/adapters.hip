@@ -18,7 +18,7 @@
 // Bound by memory: x, the partials and y move once; 2 * rank flops for each
 // element of x and y are far below the matrix rate.  Measured (kernels, 4
 // ranks, 7168 x 7168, bf16): 4096 tokens of 7 requests, rank 64: shrink 30 us
-// (59 MB of x and 40 MB of weights past the L2), expand 105 us (470 MB, 4.5
+// (59 MB of x and 40 MB of weights past the L2), expand 104 us (470 MB, 4.5
 // TB/s; the one-shot AllReduce moves 512 MiB in 88); 104 tokens with 64
 // adapters of rank 16: 10 + 8.5 us; 1 token 4.6 + 5.6 us, the time that two
 // dependent launches and their chains of loads take.
@@ -217,12 +217,11 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
 // adapter: in the products' own layout, 64 bytes a piece, 150 us; 64 columns a
 // piece 104 us, 256 columns 107 us; 1000 x 5001, whose rows are not aligned: 64
 // columns a piece 41 us, 256 columns 30 us).
-// In bf16 the registers are held to 128, four workgroups a compute unit, for
-// ranks up to 64 (runs of 4 tiles, rank 16: 124 -> 117 us in all, rank 64: 144
-// -> 141); fp32
-// would spill.
+// For bf16 ranks up to 32 the registers are held to 128, four workgroups a
+// compute unit (runs of 4 tiles, rank 16: 124 -> 117 us in all).  Larger ranks
+// and fp32 would spill (rank 64: 132 us without the bound, 133 with it).
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
-__global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR <= 2 ? 4 : 1) expand_kernel(ExpandArgs) {
+__global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
   constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts
