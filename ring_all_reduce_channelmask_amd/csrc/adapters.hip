@@ -576,10 +576,9 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   const size_t es = (size_t)elem_size(dtype);
   ShrinkArgs s{};
   ExpandArgs e{};
-  std::vector<Block> reads, partial_reads, writes;
-  reads.reserve(2 * nranks + 3);
-  partial_reads.reserve(nranks);
-  writes.reserve(ncopies + 1);
+  std::vector<Block> reads, writes;
+  reads.reserve(3 * nranks + 4);
+  writes.reserve(ncopies);
   auto flat = [](const void* p, int64_t bytes, const char* what) { return Block{p, 1, bytes, bytes, what}; };
   for (int r = 0; r < nranks; ++r) {
     s.width[r] = (int32_t)widths[r];
@@ -597,7 +596,8 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
     if (e.partial_stride[r] < outer) return argument_error("partial row stride of rank", r, "is below its width");
     if (rar_result_t q = check_pointer(partials[r], es, "partial of rank", r)) return q;
     e.partial[r] = partials[r];
-    partial_reads.push_back({partials[r], tokens, (int64_t)(outer * es), (int64_t)(e.partial_stride[r] * es), "a partial"});
+    // the thread that writes an element of y has read it of every partial
+    reads.push_back({partials[r], tokens, (int64_t)(outer * es), (int64_t)(e.partial_stride[r] * es), "a partial", kAnyOutput});
   }
   for (int k = 0; k < ncopies; ++k) {
     e.out_stride[k] = out_strides ? out_strides[k] : outer;
@@ -620,17 +620,16 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   if (workspace_bytes < need)
     return set_error(RAR_INVALID_ARGUMENT, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                                std::to_string(need) + " needed");
+  if (rar_result_t q = check_blocks(reads, writes)) return q;
   if (need) {
     if (rar_result_t q = check_pointer(workspace, 16, "workspace")) return q;
-    reads.push_back(flat(workspace, (int64_t)need, "workspace"));
+    // written while the inputs and partials are still to be read, and read
+    // while y is written
+    const Block scratch = flat(workspace, (int64_t)need, "workspace");
+    if (rar_result_t q = check_blocks({scratch}, writes)) return q;
+    for (Block& r : reads) r.in_place = kNoOutput;
+    if (rar_result_t q = check_blocks(reads, {scratch})) return q;
   }
-  if (rar_result_t q = check_blocks(reads, writes, false)) return q;
-  if (rar_result_t q = check_blocks(partial_reads, writes, true)) return q;
-  // the workspace is written while the inputs and partials are still to be read
-  const std::vector<Block> scratch(reads.end() - (need ? 1 : 0), reads.end());
-  reads.resize(reads.size() - scratch.size());
-  if (rar_result_t q = check_blocks(reads, scratch, false)) return q;
-  if (rar_result_t q = check_blocks(partial_reads, scratch, false)) return q;
   for (int r = 0; r <= nranks; ++r) s.step0[r] = cut.step0[r];
   s.ids = e.ids = ids;
   s.h = static_cast<float*>(workspace);

@@ -187,6 +187,7 @@ rar_result_t dropout_call(const void* const* src, int nsrc, void* const* dst, in
   if (rar_result_t r = check_pointer(rng, 8, "rng")) return r;
   DropoutArgs a{};
   const int64_t bytes = (int64_t)(count * es);
+  // A thread reads and writes the same elements of all buffers.
   std::vector<Block> reads, writes;
   reads.reserve(nsrc + 2);
   writes.reserve(ndst + 1);
@@ -194,7 +195,7 @@ rar_result_t dropout_call(const void* const* src, int nsrc, void* const* dst, in
   for (int r = 0; r < nsrc; ++r) {
     if (rar_result_t e = check_pointer(src[r], es, "input", r)) return e;
     a.src[r] = src[r];
-    reads.push_back({src[r], 1, bytes, bytes, "an input"});
+    reads.push_back({src[r], 1, bytes, bytes, "an input", kAnyOutput});
   }
   for (int k = 0; k < ndst; ++k) {
     if (rar_result_t e = check_pointer(dst[k], es, "output", k)) return e;
@@ -203,13 +204,13 @@ rar_result_t dropout_call(const void* const* src, int nsrc, void* const* dst, in
   }
   if (residual) {
     if (rar_result_t e = check_pointer(residual, es, "residual")) return e;
-    reads.push_back({residual, 1, bytes, bytes, "residual"});
+    reads.push_back({residual, 1, bytes, bytes, "residual", kAnyOutput});
   }
   if (dresidual) {
     if (rar_result_t e = check_pointer(dresidual, es, "dresidual")) return e;
     writes.push_back({dresidual, 1, bytes, bytes, "dresidual"});
   }
-  if (rar_result_t r = check_blocks(reads, writes, true)) return r;
+  if (rar_result_t r = check_blocks(reads, writes)) return r;
   a.residual = residual;
   a.dresidual = dresidual;
   a.rng = static_cast<const uint64_t*>(rng);

@@ -690,7 +690,7 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
     if (rar_result_t r = out(workspace, 16, (int64_t)need, "workspace")) return r;
     if (!workspace) return set_error(RAR_INVALID_ARGUMENT, "workspace is NULL");
   }
-  if (rar_result_t r = check_blocks(reads, writes, false)) return r;
+  if (rar_result_t r = check_blocks(reads, writes)) return r;
   a.rows = rows;
   a.ntop = ntop;
   a.scale = scale;
@@ -728,7 +728,9 @@ rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* wi
   reads.reserve(nranks + 6);
   writes.reserve(nranks + 6);
   for (int r = 0; r < nranks; ++r) {
-    reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits of another rank"});
+    // in place over its own logits alone: other ranks' are other workgroups'
+    reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits",
+                     widths[r] ? (int)writes.size() : kNoOutput});
     a.grad_stride[r] = grad_strides ? grad_strides[r] : widths[r];
     if (widths[r] == 0) continue;
     if (rar_result_t e = check_pointer(grads[r], es, "gradient of rank", r)) return e;
@@ -752,7 +754,7 @@ rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* wi
   if (rar_result_t r = in(grad_logprob, 4, "grad_logprob")) return r;
   if (rar_result_t r = in(grad_entropy, 4, "grad_entropy")) return r;
   if (rar_result_t r = in(grad_lse, 4, "grad_lse")) return r;
-  if (rar_result_t r = check_blocks(reads, writes, true)) return r;
+  if (rar_result_t r = check_blocks(reads, writes)) return r;
   a.scale = scale;
   a.ids = ids;
   a.lse = lse;

@@ -20,10 +20,12 @@ namespace rar {
 
 // A rectangle of device memory that a call reads or writes: `rows` rows of
 // `width` bytes, `stride` bytes apart.
+constexpr int kNoOutput = -1, kAnyOutput = -2;
 struct Block {
   const void* ptr;
   int64_t rows, width, stride;
   const char* what;
+  int in_place = kNoOutput;  // of an input: the output (its place in the list) that may be exactly it
 };
 
 // Whether two rectangles share a byte.  Exact for equal strides (columns of
@@ -43,9 +45,10 @@ inline bool blocks_overlap(const Block& a, const Block& b) {
 }
 
 // Outputs share no byte with each other, and with an input only where both
-// are the same rectangle and `in_place` allows it: every element is then
-// read by the thread that writes it, before it writes.
-inline rar_result_t check_blocks(const std::vector<Block>& reads, const std::vector<Block>& writes, bool in_place) {
+// are the same rectangle and the input names that output: it may name one
+// whose every element is written by the thread that reads the same element,
+// after it has read it, and by no other.
+inline rar_result_t check_blocks(const std::vector<Block>& reads, const std::vector<Block>& writes) {
   for (size_t i = 0; i < writes.size(); ++i) {
     for (size_t j = i + 1; j < writes.size(); ++j)
       if (blocks_overlap(writes[i], writes[j]))
@@ -55,7 +58,7 @@ inline rar_result_t check_blocks(const std::vector<Block>& reads, const std::vec
       if (!blocks_overlap(writes[i], r)) continue;
       const bool same = writes[i].ptr == r.ptr && writes[i].rows == r.rows && writes[i].width == r.width &&
                         (writes[i].stride == r.stride || r.rows == 1);
-      if (!in_place || !same)
+      if (!same || (r.in_place != kAnyOutput && r.in_place != (int)i))
         return set_error(RAR_INVALID_ARGUMENT, std::string(writes[i].what) + " " + std::to_string(i) + " overlaps " + r.what);
     }
   }
