@@ -455,10 +455,13 @@ rar_result_t rar_dropout_allreduce_backward(const void* const* grads, int ngrads
  *   workspace  16-byte aligned device memory of the size that
  *              rar_logprobs_workspace gives (0: NULL allowed); its contents
  *              do not matter before or after the call.
- * Masked tokens are -inf: they have probability 0 and are not alternatives
- * (places left over hold id -1 and -inf).  A row masked entirely gives lse
- * and logprob -inf, entropy 0.  A NaN or +inf gives NaN in its row's lse,
- * logprob and entropy; NaN is no alternative. */
+ * Masked tokens are those whose z is -inf, as that of a logit -inf, or of one
+ * whose product with scale leaves fp32's range (the type's lowest value at a
+ * scale above 1): they have probability 0 and are not alternatives (places
+ * left over hold id -1 and -inf).  A row masked entirely gives lse and
+ * logprob -inf, entropy 0.  A z that is NaN or +inf gives NaN in its row's
+ * lse, logprob, entropy and alternatives' log probabilities; NaN is no
+ * alternative. */
 rar_result_t rar_logprobs(const void* const* logits, const int64_t* widths,
                           const int64_t* strides, int nranks, int64_t rows, rar_dtype_t dtype,
                           float scale, const int64_t* ids, int ntop, float* logprob,

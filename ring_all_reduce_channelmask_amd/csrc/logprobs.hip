@@ -5,7 +5,8 @@
 //   z = scale * x,  lse = log sum_j e^{z_j},  logprob = z_id - lse,
 //   entropy = lse - sum_j p_j z_j,  p_j = e^{z_j - lse}
 //   dx_j = scale * (g [j == id] + p_j (l - g - h (log p_j + entropy)))
-// for the gradients g, h, l of logprob, entropy and lse.
+// for the gradients g, h, l of logprob, entropy and lse.  A z that rounds to
+// -inf is a masked token's, in every output and in the gradient.
 //
 // Forward: one pass over the logits.  With m a running maximum (in units of
 // log 2: M = m * scale * log2 e) and d_j = x_j * scale * log2 e - M, a thread
@@ -31,6 +32,7 @@
 #include "op_common.h"
 
 #include <cmath>
+#include <limits>
 
 namespace rar {
 namespace {
@@ -45,7 +47,6 @@ constexpr int kMaxSplits = 256;
 constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;  // 256 threads each: a grid holds less than 2^32
 constexpr int64_t kMaxRows = int64_t(1) << 23;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kLowest = -3.402823466e+38f;
 
 struct Shards {
   const void* ptr[kMaxRanks];
@@ -59,6 +60,7 @@ struct LogprobsArgs {
   int64_t rows;
   int32_t splits, ntop;
   float scale, scale2;             // scale, scale * log2 e
+  float least;                     // the least logit x with scale * x above -inf
   const int64_t* ids;
   float *logprob, *entropy, *lse;
   int32_t* top_ids;
@@ -217,8 +219,8 @@ __device__ __forceinline__ float wave_kth(float v, int k) {
 // nothing (M's rounding alone passes kFar * 2^-24 = 16, or M overflows), as one
 // whose tokens are all masked by the type's lowest value: the triple again,
 // with z rounded before M is taken off, and M and d in units of 1.  `seen` is
-// the row's triple; one without any finite logit keeps M = -inf.  Every thread
-// of the workgroup calls it.
+// the row's triple; one without any finite z keeps M = -inf.  Every thread of
+// the workgroup calls it.
 constexpr float kFar = 268435456.0f;  // 2^28
 template <class T>
 __device__ __forceinline__ Stat rescan(const Shards& x, int64_t row, float scale, Stat seen, Stat* wave_stat) {
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kWgWaves * kWaveSize) logprobs_kernel(Logprobs
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   Stat st{-INFINITY, 0.0f, 0.0f};
   bool masked = false;  // -inf has been met
-  float cut = kLowest;  // a candidate's least logit
+  float cut = args.least;  // a candidate's least logit
   int held = 0;         // candidates in LDS
   bool sorted = false;  // the best of them are in top.best
   if constexpr (kTop) {
@@ -625,6 +627,16 @@ Cut choose_cut(const Shards& s, int64_t rows, int ntop) {
   }
   return c;
 }
+// The least logit that is not masked.  fp32's own lowest up to scale 1; above,
+// the quotient is within a rounding of it.
+float least_logit(float scale) {
+  constexpr float kLowest = -std::numeric_limits<float>::max();
+  if (scale <= 1.0f) return kLowest;
+  float x = kLowest / scale;
+  while (!(x * scale >= kLowest)) x = std::nextafter(x, 0.0f);
+  for (float y; (y = std::nextafter(x, kLowest)) * scale >= kLowest;) x = y;
+  return x;
+}
 size_t workspace_for(int64_t rows, int splits, int ntop) {
   return splits == 1 ? 0 : (size_t)rows * splits * (16 + 8 * (size_t)ntop);
 }
@@ -695,6 +707,7 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
   a.ntop = ntop;
   a.scale = scale;
   a.scale2 = scale * kLog2e;
+  a.least = least_logit(scale);
   a.ids = ids;
   a.logprob = logprob;
   a.entropy = entropy;
