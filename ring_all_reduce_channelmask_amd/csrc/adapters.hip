@@ -208,6 +208,19 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
   return s;
 }
 
+// A number rounded to the payload type, but a finite one to a finite one: what
+// is left of it, v - high_part(v), is then a number too.
+constexpr float kFinite = 3.402823466e+38f;  // fp32's largest number
+template <class T>
+__device__ __forceinline__ float high_part(float v) {
+  const float r = T::widen1(T::round1(v));
+  if constexpr (T::kVec == 8) {
+    constexpr float kLargest = 3.3895313892515355e+38f;  // bf16's
+    if (fabsf(v) <= kFinite) return fminf(fmaxf(r, -kLargest), kLargest);
+  }
+  return r;
+}
+
 // y of a run of at most kTiles * 16 tokens x 256 columns, a tile of 16 tokens
 // at a time.  The run's h is laid out in LDS first, for bf16 as two bf16
 // numbers whose sum has 16 bits of it.  In the products a wave takes 64
@@ -303,8 +316,9 @@ __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) exp
     float low[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      h[e] = there && q + e < args.rank ? h[e] * scale : 0.0f;
-      low[e] = h[e] - T::widen1(T::round1(h[e]));
+      const float v = there && q + e < args.rank ? h[e] * scale : 0.0f;
+      h[e] = high_part<T>(v);
+      low[e] = fabsf(v) <= kFinite ? v - h[e] : 0.0f;  // nothing beside an infinity: inf - inf is NaN
     }
     store4<T>(reinterpret_cast<bits*>(hs[0][t]) + q, 4, h);
     if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
