@@ -222,11 +222,12 @@ __device__ __forceinline__ float high_part(float v) {
 }
 
 // y of a run of at most kTiles * 16 tokens x 256 columns, a tile of 16 tokens
-// at a time.  The run's h is laid out in LDS first, for bf16 as two bf16
-// numbers whose sum has 16 bits of it.  In the products a wave takes 64
-// columns, which are the MFMA's rows, and the tokens are its columns.  The
-// result passes through LDS, so that the partials and y move in pieces of 256
-// neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
+// at a time.  The run's h is laid out in LDS first, for bf16 as three bf16
+// numbers whose sum is h (4096 x 7168, 4 ranks, both kernels: rank 64, of two
+// numbers and 16 bits 131 us, of three 133; rank 128 189 and 197).  In the
+// products a wave takes 64 columns, which are the MFMA's rows, and the tokens
+// are its columns.  The result passes through LDS, so that the partials and y
+// move in pieces of 256 neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
 // adapter: in the products' own layout, 64 bytes a piece, 150 us; 64 columns a
 // piece 104 us, 256 columns 107 us; 1000 x 5001, whose rows are not aligned: 64
 // columns a piece 41 us, 256 columns 30 us).
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) exp
   const ExpandArgs& args = kernel_args<ExpandArgs>();
   constexpr int kStep = 4 * T::kVec, kVecs = 16 / T::kVec, kBatch = 4;
   constexpr int kRowVecs = 4 * kR + 1;  // of a token's h; one more against bank conflicts
-  constexpr int kForms = T::kVec == 8 ? 2 : 1;
+  constexpr int kForms = T::kVec == 8 ? 3 : 1;
   constexpr int kRowLanes = kRunCols / T::kVec;      // threads that move a token's columns
   constexpr int kRows = kWaveSize * T::kVec / kRunCols > 0 ? kWaveSize * T::kVec / kRunCols : 1;  // tokens a wave's vector covers
   static_assert(kRows * kVecs * kWaves == 16, "four waves move a tile");
@@ -313,15 +314,18 @@ __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) exp
         if (there && q + e < args.rank) h[e] = sum_parts(args.h + token * args.rank + q + e, args.tokens * args.rank, args.parts);
     }
     const float scale = there && args.scales ? args.scales[id] : 1.0f;
-    float low[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = there && q + e < args.rank ? h[e] * scale : 0.0f;
-      h[e] = high_part<T>(v);
-      low[e] = fabsf(v) <= kFinite ? v - h[e] : 0.0f;  // nothing beside an infinity: inf - inf is NaN
+    for (int e = 0; e < 4; ++e) h[e] = there && q + e < args.rank ? h[e] * scale : 0.0f;
+#pragma unroll
+    for (int f = 0; f < kForms; ++f) {
+      float part[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        part[e] = high_part<T>(h[e]);
+        h[e] = fabsf(h[e]) <= kFinite ? h[e] - part[e] : 0.0f;  // nothing beside an infinity: inf - inf is NaN
+      }
+      store4<T>(reinterpret_cast<bits*>(hs[f][t]) + q, 4, part);
     }
-    store4<T>(reinterpret_cast<bits*>(hs[0][t]) + q, 4, h);
-    if constexpr (kForms == 2) store4<T>(reinterpret_cast<bits*>(hs[1][t]) + q, 4, low);
   }
   const int col0 = first + wave * 64;  // of the wave's products
   int held = -1;                       // the adapter whose weights are in registers

@@ -1,5 +1,6 @@
-"""Adapters with infinities: a token's result does not depend on how many
-others are in the call.  Few tokens go one by one, more 16 at a time."""
+"""Adapters: a token's result does not depend on how many others are in the
+call, in its last bits as with infinities.  Few tokens go one by one, more 16
+at a time."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -28,6 +29,19 @@ def _call(dtype, tokens, x, down, up, partials):
     rows = out[2::4].double().cpu()
     assert all(torch.allclose(r, rows[0], rtol=0, atol=0, equal_nan=True) for r in rows)
     return rows[0]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [FEW, MANY])
+def test_all_bits_of_the_inner_sum_arrive(dtype, tokens):
+    """h = 1 + 2^-10 + 2^-20 exactly; the partials take its upper parts away,
+    and the lowest is the result."""
+    low = [2.0 ** -20, 2.0 ** -23]
+    for least in low:
+        down = [[1.0, 1.0, 1.0]] + [[0.0] * 3] * 31
+        up = [[1.0] + [0.0] * 31] * 70
+        y = _call(dtype, tokens, [1.0, 2.0 ** -10, least], down, up, [[-1.0] * 70, [-2.0 ** -10] * 70])
+        assert (y == least).all(), y
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
