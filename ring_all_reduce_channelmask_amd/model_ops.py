@@ -3,8 +3,10 @@
 Binding of the entry points in include/rar.h, which has their definitions:
 dropout and a residual in the one-shot AllReduce, log probabilities over a
 vocabulary split between the ranks, and low-rank adapters beside a
-row-parallel projection.  Tensors are on one device; what a call allocates
-(results, workspace) comes from torch's allocator on the call's stream.
+row-parallel projection.  Tensors are on one device, the current one or
+another; a call runs there, on that device's current stream or the given one
+of its streams.  What it allocates (results, workspace) comes from torch's
+allocator on the call's stream.
 """
 import collections
 import ctypes
@@ -21,18 +23,19 @@ sum of exponentials (all fp32 [rows]) and the most probable tokens (int32 ids
 and fp32 log probabilities, [rows, ntop])."""
 
 _torch = None
-_raw_stream = None
+_raw_stream = _current_device = None
 _DTYPE = {}
 
 
 def _start(ts, what):
     """The list's first tensor, its dtype code and device index."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     if _torch is None:
         import torch
         # the handle without a Stream object around it, where torch has that
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _DTYPE.update({torch.float32: _lib.DTYPE["float32"], torch.bfloat16: _lib.DTYPE["bfloat16"]})
         _torch = torch
     if not isinstance(ts, (list, tuple)) or not ts:
@@ -51,7 +54,19 @@ def _on(dev, stream):
     """The stream handle of a call, and the stream if one was given."""
     if stream is None:
         return _raw_stream(dev), None
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream must be one of cuda:{dev}, as the tensors")
     return stream.cuda_stream, stream
+
+
+def _launch(dev, fn, *args):
+    """Call an entry point, which launches on the current device: that of the
+    stream (a default stream's handle is 0 on every device)."""
+    if _current_device() == dev:
+        _lib.check(fn(*args))
+    else:
+        with _torch.cuda.device(dev):
+            _lib.check(fn(*args))
 
 
 def _new(stream, make):
@@ -137,8 +152,8 @@ def _dropout(fn, ins, outs, extra, p, rng, call, stream):
         extra = extra.data_ptr()
     rng_ptr = _vector(rng, 2, _torch.int64, dev, "rng")
     handle, _ = _on(dev, stream)
-    _lib.check(fn(_pointers(ins), len(ins), _pointers(outs), len(outs), extra, count, dt, p,
-                  rng_ptr, call, handle))
+    _launch(dev, fn, _pointers(ins), len(ins), _pointers(outs), len(outs), extra, count, dt, p,
+            rng_ptr, call, handle)
 
 
 def dropout_allreduce(sends, recvs, p, rng, call=0, residual=None, stream=None):
@@ -185,11 +200,11 @@ def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
     work = None
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=device))
-    _lib.check(_lib.load().rar_logprobs(
-        _pointers(shards), _longs(widths), _longs(strides), n, rows, dt, scale, ids_ptr, ntop,
-        out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
-        out.top_ids.data_ptr(), out.top_logprobs.data_ptr(),
-        work.data_ptr() if need else None, need, handle))
+    _launch(dev, _lib.load().rar_logprobs,
+            _pointers(shards), _longs(widths), _longs(strides), n, rows, dt, scale, ids_ptr, ntop,
+            out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
+            out.top_ids.data_ptr(), out.top_logprobs.data_ptr(),
+            work.data_ptr() if need else None, need, handle)
     return out
 
 
@@ -214,11 +229,11 @@ def logprobs_backward(shards, ids, lse, entropy, grad_logprob, grad_entropy=None
     def vec(t, what):
         return None if t is None else _vector(t, rows, f32, dev, what)
     ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids")
-    _lib.check(_lib.load().rar_logprobs_backward(
-        _pointers(shards), _longs(widths), _longs(strides), len(shards), rows, dt, scale, ids_ptr,
-        vec(lse, "lse"), vec(entropy, "entropy"), vec(grad_logprob, "grad_logprob"),
-        vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads),
-        _longs(gstrides), handle))
+    _launch(dev, _lib.load().rar_logprobs_backward,
+            _pointers(shards), _longs(widths), _longs(strides), len(shards), rows, dt, scale, ids_ptr,
+            vec(lse, "lse"), vec(entropy, "entropy"), vec(grad_logprob, "grad_logprob"),
+            vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads),
+            _longs(gstrides), handle)
     return grads
 
 
@@ -249,9 +264,9 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
     handle, other = _on(dev, stream)
     need = _workspace("rar_adapter_workspace", widths, tokens, dt, rank)
     work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
-    _lib.check(_lib.load().rar_adapter_allreduce(
-        _pointers(xs), _longs(widths), _longs(x_strides), _pointers(partials), _longs(p_strides),
-        n, _pointers(recvs), _longs(r_strides), len(recvs), tokens, outer, dt, _pointers(downs),
-        up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids"),
-        None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
-        work.data_ptr(), need, handle))
+    _launch(dev, _lib.load().rar_adapter_allreduce,
+            _pointers(xs), _longs(widths), _longs(x_strides), _pointers(partials), _longs(p_strides),
+            n, _pointers(recvs), _longs(r_strides), len(recvs), tokens, outer, dt, _pointers(downs),
+            up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids"),
+            None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
+            work.data_ptr(), need, handle)
