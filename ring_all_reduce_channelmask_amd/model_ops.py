@@ -7,6 +7,11 @@ row-parallel projection.  Tensors are on one device, the current one or
 another; a call runs there, on that device's current stream or the given one
 of its streams.  What it allocates (results, workspace) comes from torch's
 allocator on the call's stream.
+
+No call records a gradient: as torch's functions that write into given
+tensors, each refuses tensors that require one while torch records them.
+Inside torch.no_grad() or a torch.autograd.Function it takes them, and the
+*_backward calls compute the gradients.
 """
 import collections
 import ctypes
@@ -48,6 +53,13 @@ def _start(ts, what):
     if dev < 0:
         raise ValueError(f"{what} must be device tensors")
     return like, dt, dev
+
+
+def _unrecorded(what):
+    """Of tensors that require a gradient: an error while torch records them."""
+    if _torch.is_grad_enabled():
+        raise RuntimeError(f"{what}: a gradient is required, which this call would not record; call "
+                           "it under torch.no_grad() or from a torch.autograd.Function")
 
 
 def _on(dev, stream):
@@ -100,6 +112,8 @@ def _rows(ts, rows, dtype, dev, what):
     for t in ts:
         if t.dtype is not dtype or t.get_device() != dev:
             raise ValueError(f"{what} must be on cuda:{dev} with dtype {dtype}")
+        if t.requires_grad:
+            _unrecorded(what)
         shape = t.shape
         if len(shape) != 2 or shape[0] != rows:
             raise ValueError(f"{what} must be [{rows}, width] tensors")
@@ -120,6 +134,8 @@ def _vector(t, n, dtype, dev, what):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or \
             not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{n}] {dtype} tensor on cuda:{dev}")
+    if t.requires_grad:
+        _unrecorded(what)
     return t.data_ptr()
 
 
@@ -131,6 +147,8 @@ def _flat(ts, count, dtype, dev, what):
                 not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous on cuda:{dev}, with {count} elements of "
                              f"{dtype} each")
+        if t.requires_grad:
+            _unrecorded(what)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -197,6 +215,8 @@ def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
             if t.dtype is not d or t.get_device() != dev or tuple(t.shape) != (rows, ntop) or \
                     not t.is_contiguous():
                 raise ValueError(f"the alternatives must be contiguous [{rows}, {ntop}] tensors")
+            if t.requires_grad:
+                _unrecorded("the alternatives")
     work = None
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=device))
@@ -252,6 +272,8 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
     recv_outers, r_strides = _rows(recvs, tokens, dtype, dev, "recvs")
     if up.dim() != 3 or up.dtype is not dtype or up.get_device() != dev or not up.is_contiguous():
         raise ValueError("up must be a contiguous [adapters, outer, rank] tensor like xs")
+    if up.requires_grad:
+        _unrecorded("up")
     adapters, outer, rank = up.shape
     if outers != (outer,) * n or recv_outers != (outer,) * len(recvs):
         raise ValueError(f"partials (one per rank) and recvs must be [{tokens}, {outer}] tensors")
@@ -261,6 +283,8 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
         if t.dtype is not dtype or t.get_device() != dev or t.shape != (adapters, rank, k) or \
                 not t.is_contiguous():
             raise ValueError(f"downs must be contiguous [{adapters}, {rank}, width] tensors like xs")
+        if t.requires_grad:
+            _unrecorded("downs")
     handle, other = _on(dev, stream)
     need = _workspace("rar_adapter_workspace", widths, tokens, dt, rank)
     work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))

@@ -91,7 +91,7 @@ def _calls(dev=1, stream=None, grad=None):
         dresidual=t(("dropout_backward", "dresidual"), 8), stream=stream)
     yield "logprobs", lambda: rar.logprobs([t(("logprobs", "shards"), 2, 5)], whole(2),
                                            out=rar.LogProbs(*[t(("logprobs", "out"), 2) for _ in range(3)],
-                                                            Tensor(2, 0, dtype=torch.int32, dev=dev), t(None, 2, 0)), stream=stream)
+                                                            Tensor(2, 0, dtype=torch.int32, dev=dev), Tensor(2, 0, dev=dev)), stream=stream)
     yield "logprobs_backward", lambda: rar.logprobs_backward(
         [t(("logprobs_backward", "shards"), 2, 5)], whole(2), t(("logprobs_backward", "lse"), 2), t(("logprobs_backward", "entropy"), 2),
         t(("logprobs_backward", "grad_logprob"), 2), t(("logprobs_backward", "grad_entropy"), 2),
@@ -119,3 +119,26 @@ def test_a_given_stream_is_of_the_tensors_device(machine, monkeypatch):
         with pytest.raises(ValueError, match="stream"):
             call()
         assert not machine.launches, name
+
+
+ARGUMENTS = {
+    "dropout": ("sends", "recvs", "residual"),
+    "dropout_backward": ("grads", "dsends", "dresidual"),
+    "logprobs": ("shards", "out"),
+    "logprobs_backward": ("shards", "lse", "entropy", "grad_logprob", "grad_entropy", "grad_lse", "grads"),
+    "adapter": ("xs", "partials", "recvs", "downs", "up", "scales"),
+}
+
+
+@pytest.mark.parametrize("operator,argument", [(k, v) for k, vs in ARGUMENTS.items() for v in vs])
+def test_a_gradient_that_nothing_would_record_is_refused(machine, operator, argument):
+    """As torch does of functions that write into given tensors; where no
+    gradients are recorded, the call goes through."""
+    call = dict(_calls(grad=(operator, argument)))[operator]
+    with pytest.raises(RuntimeError, match="no_grad"):
+        call()
+    assert not machine.launches
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off:
+            call()
+        assert machine.launches.pop()[1] == 1
