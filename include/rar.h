@@ -398,8 +398,8 @@ rar_result_t rar_oneshot_allreduce_premul(const void* const* sendbufs, void* con
  * and RAR_BFLOAT16 (others: RAR_INVALID_ARGUMENT); sums and softmax statistics
  * are kept in fp32 and each result is rounded to its type once.  Outputs must
  * not overlap each other, nor inputs except where "in place" is said.  Strides
- * count elements between rows; a NULL stride array means rows that follow
- * each other.
+ * count elements between rows, at least a row's width and, times the rows, at
+ * most 2^58; a NULL stride array means rows that follow each other.
  */
 
 /* The one-shot AllReduce with dropout and a residual:

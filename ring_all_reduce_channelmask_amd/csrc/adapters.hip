@@ -600,8 +600,7 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
   auto flat = [](const void* p, int64_t bytes, const char* what) { return Block{p, 1, bytes, bytes, what}; };
   for (int r = 0; r < nranks; ++r) {
     s.width[r] = (int32_t)widths[r];
-    s.x_stride[r] = x_strides ? x_strides[r] : widths[r];
-    if (s.x_stride[r] < widths[r]) return argument_error("input row stride of rank", r, "is below its width");
+    if (rar_result_t q = set_stride(s.x_stride[r], x_strides, r, widths[r], tokens, "input row stride of rank")) return q;
     if (widths[r]) {
       if (rar_result_t q = check_pointer(xs[r], es, "input of rank", r)) return q;
       if (rar_result_t q = check_pointer(downs[r], es, "down weights of rank", r)) return q;
@@ -610,17 +609,14 @@ rar_result_t adapter_call(const void* const* xs, const int64_t* widths, const in
     }
     s.x[r] = xs[r];
     s.down[r] = downs[r];
-    e.partial_stride[r] = partial_strides ? partial_strides[r] : outer;
-    if (e.partial_stride[r] < outer) return argument_error("partial row stride of rank", r, "is below its width");
+    if (rar_result_t q = set_stride(e.partial_stride[r], partial_strides, r, outer, tokens, "partial row stride of rank")) return q;
     if (rar_result_t q = check_pointer(partials[r], es, "partial of rank", r)) return q;
     e.partial[r] = partials[r];
     // the thread that writes an element of y has read it of every partial
     reads.push_back({partials[r], tokens, (int64_t)(outer * es), (int64_t)(e.partial_stride[r] * es), "a partial", kAnyOutput});
   }
   for (int k = 0; k < ncopies; ++k) {
-    e.out_stride[k] = out_strides ? out_strides[k] : outer;
-    if (e.out_stride[k] < outer)
-      return argument_error("row stride of output", k, "is below its width");
+    if (rar_result_t q = set_stride(e.out_stride[k], out_strides, k, outer, tokens, "row stride of output")) return q;
     if (rar_result_t q = check_pointer(outs[k], es, "output", k)) return q;
     e.out[k] = outs[k];
     writes.push_back({outs[k], tokens, (int64_t)(outer * es), (int64_t)(e.out_stride[k] * es), "output"});

@@ -586,9 +586,7 @@ rar_result_t fill_shards(Shards& s, const void* const* logits, const int64_t* wi
     vocab += widths[r];
     tiles += (widths[r] + tile - 1) / tile;
     if (vocab > (int64_t(1) << 30)) return set_error(RAR_INVALID_ARGUMENT, "the vocabulary must have at most 2^30 tokens");
-    if (strides && strides[r] < widths[r])
-      return set_error(RAR_INVALID_ARGUMENT, "row stride of rank " + std::to_string(r) + " below its width");
-    s.stride[r] = strides ? strides[r] : widths[r];
+    if (rar_result_t e = set_stride(s.stride[r], strides, r, widths[r], rows, "row stride of rank")) return e;
   }
   if (vocab == 0) return set_error(RAR_INVALID_ARGUMENT, "the vocabulary is empty");
   s.first[nranks] = (int32_t)vocab;
@@ -744,11 +742,9 @@ rar_result_t logprobs_backward_call(const void* const* logits, const int64_t* wi
     // in place over its own logits alone: other ranks' are other workgroups'
     reads.push_back({a.x.ptr[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.x.stride[r] * es), "logits",
                      widths[r] ? (int)writes.size() : kNoOutput});
-    a.grad_stride[r] = grad_strides ? grad_strides[r] : widths[r];
     if (widths[r] == 0) continue;
     if (rar_result_t e = check_pointer(grads[r], es, "gradient of rank", r)) return e;
-    if (a.grad_stride[r] < widths[r])
-      return set_error(RAR_INVALID_ARGUMENT, "gradient row stride of rank " + std::to_string(r) + " below its width");
+    if (rar_result_t e = set_stride(a.grad_stride[r], grad_strides, r, widths[r], rows, "gradient row stride of rank")) return e;
     a.grad[r] = grads[r];
     writes.push_back({grads[r], rows, (int64_t)(widths[r] * es), (int64_t)(a.grad_stride[r] * es), "gradient"});
   }

@@ -75,6 +75,16 @@ inline rar_result_t check_float_dtype(int dtype) {
 inline rar_result_t argument_error(const char* what, int index, const char* why) {
   return set_error(RAR_INVALID_ARGUMENT, what + (index < 0 ? std::string() : " " + std::to_string(index)) + " " + why);
 }
+// Rows `stride` elements apart, of `width` of them: the last row's offset is
+// to stay below 2^60 bytes, beyond any memory and within 64-bit arithmetic.
+// One row has no use for its stride, and gets its width.
+inline rar_result_t set_stride(int64_t& stride, const int64_t* strides, int index, int64_t width, int64_t rows, const char* what) {
+  stride = strides ? strides[index] : width;
+  if (stride < width) return argument_error(what, index, "is below its width");
+  if (rows <= 1) stride = width;
+  else if (stride > (int64_t(1) << 58) / rows) return argument_error(what, index, "is out of range");
+  return RAR_SUCCESS;
+}
 inline rar_result_t check_pointer(const void* p, size_t align, const char* what, int index = -1) {
   if (!p) return argument_error(what, index, "is NULL");
   if (reinterpret_cast<uintptr_t>(p) & (align - 1)) return argument_error(what, index, "is not aligned to its element size");

@@ -1,12 +1,12 @@
 """What the operators around an AllReduce refuse beyond malformed arguments:
-buffers that workgroups would race on.  Every call below fails on the host,
-before any HIP call; the addresses are made up and never dereferenced.  No GPU
-needed."""
+buffers that workgroups would race on, row strides beyond any memory.  Every
+call below fails on the host, before any HIP call; the addresses are made up
+and never dereferenced.  No GPU needed."""
 import pytest
 
 from ring_all_reduce_channelmask_amd import _lib
 
-from .test_model_ops_args import A, BAD, BF16, F32, _backward, _dropout
+from .test_model_ops_args import A, BAD, BF16, F32, _adapters, _backward, _dropout, _logprobs
 
 LOGITS = (A, A + (1 << 20))
 
@@ -46,3 +46,19 @@ def test_the_generators_state_as_an_output(back):
         assert "rng" in _message()
     if back:
         assert _dropout(count=4, res=A + 65536, back=True) == BAD
+
+
+@pytest.mark.parametrize("stride", [1 << 62, 1 << 61, (1 << 63) - 1, 1 << 57])
+def test_row_strides_beyond_any_memory(stride):
+    """Rows so far apart that their offsets in bytes leave 64 bits: refused,
+    whichever operand has them (a multiple of 2^64 bytes divided by zero).  One
+    row has no use for its stride."""
+    far = (stride, stride)
+    one = dict(strides=far, gstrides=far, grads=(A + 64, A + (7 << 20)))  # in part over the logits
+    assert _backward(rows=1, **one) == BAD and "overlaps" in _message()
+    for kw in (dict(strides=far), dict(gstrides=far), one):
+        assert _backward(**kw) == BAD and "stride" in _message(), kw
+    assert _logprobs(strides=far, lp=A + 64) == BAD and "stride" in _message()
+    for kw in (dict(xstrides=far), dict(pstrides=far), dict(ostrides=far[:1])):
+        assert _adapters(**kw) == BAD and "stride" in _message(), kw
+        assert _adapters(tokens=1, outs=(A,), **kw) == BAD and "overlaps" in _message(), kw
