@@ -208,23 +208,32 @@ __device__ __forceinline__ float sum_parts(const float* h, int64_t stride, int p
   return s;
 }
 
-// A number rounded to the payload type, but a finite one to a finite one: what
-// is left of it, v - high_part(v), is then a number too.
-constexpr float kFinite = 3.402823466e+38f;  // fp32's largest number
-template <class T>
-__device__ __forceinline__ float high_part(float v) {
-  const float r = T::widen1(T::round1(v));
-  if constexpr (T::kVec == 8) {
-    constexpr float kLargest = 3.3895313892515355e+38f;  // bf16's
-    if (fabsf(v) <= kFinite) return fminf(fmaxf(r, -kLargest), kLargest);
+// A number as the sum of n of the payload type: fp32 itself, or three of bf16,
+// each the leading 8 bits of what is left (toward zero: a finite number's are
+// finite).  They have the number's sign, and are not 0 unless it is, or is
+// below 2^-93 (2^-40 of it in the place of nothing left): so an infinite
+// weight's products with them add up to an infinity, where one with 0 would
+// give NaN.
+template <class T, int n>
+__device__ __forceinline__ void split(float v, float* part) {
+  part[0] = v;
+  if constexpr (n > 1) {
+    const float least = v * 0x1p-40f;  // of an infinity: itself
+    part[0] = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+    float left = fabsf(v) <= 3.402823466e+38f ? v - part[0] : 0.0f;  // fp32's largest
+#pragma unroll
+    for (int f = 1; f < n; ++f) {
+      const float head = __uint_as_float(__float_as_uint(left) & 0xFFFF0000u);
+      left -= head;
+      part[f] = head != 0.0f ? head : least;
+    }
   }
-  return r;
 }
 
 // y of a run of at most kTiles * 16 tokens x 256 columns, a tile of 16 tokens
 // at a time.  The run's h is laid out in LDS first, for bf16 as three bf16
 // numbers whose sum is h (4096 x 7168, 4 ranks, both kernels: rank 64, of two
-// numbers and 16 bits 131 us, of three 133; rank 128 189 and 197).  In the
+// numbers and 16 bits 131 us, of three 132; rank 128 189 and 193).  In the
 // products a wave takes 64 columns, which are the MFMA's rows, and the tokens
 // are its columns.  The result passes through LDS, so that the partials and y
 // move in pieces of 256 neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
@@ -316,15 +325,13 @@ __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) exp
     const float scale = there && args.scales ? args.scales[id] : 1.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = there && q + e < args.rank ? h[e] * scale : 0.0f;
+    float part[4][kForms];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split<T, kForms>(h[e], part[e]);
 #pragma unroll
     for (int f = 0; f < kForms; ++f) {
-      float part[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        part[e] = high_part<T>(h[e]);
-        h[e] = fabsf(h[e]) <= kFinite ? h[e] - part[e] : 0.0f;  // nothing beside an infinity: inf - inf is NaN
-      }
-      store4<T>(reinterpret_cast<bits*>(hs[f][t]) + q, 4, part);
+      const float row[4] = {part[0][f], part[1][f], part[2][f], part[3][f]};
+      store4<T>(reinterpret_cast<bits*>(hs[f][t]) + q, 4, row);
     }
   }
   const int col0 = first + wave * 64;  // of the wave's products

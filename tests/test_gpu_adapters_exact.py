@@ -76,3 +76,24 @@ def test_an_inner_sum_between_the_largest_numbers(dtype, tokens, sign):
     if dtype == "bfloat16":
         want = 2.0 ** 118  # rounded to 8 bits
     assert (y == sign * want).all(), y
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [FEW, MANY])
+@pytest.mark.parametrize("h", [1.0, 1.0 - 2.0 ** -12, -3.0 - 2.0 ** -9, 0.0])
+def test_infinite_weights_of_the_second_matrix(dtype, tokens, h):
+    """An output with an infinite weight is infinite with the sign of its
+    product; NaN where the inner sum is 0 or where two such products differ."""
+    inf = float("inf")
+    up = [[1.0] * 32 for _ in range(70)]
+    up[3][0], up[4][31], up[69][9] = inf, -inf, inf
+    up[64][2], up[64][3] = inf, -inf
+    up[65][2] = float("nan")
+    first = round(h)
+    down = [[float(first), h - first]] * 32
+    y = _call(dtype, tokens, [1.0, 1.0], down, up, [[1.0] * 70])
+    for c, sign in ((3, 1), (4, -1), (69, 1)):
+        assert y[c].isnan() if h == 0 else y[c] == sign * (inf if h > 0 else -inf), c
+    assert y[64].isnan() and y[65].isnan()
+    rest = [c for c in range(70) if c not in (3, 4, 64, 65, 69)]
+    assert (y[rest] - (1 + 32 * h)).abs().max() <= abs(1 + 32 * h) * 2.0 ** -8
