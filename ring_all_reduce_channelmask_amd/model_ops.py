@@ -5,11 +5,12 @@ dropout and a residual in the one-shot AllReduce, log probabilities over a
 vocabulary split between the ranks, and low-rank adapters beside a
 row-parallel projection.  Tensors are on one device, the current one or
 another; a call runs there, on that device's current stream or the given one
-of its streams.  What it allocates (results, workspace) comes from torch's
-allocator on the call's stream.
+of its streams, with that device current: a launch goes to the current device,
+and the default stream's handle is the same on all.  What it allocates
+(results, workspace) comes from torch's allocator on the call's stream.
 
 No call records a gradient: as torch's functions that write into given
-tensors, each refuses tensors that require one while torch records them.
+tensors, each refuses inputs that require one while torch records them.
 Inside torch.no_grad() or a torch.autograd.Function it takes them, and the
 *_backward calls compute the gradients.
 """
@@ -56,7 +57,7 @@ def _start(ts, what):
 
 
 def _unrecorded(what):
-    """Of tensors that require a gradient: an error while torch records them."""
+    """Of inputs that require a gradient: an error while torch records them."""
     if _torch.is_grad_enabled():
         raise RuntimeError(f"{what}: a gradient is required, which this call would not record; call "
                            "it under torch.no_grad() or from a torch.autograd.Function")
@@ -69,16 +70,6 @@ def _on(dev, stream):
     if getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"stream must be one of cuda:{dev}, as the tensors")
     return stream.cuda_stream, stream
-
-
-def _launch(dev, fn, *args):
-    """Call an entry point, which launches on the current device: that of the
-    stream (a default stream's handle is 0 on every device)."""
-    if _current_device() == dev:
-        _lib.check(fn(*args))
-    else:
-        with _torch.cuda.device(dev):
-            _lib.check(fn(*args))
 
 
 def _new(stream, make):
@@ -104,7 +95,7 @@ def _longs(values):
     return (ctypes.c_int64 * len(values))(*values)
 
 
-def _rows(ts, rows, dtype, dev, what):
+def _rows(ts, rows, dtype, dev, what, read=True):
     """Widths and row strides (tuples) of [rows, width] tensors with unit column stride."""
     if not isinstance(ts, (list, tuple)) or not ts:
         raise ValueError(f"{what} must be a list of tensors")
@@ -112,7 +103,7 @@ def _rows(ts, rows, dtype, dev, what):
     for t in ts:
         if t.dtype is not dtype or t.get_device() != dev:
             raise ValueError(f"{what} must be on cuda:{dev} with dtype {dtype}")
-        if t.requires_grad:
+        if read and t.requires_grad:
             _unrecorded(what)
         shape = t.shape
         if len(shape) != 2 or shape[0] != rows:
@@ -130,16 +121,16 @@ def _rows(ts, rows, dtype, dev, what):
     return tuple(widths), tuple(strides)
 
 
-def _vector(t, n, dtype, dev, what):
+def _vector(t, n, dtype, dev, what, read=True):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (n,) or \
             not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous [{n}] {dtype} tensor on cuda:{dev}")
-    if t.requires_grad:
+    if read and t.requires_grad:
         _unrecorded(what)
     return t.data_ptr()
 
 
-def _flat(ts, count, dtype, dev, what):
+def _flat(ts, count, dtype, dev, what, read=True):
     if not isinstance(ts, (list, tuple)) or not ts:
         raise ValueError(f"{what} must be a list of tensors")
     for t in ts:
@@ -147,7 +138,7 @@ def _flat(ts, count, dtype, dev, what):
                 not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous on cuda:{dev}, with {count} elements of "
                              f"{dtype} each")
-        if t.requires_grad:
+        if read and t.requires_grad:
             _unrecorded(what)
 
 
@@ -160,18 +151,21 @@ def _workspace(entry, *shape):
     return need.value
 
 
-def _dropout(fn, ins, outs, extra, p, rng, call, stream):
+def _dropout(fn, ins, outs, extra, extra_read, p, rng, call, stream):
     like, dt, dev = _start(ins, "the inputs")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return _dropout(fn, ins, outs, extra, extra_read, p, rng, call, stream)
     dtype, count = like.dtype, like.numel()
     _flat(ins, count, dtype, dev, "the inputs")
-    _flat(outs, count, dtype, dev, "the outputs")
+    _flat(outs, count, dtype, dev, "the outputs", False)
     if extra is not None:
-        _flat((extra,), count, dtype, dev, "the residual or its gradient")
+        _flat((extra,), count, dtype, dev, "the residual or its gradient", extra_read)
         extra = extra.data_ptr()
-    rng_ptr = _vector(rng, 2, _torch.int64, dev, "rng")
+    rng_ptr = _vector(rng, 2, _torch.int64, dev, "rng", False)
     handle, _ = _on(dev, stream)
-    _launch(dev, fn, _pointers(ins), len(ins), _pointers(outs), len(outs), extra, count, dt, p,
-            rng_ptr, call, handle)
+    _lib.check(fn(_pointers(ins), len(ins), _pointers(outs), len(outs), extra, count, dt, p,
+                  rng_ptr, call, handle))
 
 
 def dropout_allreduce(sends, recvs, p, rng, call=0, residual=None, stream=None):
@@ -180,14 +174,15 @@ def dropout_allreduce(sends, recvs, p, rng, call=0, residual=None, stream=None):
     ``rng`` is an int64 tensor [seed, offset] on the device; ``call`` is added
     to the offset.  The mask is drawn from them, never stored.  An output may
     be one of the inputs or the residual."""
-    _dropout(_lib.load().rar_dropout_allreduce, sends, recvs, residual, p, rng, call, stream)
+    _dropout(_lib.load().rar_dropout_allreduce, sends, recvs, residual, True, p, rng, call,
+             stream)
 
 
 def dropout_allreduce_backward(grads, dsends, p, rng, call=0, dresidual=None, stream=None):
     """The gradient of dropout_allreduce from the gradients of its copies:
     ``dresidual = sum of grads``, ``dsends[r] = dropout(sum of grads)``."""
-    _dropout(_lib.load().rar_dropout_allreduce_backward, grads, dsends, dresidual, p, rng, call,
-             stream)
+    _dropout(_lib.load().rar_dropout_allreduce_backward, grads, dsends, dresidual, False, p, rng,
+             call, stream)
 
 
 def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
@@ -196,10 +191,13 @@ def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
     vocabulary in rank order), with the entropy and the ``ntop`` most probable
     tokens.  Returns a LogProbs, written into ``out`` if one is given."""
     like, dt, dev = _start(shards, "shards")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return logprobs(shards, ids, ntop, scale, out, stream)
     dtype, rows, n = like.dtype, like.size(0), len(shards)
     widths, strides = _rows(shards, rows, dtype, dev, "shards")
     handle, other = _on(dev, stream)
-    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids")
+    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids", False)
     need = _workspace("rar_logprobs_workspace", widths, rows, dt, ntop)
     f32, i32, device = _torch.float32, _torch.int32, like.device
     if out is None:
@@ -210,21 +208,19 @@ def logprobs(shards, ids, ntop=0, scale=1.0, out=None, stream=None):
         out = _new(other, make)
     else:
         for t, what in zip(out[:3], ("logprob", "entropy", "lse")):
-            _vector(t, rows, f32, dev, what)
+            _vector(t, rows, f32, dev, what, False)
         for t, d in ((out.top_ids, i32), (out.top_logprobs, f32)):
             if t.dtype is not d or t.get_device() != dev or tuple(t.shape) != (rows, ntop) or \
                     not t.is_contiguous():
                 raise ValueError(f"the alternatives must be contiguous [{rows}, {ntop}] tensors")
-            if t.requires_grad:
-                _unrecorded("the alternatives")
     work = None
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=device))
-    _launch(dev, _lib.load().rar_logprobs,
-            _pointers(shards), _longs(widths), _longs(strides), n, rows, dt, scale, ids_ptr, ntop,
-            out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
-            out.top_ids.data_ptr(), out.top_logprobs.data_ptr(),
-            work.data_ptr() if need else None, need, handle)
+    _lib.check(_lib.load().rar_logprobs(
+        _pointers(shards), _longs(widths), _longs(strides), n, rows, dt, scale, ids_ptr, ntop,
+        out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
+        out.top_ids.data_ptr(), out.top_logprobs.data_ptr(),
+        work.data_ptr() if need else None, need, handle))
     return out
 
 
@@ -235,25 +231,29 @@ def logprobs_backward(shards, ids, lse, entropy, grad_logprob, grad_entropy=None
     logprobs returned (``entropy`` may be None without ``grad_entropy``).
     Writes into ``grads`` if given, which may be ``shards`` (in place)."""
     like, dt, dev = _start(shards, "shards")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return logprobs_backward(shards, ids, lse, entropy, grad_logprob, grad_entropy,
+                                     grad_lse, scale, grads, stream)
     dtype, rows = like.dtype, like.size(0)
     widths, strides = _rows(shards, rows, dtype, dev, "shards")
     handle, other = _on(dev, stream)
     if grads is None:
         grads = _new(other, lambda: [_torch.empty((rows, k), dtype=dtype, device=like.device)
                                      for k in widths])
-    gwidths, gstrides = _rows(grads, rows, dtype, dev, "grads")
+    gwidths, gstrides = _rows(grads, rows, dtype, dev, "grads", False)
     if gwidths != widths:
         raise ValueError("grads must have the widths of shards")
     f32 = _torch.float32
 
     def vec(t, what):
         return None if t is None else _vector(t, rows, f32, dev, what)
-    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids")
-    _launch(dev, _lib.load().rar_logprobs_backward,
-            _pointers(shards), _longs(widths), _longs(strides), len(shards), rows, dt, scale, ids_ptr,
-            vec(lse, "lse"), vec(entropy, "entropy"), vec(grad_logprob, "grad_logprob"),
-            vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads),
-            _longs(gstrides), handle)
+    ids_ptr = _vector(ids, rows, _torch.int64, dev, "ids", False)
+    _lib.check(_lib.load().rar_logprobs_backward(
+        _pointers(shards), _longs(widths), _longs(strides), len(shards), rows, dt, scale, ids_ptr,
+        vec(lse, "lse"), vec(entropy, "entropy"), vec(grad_logprob, "grad_logprob"),
+        vec(grad_entropy, "grad_entropy"), vec(grad_lse, "grad_lse"), _pointers(grads),
+        _longs(gstrides), handle))
     return grads
 
 
@@ -266,10 +266,13 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
     ``up``: [adapters, outer, rank]; ``scales``: fp32 [adapters].  An output
     may be one of the partials."""
     like, dt, dev = _start(xs, "xs")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return adapter_allreduce(xs, partials, recvs, downs, up, ids, scales, stream)
     dtype, tokens, n = like.dtype, like.size(0), len(xs)
     widths, x_strides = _rows(xs, tokens, dtype, dev, "xs")
     outers, p_strides = _rows(partials, tokens, dtype, dev, "partials")
-    recv_outers, r_strides = _rows(recvs, tokens, dtype, dev, "recvs")
+    recv_outers, r_strides = _rows(recvs, tokens, dtype, dev, "recvs", False)
     if up.dim() != 3 or up.dtype is not dtype or up.get_device() != dev or not up.is_contiguous():
         raise ValueError("up must be a contiguous [adapters, outer, rank] tensor like xs")
     if up.requires_grad:
@@ -288,9 +291,9 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
     handle, other = _on(dev, stream)
     need = _workspace("rar_adapter_workspace", widths, tokens, dt, rank)
     work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
-    _launch(dev, _lib.load().rar_adapter_allreduce,
-            _pointers(xs), _longs(widths), _longs(x_strides), _pointers(partials), _longs(p_strides),
-            n, _pointers(recvs), _longs(r_strides), len(recvs), tokens, outer, dt, _pointers(downs),
-            up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids"),
-            None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
-            work.data_ptr(), need, handle)
+    _lib.check(_lib.load().rar_adapter_allreduce(
+        _pointers(xs), _longs(widths), _longs(x_strides), _pointers(partials), _longs(p_strides),
+        n, _pointers(recvs), _longs(r_strides), len(recvs), tokens, outer, dt, _pointers(downs),
+        up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids", False),
+        None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
+        work.data_ptr(), need, handle))
