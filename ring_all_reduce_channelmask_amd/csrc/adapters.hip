@@ -18,10 +18,12 @@
 // Bound by memory: x, the partials and y move once; 2 * rank flops for each
 // element of x and y are far below the matrix rate.  Measured (kernels, 4
 // ranks, 7168 x 7168, bf16): 4096 tokens of 7 requests, rank 64: shrink 30 us
-// (59 MB of x and 40 MB of weights past the L2), expand 104 us (470 MB, 4.5
-// TB/s; the one-shot AllReduce moves 512 MiB in 88); 104 tokens with 64
-// adapters of rank 16: 10 + 8.5 us; 1 token 4.6 + 5.6 us, the time that two
-// dependent launches and their chains of loads take.
+// (59 MB of x and 40 MB of weights past the L2), expand 108 us (470 MB, 4.4
+// TB/s; the one-shot AllReduce moves 512 MiB in 88); 512 tokens, each with one
+// of 64 adapters of rank 64: 67 + 77 us (183 MB), where a tile of tokens takes
+// one adapter after the other; 104 tokens with 64 adapters of rank 16: 9.8 +
+// 9.2 us; 1 token 4.4 + 5.6 us, the time that two dependent launches and their
+// chains of loads take.  fp32: 4096 tokens 86 + 199 us, 104 tokens 16.8 + 12.2.
 #include "op_common.h"
 
 namespace rar {
@@ -236,13 +238,16 @@ __device__ __forceinline__ void split(float v, float* part) {
 // numbers and 16 bits 131 us, of three 132; rank 128 189 and 193).  In the
 // products a wave takes 64 columns, which are the MFMA's rows, and the tokens
 // are its columns.  The result passes through LDS, so that the partials and y
-// move in pieces of 256 neighbouring columns, four tokens a wave (4096 x 7168, 4 ranks, without any
-// adapter: in the products' own layout, 64 bytes a piece, 150 us; 64 columns a
-// piece 104 us, 256 columns 107 us; 1000 x 5001, whose rows are not aligned: 64
-// columns a piece 41 us, 256 columns 30 us).
+// move in pieces of 256 neighbouring columns, four tokens a wave (4096 x 7168,
+// 4 ranks, without any adapter, when this was chosen: in the products' own
+// layout, 64 bytes a piece, 150 us; 64 columns a piece 104 us, 256 columns 107
+// us, and 93 now; 1000 x 5001, whose rows are not aligned: 64 columns a piece
+// 41 us, 256 columns 30 us).
 // For bf16 ranks up to 32 the registers are held to 128, four workgroups a
-// compute unit (runs of 4 tiles, rank 16: 124 -> 117 us in all).  Larger ranks
-// and fp32 would spill (rank 64: 132 us without the bound, 133 with it).
+// compute unit (both kernels, rank 16: 1000 x 7168 without the bound 42 us,
+// with it 39; 4096 x 7168 111.5 and 110.5, at rank 32 112.2 and 112.7).
+// Larger ranks lose by it (rank 64 132 us without, 133 with it; 48 137 and
+// 141).
 template <class T, int kR, int kTiles>  // kR vectors of each lane group cover the adapter's rank
 __global__ void __launch_bounds__(kThreads, T::kVec == 8 && kR == 1 ? 4 : 1) expand_kernel(ExpandArgs) {
   const ExpandArgs& args = kernel_args<ExpandArgs>();
@@ -558,10 +563,13 @@ Cut cut_call(const int64_t* widths, int nranks, int64_t tokens, int dtype, int r
   // second matrix is read for every token; in tiles, for every adapter of a
   // tile.  7168 x 7168, 4 ranks, by token / in tiles, us:
   //            rank 16, one adapter each, of 4 requests; rank 64, each, of 4
-  //   64 tokens          15 / 37         10 / 14          27 / 36   16 / 18
-  //   128                21 / 42         13 / 14          44 / 44   20 / 19
-  //   512                56 / 67         29 / 24         143 / 131  47 / 30
-  //   1024               92 / 117        45 / 38         255 / 237  80 / 47
+  //   64 tokens          15 / 37         10 / 14          27 / 36   16 / 17
+  //   128                21 / 42         13 / 15          43 / 42   20 / 18
+  //   512                55 / 67         28 / 24         140 / 138  46 / 31
+  //   1024               90 / 118        43 / 38         256 / 238  81 / 48
+  // Which tokens share an adapter is known on the device alone, so the bound
+  // is one for both: where each column pair turns, the worse choice costs less
+  // than a third.
   c.by_token = tokens * rank <= 8192;
   c.m = c.by_token ? 1 : 2;
   c.tiles = (int)std::max<int64_t>(1, (tokens + 16 * c.m - 1) / (16 * c.m));

@@ -15,8 +15,9 @@
 // Bound by memory: (inputs + residual + outputs) * count elements move once.
 // Seven rounds cost 14 products of 32 x 32 bits for 8 elements, which hides
 // behind the loads.  Measured (kernel): 4 ranks of 16M fp32 with a residual
-// 100 us = 6.0 TB/s; 8 ranks of 32M bf16, gradient, 190 us = 5.6 TB/s; 4 ranks
-// of 104 x 7168 bf16 5.3 us; 7168 elements 3.3 us.
+// 100 us = 6.0 TB/s; 8 ranks of 32M bf16, gradient, 195 us = 5.5 TB/s (189 to
+// 198 on other machines); 4 ranks of 104 x 7168 bf16 5.5 us; 7168 elements 3.3
+// us.
 #include "op_common.h"
 
 #include <cmath>
@@ -221,7 +222,8 @@ rar_result_t dropout_call(const void* const* src, int nsrc, void* const* dst, in
   a.cut = (uint32_t)std::nearbyint(p * 65536.0);
   a.factor = a.cut < 65536u ? (float)(65536.0 / (65536.0 - a.cut)) : 0.0f;
   // One pass of a wave each: a new workgroup's loads start while others store
-  // (8 ranks of 32M bf16: 2048 workgroups 206 us, 4096 198, 8192 192, all 190).
+  // (8 ranks of 32M bf16, on one machine: 2048 workgroups 206 us, 4096 198, 8192
+  // 192, all 190).
   const int64_t blocks = std::min<int64_t>(((int64_t)count + 2047) / 2048, 65536);
   return launch_kernel(get_dropout_kernel(dtype, backward), dim3((unsigned)blocks), dim3(256), &a, stream);
 }

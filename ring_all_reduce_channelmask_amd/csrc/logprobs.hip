@@ -13,7 +13,8 @@
 // keeps s = sum 2^{d_j} and u = sum 2^{d_j} d_j, and rescales both by
 // 2^{M - M'} (u also by the shift) when its maximum grows; two such triples
 // join the same way.  Then lse = ln 2 (M + log2 s) and entropy = ln 2
-// (log2 s - u / s).  All of it is fp32.
+// (log2 s - u / s).  All of it is fp32; exp2 and log2 are the vector unit's
+// own, which err by one unit in the last place.
 //
 // The logits are cut into tiles that do not cross ranks, one for a wave at a
 // time; a workgroup takes a run of consecutive tiles of one row.  Where there
@@ -21,14 +22,15 @@
 // and their best tokens in the workspace for a second kernel to join.
 //
 // Bound: in bf16 the vector units and memory alike.  A logit costs 5.5 plain
-// operations and an exp2 at a quarter of their rate, 38 cycles for a wave's 64:
-// 7.8 TB/s on all units at 2.4 GHz.  Measured (kernel): 4096 rows of 131072
-// bf16 without alternatives 167 us = 6.4 TB/s; 104 masked rows of 131075 with
-// 5 alternatives 17.6 us and 5 us for the join; 1 row of 32003 with 20
-// alternatives 9.9 us, of which the alternatives are 4 us (one threshold, one
-// list, one sort of about 25 keys).  The gradient is bound by memory: 4096
-// rows of 131072 bf16 338 us = 6.4 TB/s; 333 rows of 32003 fp32 with an
-// entropy gradient 17.6 us = 4.8 TB/s.
+// operations and an exp2 at a quarter of their rate, 5.5 * 4 + 16 = 38 cycles
+// for a wave's 64: 8.3 TB/s on all 1024 units at 2.4 GHz.  Measured (kernel):
+// 4096 rows of 131072 bf16 without alternatives 171 us = 6.3 TB/s, 2048 rows
+// of fp32 163 us = 6.6; 104 masked rows of 131075 with 5 alternatives 17.7 us
+// (fp32 20.6) and 5 us for the join; 1 row of 32003 with 20 alternatives 10.0
+// us, of which the alternatives are 4 us (one threshold, one list, one sort of
+// about 25 keys).  The gradient is bound by memory: 4096 rows of 131072 bf16
+// 344 us = 6.2 TB/s; 333 rows of 32003 fp32 with an entropy gradient 18.4 us =
+// 4.6 TB/s.
 #include "op_common.h"
 
 #include <cmath>
@@ -57,7 +59,6 @@ struct Shards {
 };
 struct LogprobsArgs {
   Shards x;
-  int64_t rows;
   int32_t splits, ntop;
   float scale, scale2;             // scale, scale * log2 e
   float least;                     // the least logit x with scale * x above -inf
@@ -701,7 +702,6 @@ rar_result_t logprobs_call(const void* const* logits, const int64_t* widths, con
     if (!workspace) return set_error(RAR_INVALID_ARGUMENT, "workspace is NULL");
   }
   if (rar_result_t r = check_blocks(reads, writes)) return r;
-  a.rows = rows;
   a.ntop = ntop;
   a.scale = scale;
   a.scale2 = scale * kLog2e;
