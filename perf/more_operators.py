@@ -139,13 +139,11 @@ def prepare(case, seed):
     s["xs"] = [_randn(g, T, k).to(t) for k in _parts(K, case["ranks"])]
     for x in s["xs"]:  # a few channels far above the others
         x[:, torch.randint(0, x.shape[1], (4,), generator=g, device="cuda")] *= 8
-    s["weights"], scales = [], []
-    for k in _parts(K, case["ranks"]):
-        w = _randn(g, D, k) / K ** 0.5
-        most = w.abs().amax(1)
-        s["weights"].append(torch.round(w * (127 / most)[:, None]).to(torch.int8))
-        scales.append(most / 127)
-    s["w_scales"] = torch.stack(scales)
+    w = _randn(g, D, K) / K ** 0.5
+    most = w.abs().amax(1)
+    w = torch.round(w * (127 / most)[:, None]).to(torch.int8)
+    s["weights"] = [part.contiguous() for part in w.split(_parts(K, case["ranks"]), 1)]
+    s["w_scales"] = most / 127
     s["resid"] = _randn(g, T, D).to(t) if case["residual"] else None
     s["recvs"] = [torch.empty(T, D, dtype=t, device="cuda") for _ in range(case["copies"])]
     return s
@@ -225,11 +223,12 @@ def _plain_norms_backward(s):
 
 def _plain_projection(s):
     y = 0.0
-    for x, w, b in zip(s["xs"], s["weights"], s["w_scales"]):
-        most = x.abs().amax(1, keepdim=True).float()
+    most = torch.stack([x.abs().amax(1, keepdim=True).float() for x in s["xs"]]).amax(0)
+    for x, w in zip(s["xs"], s["weights"]):
         # 64 bits: a value next to the middle of two whole numbers
         q = torch.round(x.double() * 127 / most.double()) if x.dtype == torch.float32 else torch.round(x.float() * 127 / most)
-        y = y + (q.float() @ w.float().T) * (most / 127 * b)
+        y = y + q.float() @ w.float().T
+    y = y * (most / 127 * s["w_scales"])
     if s["resid"] is not None:
         y = s["resid"].float() + y
     y = y.to(s["xs"][0].dtype)
@@ -289,7 +288,7 @@ def work(case):
         moved = 1 + (N + 1) * case["pre"] + (case["post"] or case["groups"] > 0) + C + case["residual"]
         return {"bytes": size * (n * moved + 2 * vectors), "flops": n * (N + 25)}
     T, K, D = case["tokens"], case["inner"], case["outer"]
-    return {"bytes": T * K * size + K * D + 4 * N * D + T * D * size * (C + case["residual"]), "flops": 2 * T * K * D + T * D * N}
+    return {"bytes": T * K * size + K * D + 4 * D + T * D * size * (C + case["residual"]), "flops": 2 * T * K * D}
 
 
 def exact(case, seed):
@@ -344,11 +343,10 @@ def exact(case, seed):
         out["dpartials"] = [got["total"]] * case["copies"]
         return out
     y = torch.zeros(case["tokens"], case["outer"], dtype=torch.float64, device="cuda")
-    for r, x in enumerate(s["xs"]):
-        x = x.double()
-        most = x.abs().max(1)[0]
-        whole = (x * 127 / most[:, None]).round()
-        y += (whole @ s["weights"][r].double().T) * (most / 127)[:, None] * s["w_scales"][r].double()
+    most = torch.cat(s["xs"], 1).double().abs().max(1)[0]
+    for x, w in zip(s["xs"], s["weights"]):
+        y += (x.double() * 127 / most[:, None]).round() @ w.double().T
+    y *= (most / 127)[:, None] * s["w_scales"].double()
     if case["residual"]:
         y += s["resid"].double()
     return [y] * case["copies"]
