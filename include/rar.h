@@ -388,9 +388,10 @@ rar_result_t rar_oneshot_allreduce_premul(const void* const* sendbufs, void* con
 
 /* ---- operators around an AllReduce ------------------------------------------
  *
- * A model split over N virtual ranks reduces over them in three places: after
- * a row-parallel projection, in the residual stream that follows it, and in
- * the loss over a vocabulary split between the ranks.  The entry points below
+ * A model split over N virtual ranks reduces over them where tokens enter it
+ * from a split embedding, after a row-parallel projection, in the residual
+ * stream and the norms that follow it, and in the loss over a vocabulary split
+ * between the ranks.  The entry points below
  * compute those reductions together with what surrounds them.  None needs a
  * communicator or allocates anything; each is stream ordered, can be captured
  * into a HIP graph, checks its arguments on the host before anything is
@@ -511,6 +512,144 @@ rar_result_t rar_adapter_allreduce(const void* const* xs, const int64_t* widths,
                                    void* workspace, size_t workspace_bytes, void* stream);
 rar_result_t rar_adapter_workspace(const int64_t* widths, int nranks, int64_t tokens,
                                    rar_dtype_t dtype, int rank, size_t* bytes);
+
+/* Token embeddings from a table split by vocabulary: rank r holds rows[r] rows
+ * (0 allowed) of the table E, which follow rank r-1's (1 to 2^30 in all), as
+ * the logits of rar_logprobs do:
+ *   recvbufs[k][t] = scale * E[ids[t]]     for every copy k,
+ * zeros where ids[t] is outside the vocabulary (such as -1, padding).  Of the
+ * AllReduce of the split lookup only the owner's row is read.
+ *   tables     nranks (1..64) device pointers, [rows[r]] of width elements.
+ *   ids        [tokens] int64 in device memory; tokens 0..2^24 (0 launches
+ *              nothing), width 1..2^24, scale finite, nrecv 1..64. */
+rar_result_t rar_embedding_allreduce(const void* const* tables, const int64_t* rows,
+                                     const int64_t* table_strides, int nranks, int64_t width,
+                                     rar_dtype_t dtype, const int64_t* ids, int64_t tokens,
+                                     float scale, void* const* recvbufs,
+                                     const int64_t* recv_strides, int nrecv, void* stream);
+
+/* Its gradient from the gradients of the copies (ngrads 1..64):
+ *   dE[v] = scale * sum over t with ids[t] = v of sum over k of grads[k][t],
+ * summed in fp32 in the order of the positions t.  Without `accumulate` every
+ * row of dtables is written, those of tokens that do not occur with zeros
+ * (tokens 0: all); with it (1), the rows of tokens that occur are added to and
+ * no others are read or written.
+ *   dtables    like the tables, of table_dtype: dtype or RAR_FLOAT32.
+ *   workspace  16-byte aligned device memory, rar_embedding_workspace bytes
+ *              (0: NULL allowed). */
+rar_result_t rar_embedding_allreduce_backward(const void* const* grads,
+                                              const int64_t* grad_strides, int ngrads,
+                                              int64_t tokens, int64_t width, rar_dtype_t dtype,
+                                              const int64_t* ids, float scale,
+                                              void* const* dtables, const int64_t* rows,
+                                              const int64_t* dtable_strides, int nranks,
+                                              rar_dtype_t table_dtype, int accumulate,
+                                              void* workspace, size_t workspace_bytes,
+                                              void* stream);
+rar_result_t rar_embedding_workspace(const int64_t* rows, int nranks, int64_t tokens,
+                                     int64_t width, rar_dtype_t dtype, size_t* bytes);
+
+/* The AllReduce of a block's partial products with the norms before and after
+ * the block, its gate and residual scale.  With rms(x) = x / sqrt(mean of
+ * x^2 over the row + eps):
+ *   total     = sum over r of partials[r]
+ *   hidden[k] = residual_scale * residual + gate * (rms(total) * post_weight)
+ *   outs[k]   = rms(hidden) * pre_weight
+ * total is what the gradient needs, hidden the residual stream behind the
+ * block, outs the next block's input.  Each norm is taken of the fp32 values,
+ * before they are rounded.  A row whose mean of x^2 leaves fp32's range
+ * counts it as infinity. */
+typedef struct {
+  int64_t rows, width;      /* 0..2^24 (0 launches nothing forward), 1..32768    */
+  int32_t dtype;            /* rar_dtype_t of every operand                      */
+  float eps;                /* positive and finite                               */
+  float residual_scale;     /* finite                                            */
+  int32_t pad;
+  const void* post_weight;  /* [width]; NULL: no norm of the sum (total itself)  */
+  const void* pre_weight;   /* [width]; needed where there are outs              */
+  const void* gate;         /* [gate_groups] of width elements; NULL for none    */
+  int64_t gate_groups;      /* divides the rows: row i has gate                  */
+                            /* i / (rows / gate_groups); 1: one for all          */
+  int64_t gate_stride;      /* between gates; 0: width                           */
+} rar_norm_t;
+
+/*   partials    nranks (1..64), folded in rank order
+ *   residual    NULL for none
+ *   hidden, outs   nhidden and nouts (0..64, not both 0) copies
+ *   total       NULL if not wanted
+ * A stride of 0 of residual and total means width.  An output may be exactly
+ * a partial or the residual (in place). */
+rar_result_t rar_norm_allreduce(const rar_norm_t* norm, const void* const* partials,
+                                const int64_t* partial_strides, int nranks, const void* residual,
+                                int64_t residual_stride, void* const* hidden,
+                                const int64_t* hidden_strides, int nhidden, void* const* outs,
+                                const int64_t* out_strides, int nouts, void* total,
+                                int64_t total_stride, void* stream);
+
+/* Its gradient for the same norm, from the gradients of every copy of hidden
+ * and of outs (ngrad_hidden, ngrad_outs 0..64, not both 0) and from what the
+ * forward call wrote: hidden (needed with grad_outs) and total (needed with
+ * post_weight or for dgate).
+ *   dpartials   ndpartials (0..64) copies of the partials' gradient, which is
+ *               the same for every rank
+ *   dresidual, dpost_weight, dgate, dpre_weight   NULL if not wanted; sums
+ *               over rows are kept in fp32 and rounded once (rows 0: zeros)
+ * dpartials and dresidual may be exactly an input of [rows, width] (in place).
+ *   workspace   16-byte aligned device memory, rar_norm_workspace bytes. */
+rar_result_t rar_norm_allreduce_backward(const rar_norm_t* norm, const void* const* grad_hidden,
+                                         const int64_t* grad_hidden_strides, int ngrad_hidden,
+                                         const void* const* grad_outs,
+                                         const int64_t* grad_out_strides, int ngrad_outs,
+                                         const void* total, int64_t total_stride,
+                                         const void* hidden, int64_t hidden_stride,
+                                         void* const* dpartials, const int64_t* dpartial_strides,
+                                         int ndpartials, void* dresidual,
+                                         int64_t dresidual_stride, void* dpost_weight,
+                                         void* dgate, int64_t dgate_stride, void* dpre_weight,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+rar_result_t rar_norm_workspace(const rar_norm_t* norm, size_t* bytes);
+
+/* Rows split over the ranks (widths[r] columns each, 0 allowed, 131071 in all)
+ * to 8-bit integers with one scale a row, whatever the split:
+ *   scales[t] = max over r, k of |xs[r][t][k]| / 127
+ *   quantized[r][t][k] = 127 * xs[r][t][k] / that max, to the nearest integer
+ * (ties to even).  A row of zeros has scale 0 and zeros; a row that holds a
+ * NaN or an infinity has scale NaN and zeros.  Serves activations (a scale per
+ * token) and weights (a row and a scale per output channel).
+ *   rows 0..2^24 (0 launches nothing); scales [rows] fp32. */
+rar_result_t rar_quantize_rows(const void* const* xs, const int64_t* widths,
+                               const int64_t* x_strides, int nranks, int64_t rows,
+                               rar_dtype_t dtype, int8_t* const* quantized,
+                               const int64_t* q_strides, float* scales, void* stream);
+
+/* The AllReduce of a row-parallel projection in 8-bit integers: rank r holds
+ * widths[r] columns (0 allowed, 131071 in all) of the tokens and of the
+ * weights, with one scale a token and one a channel for all ranks:
+ *   recvbufs[k][t][d] = residual[t][d] + x_scales[t] * weight_scales[d] *
+ *                       sum over r, i of xs[r][t][i] * weights[r][d][i]
+ * for every copy k.  The sum is one of integers, exact, so the result does not
+ * depend on how the columns are split.
+ *   xs         [tokens] of widths[r] int8     weights  [outer] of widths[r] int8
+ *   x_scales   [tokens] fp32                  weight_scales  [outer] fp32
+ *   residual, recvbufs   [tokens] of outer elements of dtype; residual NULL for
+ *              none, residual_stride 0: outer.  An output may be exactly the
+ *              residual (in place).
+ *   tokens 0..2^24 (0 launches nothing), outer 1..2^24, nranks, nrecv 1..64.
+ *   workspace  16-byte aligned device memory, rar_int8_projection_workspace
+ *              bytes (0: NULL allowed).
+ * It is fastest where rows begin on multiples of 16 bytes. */
+rar_result_t rar_int8_projection_allreduce(const int8_t* const* xs, const int64_t* widths,
+                                           const int64_t* x_strides, const float* x_scales,
+                                           const int8_t* const* weights,
+                                           const int64_t* weight_strides,
+                                           const float* weight_scales, int nranks,
+                                           int64_t tokens, int64_t outer, rar_dtype_t dtype,
+                                           const void* residual, int64_t residual_stride,
+                                           void* const* recvbufs, const int64_t* recv_strides,
+                                           int nrecv, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+rar_result_t rar_int8_projection_workspace(const int64_t* widths, int nranks, int64_t tokens,
+                                           int64_t outer, rar_dtype_t dtype, size_t* bytes);
 
 /* Watchdog status: RAR_ABORTED if a launch on this communicator timed out in
  * a wait, else RAR_SUCCESS.  Does not synchronize; reflects launches the

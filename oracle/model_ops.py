@@ -145,3 +145,156 @@ def adapters(xs, partials, downs, up, ids, scales, dtype):
         bound[t] += s * (np.abs(up[a]) @ off_h)
     bound = bound + np.abs(y) * 4 * U
     return y, bound + (np.abs(y) + bound) * ROUND[dtype]
+
+
+def embedding(table, ids, scale, dtype):
+    """(y, bound): scale * table[id], zeros for ids outside the table."""
+    scale = float(np.float32(scale))
+    ids = np.asarray(ids)
+    there = (ids >= 0) & (ids < len(table))
+    y = np.where(there[:, None], table[np.where(there, ids, 0)] * scale, 0.0)
+    return y, np.abs(y) * (U + ROUND[dtype] * (1 + U))
+
+
+def embedding_backward(grads, ids, vocab, scale, dtype, old=None):
+    """(gradient [vocab, width], bound) of a table, `old` added to."""
+    scale = float(np.float32(scale))
+    tokens, width = grads[0].shape
+    total, size, count = np.zeros((vocab, width)), np.zeros((vocab, width)), np.zeros(vocab)
+    for t, v in enumerate(ids):
+        if 0 <= v < vocab:
+            count[v] += 1
+            for g in grads:
+                total[v] += g[t]
+                size[v] += np.abs(g[t])
+    # a sum of n terms; the product with scale; the sum with what was there
+    err = abs(scale) * size * ((count[:, None] * len(grads) + 1) * U)
+    y = total * scale
+    if old is not None:
+        y = y + old
+        err = err + np.abs(y) * U
+    err = err + (np.abs(y) + err) * ROUND[dtype]
+    if old is not None:
+        err[count == 0] = 0.0
+    return y, err
+
+
+# A row's sums: up to 32 terms a thread, 64 lanes and 16 waves by halves and in
+# turn, and what each term's own roundings add (3)
+ROW = (32 + 6 + 16 + 3) * U
+
+
+def _rms_parts(x, ex, eps):
+    """1 / sqrt(mean x^2 + eps) of each row of x (known to ex) and its relative error."""
+    squares = (x * x).sum(1, keepdims=True)
+    off = 2 * np.sqrt((ex * ex).sum(1, keepdims=True) / np.where(squares > 0, squares, 1.0))
+    r = 1.0 / np.sqrt(squares / x.shape[1] + eps)
+    return r, 0.5 * (ROW + off) + 4 * U
+
+
+def _rounded(y, err, dtype):
+    return y, err + (np.abs(y) + err) * ROUND[dtype]
+
+
+def _spread(gate, rows):
+    return None if gate is None else np.repeat(gate, rows // len(gate), axis=0)
+
+
+def norms(partials, residual, scale, post, gate, pre, eps, dtype):
+    """{"total", "hidden", "out"}: (values, bound) of the norms around a block."""
+    scale, eps = float(np.float32(scale)), float(np.float32(eps))
+    s, size = partials.sum(0), np.abs(partials).sum(0)
+    es = size * len(partials) * U
+    u, eu = s, es
+    if post is not None:
+        q, eq = _rms_parts(s, es, eps)
+        u = s * q * post
+        eu = np.abs(u) * (eq + 3 * U) + es * np.abs(q * post)
+    g = _spread(gate, len(s))
+    if g is not None:
+        u, eu = u * g, eu * np.abs(g) + np.abs(u * g) * U
+    h, eh = u, eu
+    if residual is not None:
+        h = scale * residual + u
+        eh = eu + (np.abs(scale * residual) + np.abs(h) + eu) * 2 * U
+    out = {"total": _rounded(s, es, dtype), "hidden": _rounded(h, eh, dtype)}
+    if pre is not None:
+        r, er = _rms_parts(h, eh, eps)
+        y = h * r * pre
+        out["out"] = _rounded(y, np.abs(y) * (er + 3 * U) + eh * np.abs(r * pre), dtype)
+    return out
+
+
+def norms_backward(grad_hidden, grad_outs, total, hidden, scale, post, gate, pre, eps, dtype):
+    """{"dpartial", "dresidual", "dpost", "dgate", "dpre"}: (values, bound)."""
+    scale, eps = float(np.float32(scale)), float(np.float32(eps))
+    some = list(grad_hidden) + list(grad_outs)
+    rows, width = some[0].shape
+    column = (rows + 40) * U  # a sum over the rows, in parts
+    d, ed, out = np.zeros((rows, width)), np.zeros((rows, width)), {}
+    for e in grad_hidden:
+        d, ed = d + e, ed + np.abs(e) * len(grad_hidden) * U
+    if len(grad_outs):
+        n = sum(grad_outs)
+        en = sum(np.abs(e) for e in grad_outs) * len(grad_outs) * U
+        h = hidden
+        r, er = _rms_parts(h, np.zeros_like(h), eps)
+        dot = (n * pre * h).sum(1, keepdims=True)
+        edot = (en * np.abs(pre * h)).sum(1, keepdims=True) + ROW * np.abs(n * pre * h).sum(1, keepdims=True)
+        c = dot / width * r * r
+        ec = edot / width * r * r + np.abs(c) * (2 * er + 4 * U)
+        add = r * (n * pre - h * c)
+        size = r * (np.abs(n * pre) + np.abs(h * c))
+        eadd = r * (en * np.abs(pre) + np.abs(h) * ec) + size * (er + 4 * U)
+        term = n * h * r
+        eterm = en * np.abs(h * r) + np.abs(term) * (er + 3 * U)
+        out["dpre"] = _rounded(term.sum(0), eterm.sum(0) + column * np.abs(term).sum(0), dtype)
+        d, ed = d + add, ed + eadd + (np.abs(d) + np.abs(add)) * 2 * U
+    out["dresidual"] = _rounded(scale * d, abs(scale) * (ed + np.abs(d) * U), dtype)
+    g = _spread(gate, rows)
+    v, ev = (d, ed) if g is None else (d * g, ed * np.abs(g) + np.abs(d * g) * U)
+    if post is not None:
+        s = total
+        q, eq = _rms_parts(s, np.zeros_like(s), eps)
+        u, eu = s * q * post, np.abs(s * q * post) * (eq + 3 * U)
+        term = v * s * q
+        eterm = ev * np.abs(s * q) + np.abs(term) * (eq + 3 * U)
+        out["dpost"] = _rounded(term.sum(0), eterm.sum(0) + column * np.abs(term).sum(0), dtype)
+        dot = (v * post * s).sum(1, keepdims=True)
+        edot = (ev * np.abs(post * s)).sum(1, keepdims=True) + ROW * np.abs(v * post * s).sum(1, keepdims=True)
+        c = dot / width * q * q
+        ec = edot / width * q * q + np.abs(c) * (2 * eq + 4 * U)
+        ds = q * (v * post - s * c)
+        eds = q * (ev * np.abs(post) + np.abs(s) * ec) + q * (np.abs(v * post) + np.abs(s * c)) * (eq + 4 * U)
+    else:
+        u, eu = total, 0.0
+        ds, eds = v, ev
+    if gate is not None and u is not None:
+        term = (d * u).reshape(len(gate), -1, width)
+        eterm = (ed * np.abs(u) + np.abs(d) * eu + np.abs(d * u) * 2 * U).reshape(term.shape)
+        out["dgate"] = _rounded(term.sum(1), eterm.sum(1) + column * np.abs(term).sum(1), dtype)
+    out["dpartial"] = _rounded(ds, eds, dtype)
+    return out
+
+
+def quantize_rows(xs):
+    """(list of integers like xs, scales in 64 bits, rows that are not finite):
+    exact, for a quotient of 24-bit numbers that is no tie is further from one
+    than 64 bits round by."""
+    with np.errstate(invalid="ignore"):
+        most = np.max([np.abs(x).max(axis=1) if x.shape[1] else np.zeros(len(x)) for x in xs], axis=0)
+        bad = ~np.isfinite(np.sum([np.abs(x).sum(axis=1) * 0 for x in xs], axis=0) + most * 0)
+        div = np.where(bad | (most == 0), 1.0, most)
+        return [np.where((bad | (most == 0))[:, None], 0.0, np.rint(np.where(np.isfinite(x), x, 0.0) * 127 / div[:, None])) for x in xs], most / 127, bad
+
+
+def int8_projection(xs, x_scales, weights, w_scales, residual, dtype):
+    """(y, bound): the integer sum is exact; it is rounded to fp32 and
+    multiplied twice."""
+    acc = sum(x.astype(float) @ w.astype(float).T for x, w in zip(xs, weights))  # below 2^53: exact
+    y = acc * x_scales[:, None] * w_scales[None, :]
+    err = np.abs(y) * 3 * U
+    if residual is not None:
+        y = y + residual
+        err = err + (np.abs(y) + err) * U
+    return y, err + (np.abs(y) + err) * ROUND[dtype]

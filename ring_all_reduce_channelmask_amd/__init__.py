@@ -16,10 +16,14 @@ import ctypes
 from . import _lib
 from ._lib import RarError  # noqa: F401
 from .model_ops import (LogProbs, adapter_allreduce, dropout_allreduce,  # noqa: F401
-                        dropout_allreduce_backward, logprobs, logprobs_backward)
+                        dropout_allreduce_backward, embedding_allreduce, embedding_allreduce_backward,
+                        int8_projection_allreduce, logprobs, logprobs_backward, norm_allreduce,
+                        norm_allreduce_backward, quantize_rows)
 
 __all__ = ["Comm", "ring_allreduce", "ring_allreduce_noalloc", "oneshot_allreduce", "ring_info", "graph_text", "plan_pieces", "RarError",
-           "dropout_allreduce", "dropout_allreduce_backward", "logprobs", "logprobs_backward", "LogProbs", "adapter_allreduce"]
+           "dropout_allreduce", "dropout_allreduce_backward", "logprobs", "logprobs_backward", "LogProbs", "adapter_allreduce",
+           "embedding_allreduce", "embedding_allreduce_backward", "norm_allreduce", "norm_allreduce_backward", "quantize_rows",
+           "int8_projection_allreduce"]
 
 
 def _dtype_name(t):

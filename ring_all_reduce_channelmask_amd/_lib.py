@@ -39,6 +39,14 @@ class TraceRec(ctypes.Structure):
                 ("recv_step", ctypes.c_uint64), ("waves", ctypes.c_int32), ("pad", ctypes.c_int32)]
 
 
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("pad", ctypes.c_int32), ("post_weight", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_groups", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
+
+
 class Piece(ctypes.Structure):
     _fields_ = [("channel", ctypes.c_int32), ("channel_id", ctypes.c_int32),
                 ("work", ctypes.c_int32), ("pad", ctypes.c_int32),
@@ -104,6 +112,34 @@ SIGNATURES = [
      [_c.c_size_t, _c.c_void_p]),
     ("rar_adapter_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
                                          _c.POINTER(_c.c_size_t)]),
+    ("rar_embedding_allreduce", _c.c_int, [_vpp, _lp, _lp, _c.c_int, _c.c_int64, _c.c_int,
+                                           _c.c_void_p, _c.c_int64, _c.c_float, _vpp, _lp,
+                                           _c.c_int, _c.c_void_p]),
+    ("rar_embedding_allreduce_backward", _c.c_int, [_vpp, _lp, _c.c_int, _c.c_int64, _c.c_int64,
+                                                    _c.c_int, _c.c_void_p, _c.c_float, _vpp, _lp,
+                                                    _lp, _c.c_int, _c.c_int, _c.c_int,
+                                                    _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    ("rar_embedding_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int,
+                                           _c.POINTER(_c.c_size_t)]),
+    ("rar_norm_allreduce", _c.c_int, [_c.POINTER(Norm), _vpp, _lp, _c.c_int, _c.c_void_p,
+                                      _c.c_int64, _vpp, _lp, _c.c_int, _vpp, _lp, _c.c_int,
+                                      _c.c_void_p, _c.c_int64, _c.c_void_p]),
+    ("rar_norm_allreduce_backward", _c.c_int, [_c.POINTER(Norm), _vpp, _lp, _c.c_int, _vpp, _lp,
+                                               _c.c_int, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                               _c.c_int64, _vpp, _lp, _c.c_int, _c.c_void_p,
+                                               _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int64,
+                                               _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                               _c.c_void_p]),
+    ("rar_norm_workspace", _c.c_int, [_c.POINTER(Norm), _c.POINTER(_c.c_size_t)]),
+    ("rar_quantize_rows", _c.c_int, [_vpp, _lp, _lp, _c.c_int, _c.c_int64, _c.c_int, _vpp, _lp,
+                                     _c.c_void_p, _c.c_void_p]),
+    ("rar_int8_projection_allreduce", _c.c_int, [_vpp, _lp, _lp, _c.c_void_p, _vpp, _lp,
+                                                 _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64,
+                                                 _c.c_int, _c.c_void_p, _c.c_int64, _vpp, _lp,
+                                                 _c.c_int, _c.c_void_p, _c.c_size_t,
+                                                 _c.c_void_p]),
+    ("rar_int8_projection_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int,
+                                                 _c.POINTER(_c.c_size_t)]),
     ("rar_comm_get_async_error", _c.c_int, [_c.c_void_p]),
     ("rar_comm_query_state", _c.c_int, [_c.c_void_p, _c.POINTER(_c.c_int64), _c.c_size_t,
                                         _c.POINTER(_c.c_size_t)]),

@@ -3,7 +3,7 @@
 The library holds the ring AllReduce kernel (one translation unit per payload
 type, each instantiating every protocol and reduction operator), the one-shot
 kernel, the operators around an AllReduce (dropout, log probabilities,
-adapters), the host planner and the C ABI declared in ``include/rar.h``.  The
+adapters, embeddings, norms, 8-bit projections), the host planner and the C ABI declared in ``include/rar.h``.  The
 sources compile to objects in parallel and are linked once.  Always compiles
 (the caller decides when).
 """
@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "librar.so")
 SOURCES = ["csrc/ring_kernel_i32.hip", "csrc/ring_kernel_f32.hip", "csrc/ring_kernel_bf16.hip",
            "csrc/oneshot_kernel.hip", "csrc/plan.cpp", "csrc/capi.cpp", "csrc/noalloc.hip",
-           "csrc/dropout.hip", "csrc/logprobs.hip", "csrc/adapters.hip"]
+           "csrc/dropout.hip", "csrc/logprobs.hip", "csrc/adapters.hip", "csrc/embedding.hip",
+           "csrc/norms.hip", "csrc/projection8.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

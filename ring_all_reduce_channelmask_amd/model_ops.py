@@ -2,8 +2,10 @@
 
 Binding of the entry points in include/rar.h, which has their definitions:
 dropout and a residual in the one-shot AllReduce, log probabilities over a
-vocabulary split between the ranks, and low-rank adapters beside a
-row-parallel projection.  Tensors are on one device, the current one or
+vocabulary split between the ranks, low-rank adapters beside a row-parallel
+projection, embeddings from a table split by vocabulary, the norms around a
+block with its gate and residual scale, and row-parallel projections in 8-bit
+integers.  Tensors are on one device, the current one or
 another; a call runs there, on that device's current stream or the given one
 of its streams, with that device current: a launch goes to the current device,
 and the default stream's handle is the same on all.  What it allocates
@@ -21,7 +23,9 @@ import functools
 from . import _lib
 
 __all__ = ["LogProbs", "adapter_allreduce", "dropout_allreduce", "dropout_allreduce_backward",
-           "logprobs", "logprobs_backward"]
+           "embedding_allreduce", "embedding_allreduce_backward", "int8_projection_allreduce",
+           "logprobs", "logprobs_backward", "norm_allreduce", "norm_allreduce_backward",
+           "quantize_rows"]
 
 LogProbs = collections.namedtuple("LogProbs", "logprob entropy lse top_ids top_logprobs")
 LogProbs.__doc__ = """Of each row: the given token's log probability, the entropy, the log of the
@@ -297,3 +301,262 @@ def adapter_allreduce(xs, partials, recvs, downs, up, ids, scales=None, stream=N
         up.data_ptr(), adapters, rank, _vector(ids, tokens, _torch.int64, dev, "ids", False),
         None if scales is None else _vector(scales, adapters, _torch.float32, dev, "scales"),
         work.data_ptr(), need, handle))
+
+
+def _table_rows(ts, width, dtype, dev, what, read=True):
+    """Numbers of rows and row strides (tuples) of [rows, width] tensors with unit column stride."""
+    if not isinstance(ts, (list, tuple)) or not ts:
+        raise ValueError(f"{what} must be a list of tensors")
+    rows, strides = [], []
+    for t in ts:
+        if t.dim() != 2 or t.shape[1] != width:
+            raise ValueError(f"{what} must be [rows, {width}] tensors")
+        rows.append(t.shape[0])
+        if t.shape[0] == 0 and t.dtype is dtype and t.get_device() == dev:
+            strides.append(width)  # a rank without rows: its strides mean nothing
+        else:
+            strides.append(_rows((t,), t.shape[0], dtype, dev, what, read)[1][0])
+    return tuple(rows), tuple(strides)
+
+
+def embedding_allreduce(tables, ids, recvs, scale=1.0, stream=None):
+    """``recvs[k][t] = scale * E[ids[t]]`` for every copy k, the table E split
+    by vocabulary: ``tables`` has a [rows, width] tensor per rank, in rank
+    order.  ``ids``: int64 [tokens]; outside the vocabulary (-1): zeros."""
+    like, dt, dev = _start(tables, "tables")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return embedding_allreduce(tables, ids, recvs, scale, stream)
+    if like.dim() != 2 or ids.dim() != 1:
+        raise ValueError("tables must be [rows, width] tensors and ids a [tokens] one")
+    dtype, width, tokens = like.dtype, like.size(1), ids.size(0)
+    rows, strides = _table_rows(tables, width, dtype, dev, "tables")
+    widths, r_strides = _rows(recvs, tokens, dtype, dev, "recvs", False)
+    if widths != (width,) * len(recvs):
+        raise ValueError(f"recvs must be [{tokens}, {width}] tensors")
+    handle, _ = _on(dev, stream)
+    _lib.check(_lib.load().rar_embedding_allreduce(
+        _pointers(tables), _longs(rows), _longs(strides), len(tables), width, dt,
+        _vector(ids, tokens, _torch.int64, dev, "ids", False), tokens, scale, _pointers(recvs),
+        _longs(r_strides), len(recvs), handle))
+
+
+def embedding_allreduce_backward(grads, ids, dtables, scale=1.0, accumulate=False, stream=None):
+    """The gradient of embedding_allreduce's tables from those of its copies,
+    into ``dtables`` (like the tables, of the gradients' dtype or float32):
+    every row is written, or with ``accumulate`` the rows of tokens that occur
+    are added to.  Equal tokens are summed in fp32, in order."""
+    like, dt, dev = _start(grads, "grads")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return embedding_allreduce_backward(grads, ids, dtables, scale, accumulate, stream)
+    if like.dim() != 2:
+        raise ValueError("grads must be [tokens, width] tensors")
+    dtype, (tokens, width) = like.dtype, like.shape
+    widths, g_strides = _rows(grads, tokens, dtype, dev, "grads")
+    if widths != (width,) * len(grads):
+        raise ValueError(f"grads must be [{tokens}, {width}] tensors")
+    if not isinstance(dtables, (list, tuple)) or not dtables or \
+            dtables[0].dtype not in (dtype, _torch.float32):
+        raise ValueError(f"dtables must be a list of {dtype} or float32 tensors")
+    out_dtype = dtables[0].dtype
+    rows, strides = _table_rows(dtables, width, out_dtype, dev, "dtables", False)
+    handle, other = _on(dev, stream)
+    need = _workspace("rar_embedding_workspace", rows, tokens, width, dt)
+    work = None
+    if need:
+        work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
+    _lib.check(_lib.load().rar_embedding_allreduce_backward(
+        _pointers(grads), _longs(g_strides), len(grads), tokens, width, dt,
+        _vector(ids, tokens, _torch.int64, dev, "ids", False), scale, _pointers(dtables),
+        _longs(rows), _longs(strides), len(dtables), _DTYPE[out_dtype], int(bool(accumulate)),
+        work.data_ptr() if need else None, need, handle))
+
+
+def _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, pre_weight):
+    """The arguments that a norm and its gradient share; the second value
+    keeps a reshaped gate alive."""
+    def weight(t, what):
+        return None if t is None else _vector(t, width, dtype, dev, what)
+    n = _lib.Norm(rows=rows, width=width, dtype=dt, eps=eps, residual_scale=residual_scale,
+                  post_weight=weight(post_weight, "post_weight"),
+                  pre_weight=weight(pre_weight, "pre_weight"))
+    if gate is not None and rows:
+        n.gate, n.gate_groups, n.gate_stride = _gate(gate, width, dtype, dev, "gate")
+    return n
+
+
+def _gate(t, width, dtype, dev, what, read=True):
+    """Address, groups and stride of a [width] or [groups, width] tensor."""
+    if len(t.shape) == 1:
+        return _vector(t, width, dtype, dev, what, read), 1, width
+    if len(t.shape) != 2 or t.shape[1] != width:
+        raise ValueError(f"{what} must be a [{width}] or [groups, {width}] tensor")
+    return t.data_ptr(), t.shape[0], _rows((t,), t.shape[0], dtype, dev, what, read)[1][0]
+
+
+def _copies(ts, rows, width, dtype, dev, what, read):
+    """Addresses, strides and number of [rows, width] tensors (none allowed)."""
+    if not isinstance(ts, (list, tuple)):
+        raise ValueError(f"{what} must be a list of tensors")
+    if not ts:
+        return None, None, 0
+    widths, strides = _rows(ts, rows, dtype, dev, what, read)
+    if widths != (width,) * len(ts):
+        raise ValueError(f"{what} must be [{rows}, {width}] tensors")
+    return _pointers(ts), _longs(strides), len(ts)
+
+
+def _single(t, rows, width, dtype, dev, what, read):
+    """Address and stride of a [rows, width] tensor or None."""
+    if t is None:
+        return None, 0
+    widths, strides = _rows((t,), rows, dtype, dev, what, read)
+    if widths != (width,):
+        raise ValueError(f"{what} must be a [{rows}, {width}] tensor")
+    return t.data_ptr(), strides[0]
+
+
+def norm_allreduce(partials, hidden, outs, residual=None, residual_scale=1.0, post_weight=None,
+                   gate=None, pre_weight=None, eps=1e-6, total=None, stream=None):
+    """The AllReduce of a block's partial products with the norms around the
+    block, with ``rms(x) = x / sqrt(mean(x^2) + eps)`` of each row:
+
+        total     = sum of partials
+        hidden[k] = residual_scale * residual + gate * (rms(total) * post_weight)
+        outs[k]   = rms(hidden) * pre_weight
+
+    All of them [rows, width] tensors; ``hidden`` and ``outs`` lists of copies
+    (one of them may be empty), ``total`` what the gradient needs, if wanted.
+    Without ``post_weight`` the sum is not normed.  ``gate``: a [width] vector,
+    or [groups, width], where the rows are as many equal runs.  An output may
+    be one of the partials or the residual."""
+    like, dt, dev = _start(partials, "partials")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return norm_allreduce(partials, hidden, outs, residual, residual_scale, post_weight,
+                                  gate, pre_weight, eps, total, stream)
+    if len(like.shape) != 2:
+        raise ValueError("partials must be [rows, width] tensors")
+    dtype, (rows, width) = like.dtype, like.shape
+    n = _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, pre_weight)
+    handle, _ = _on(dev, stream)
+    _lib.check(_lib.load().rar_norm_allreduce(
+        ctypes.byref(n), *_copies(partials, rows, width, dtype, dev, "partials", True),
+        *_single(residual, rows, width, dtype, dev, "residual", True),
+        *_copies(hidden, rows, width, dtype, dev, "hidden", False),
+        *_copies(outs, rows, width, dtype, dev, "outs", False),
+        *_single(total, rows, width, dtype, dev, "total", False), handle))
+
+
+def norm_allreduce_backward(grad_hidden, grad_outs, dpartials, total=None, hidden=None,
+                            residual_scale=1.0, post_weight=None, gate=None, pre_weight=None,
+                            eps=1e-6, dresidual=None, dpost_weight=None, dgate=None,
+                            dpre_weight=None, stream=None):
+    """The gradient of norm_allreduce from those of the copies of hidden and of
+    outs (lists; one may be empty) and from its ``total`` (needed with a
+    ``post_weight`` or for ``dgate``) and ``hidden`` (needed with
+    ``grad_outs``).  Writes the partials' gradient, the same for every rank,
+    into each tensor of ``dpartials``, and those of the residual, the weights
+    and the gate where they are given."""
+    given = list(grad_hidden) + list(grad_outs)
+    like, dt, dev = _start(given, "grad_hidden and grad_outs")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return norm_allreduce_backward(grad_hidden, grad_outs, dpartials, total, hidden,
+                                           residual_scale, post_weight, gate, pre_weight, eps,
+                                           dresidual, dpost_weight, dgate, dpre_weight, stream)
+    if len(like.shape) != 2:
+        raise ValueError("gradients must be [rows, width] tensors")
+    dtype, (rows, width) = like.dtype, like.shape
+    n = _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, pre_weight)
+
+    def vector(t, what):
+        return None if t is None else _vector(t, width, dtype, dev, what, False)
+    dgate_ptr, dgate_stride = None, 0
+    if dgate is not None:
+        if gate is None or dgate.shape != gate.shape:
+            raise ValueError("dgate must have the shape of gate")
+        if rows:
+            dgate_ptr, _, dgate_stride = _gate(dgate, width, dtype, dev, "dgate", False)
+        else:
+            dgate.zero_()
+    handle, other = _on(dev, stream)
+    lib, need = _lib.load(), ctypes.c_size_t()
+    _lib.check(lib.rar_norm_workspace(ctypes.byref(n), ctypes.byref(need)))
+    need = need.value
+    work = None
+    if need:
+        work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
+    _lib.check(lib.rar_norm_allreduce_backward(
+        ctypes.byref(n), *_copies(grad_hidden, rows, width, dtype, dev, "grad_hidden", True),
+        *_copies(grad_outs, rows, width, dtype, dev, "grad_outs", True),
+        *_single(total, rows, width, dtype, dev, "total", True),
+        *_single(hidden, rows, width, dtype, dev, "hidden", True),
+        *_copies(dpartials, rows, width, dtype, dev, "dpartials", False),
+        *_single(dresidual, rows, width, dtype, dev, "dresidual", False),
+        vector(dpost_weight, "dpost_weight"), dgate_ptr, dgate_stride,
+        vector(dpre_weight, "dpre_weight"), work.data_ptr() if need else None, need, handle))
+
+
+def quantize_rows(xs, quantized=None, scales=None, stream=None):
+    """Rows split over the ranks (``xs``: a [rows, width] tensor per rank) to
+    8-bit integers with one scale a row for all ranks, the largest magnitude /
+    127: returns (int8 tensors like xs, fp32 scales [rows]), written into those
+    given.  New tensors have rows that begin on multiples of 16 bytes."""
+    like, dt, dev = _start(xs, "xs")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return quantize_rows(xs, quantized, scales, stream)
+    dtype, rows = like.dtype, like.size(0)
+    widths, strides = _rows(xs, rows, dtype, dev, "xs")
+    handle, other = _on(dev, stream)
+    int8, f32, device = _torch.int8, _torch.float32, like.device
+    if quantized is None:
+        quantized = _new(other, lambda: [_torch.empty((rows, (k + 15) // 16 * 16), dtype=int8, device=device)[:, :k]
+                                         for k in widths])
+    if scales is None:
+        scales = _new(other, lambda: _torch.empty(rows, dtype=f32, device=device))
+    q_widths, q_strides = _rows(quantized, rows, int8, dev, "quantized", False)
+    if q_widths != widths:
+        raise ValueError("quantized must have the widths of xs")
+    _lib.check(_lib.load().rar_quantize_rows(
+        _pointers(xs), _longs(widths), _longs(strides), len(xs), rows, dt, _pointers(quantized),
+        _longs(q_strides), _vector(scales, rows, f32, dev, "scales", False), handle))
+    return quantized, scales
+
+
+def int8_projection_allreduce(xs, x_scales, weights, weight_scales, recvs, residual=None,
+                              stream=None):
+    """``recvs[k][t, d] = residual[t, d] + x_scales[t] * weight_scales[d] *
+    sum_r xs[r][t] . weights[r][d]`` for every copy k, the sum in exact integers.
+
+    ``xs``: an int8 [tokens, width] tensor per rank, ``weights``: an int8
+    [outer, width] one, as quantize_rows gives them; the scales fp32 [tokens]
+    and [outer].  ``recvs`` and ``residual`` are float32 or bfloat16; an output
+    may be the residual."""
+    like, dt, dev = _start(recvs, "recvs")
+    if _current_device() != dev:
+        with _torch.cuda.device(dev):
+            return int8_projection_allreduce(xs, x_scales, weights, weight_scales, recvs, residual,
+                                             stream)
+    if len(like.shape) != 2:
+        raise ValueError("recvs must be [tokens, outer] tensors")
+    dtype, (tokens, outer) = like.dtype, like.shape
+    int8, f32 = _torch.int8, _torch.float32
+    widths, x_strides = _rows(xs, tokens, int8, dev, "xs", False)
+    w_widths, w_strides = _rows(weights, outer, int8, dev, "weights", False)
+    if w_widths != widths:
+        raise ValueError("weights must have the widths of xs")
+    recv_ptrs, r_strides, copies = _copies(recvs, tokens, outer, dtype, dev, "recvs", False)
+    res, res_stride = _single(residual, tokens, outer, dtype, dev, "residual", True)
+    handle, other = _on(dev, stream)
+    need = _workspace("rar_int8_projection_workspace", widths, tokens, outer, dt)
+    work = None
+    if need:
+        work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
+    _lib.check(_lib.load().rar_int8_projection_allreduce(
+        _pointers(xs), _longs(widths), _longs(x_strides),
+        _vector(x_scales, tokens, f32, dev, "x_scales"), _pointers(weights), _longs(w_strides),
+        _vector(weight_scales, outer, f32, dev, "weight_scales"), len(xs), tokens, outer, dt, res,
+        res_stride, recv_ptrs, r_strides, copies, work.data_ptr() if need else None, need, handle))

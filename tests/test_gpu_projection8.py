@@ -1,0 +1,281 @@
+"""Row-parallel projections in 8-bit integers and the quantisation of rows,
+against the definition."""
+import numpy as np
+import pytest
+
+from oracle import model_ops
+
+from .test_gpu_embedding import _tensor
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ["float32", "bfloat16"]
+
+
+def _bytes(a, pad=0, skip=0):
+    """An int8 device tensor, its rows widened by pad bytes of 85 and starting
+    skip bytes into the buffer."""
+    import torch
+    t = torch.from_numpy(np.asarray(a)).to(torch.int8)
+    if pad or skip:
+        held = torch.full((t.shape[0] * (t.shape[1] + pad) + skip,), 85, dtype=torch.int8, device="cuda")
+        view = held[skip:].view(t.shape[0], t.shape[1] + pad)[:, :t.shape[1]]
+        view.copy_(t)
+        return view
+    return t.cuda()
+
+
+# ---- quantisation ----
+
+QUANT = [
+    ([1], 1), ([7], 3), ([0, 5], 2), ([64, 64], 9), ([2049], 4), ([1792] * 4, 3), ([1667] * 3, 5), ([9000], 3), ([33] * 64, 2), ([3001, 0, 8000], 2),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("widths,rows", QUANT, ids=[f"n{len(c[0])}-k{sum(c[0])}-r{c[1]}" for c in QUANT])
+def test_quantize(dtype, widths, rows):
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    r = np.random.default_rng(sum(widths))
+    for pad, skip in ((0, 0), (3, 1)):
+        xs = [_tensor(r.standard_normal((rows, w)) * np.exp(r.standard_normal((rows, 1)) * 5), dtype, pad, skip) for w in widths]
+        outs = [_bytes(np.full((rows, w), 99), pad, skip) for w in widths] if pad else None
+        q, scales = rar.quantize_rows([x[0] for x in xs], quantized=outs)
+        want, want_scales, bad = model_ops.quantize_rows([x[1] for x in xs])
+        assert not bad.any()
+        for g, w in zip(q, want):
+            assert np.array_equal(g.cpu().numpy(), w)
+        assert (np.abs(scales.double().cpu().numpy() - want_scales) <= want_scales * 2.0 ** -24).all()
+        if pad:
+            for g, w in zip(outs, widths):
+                assert (g.as_strided((rows, w + pad), (w + pad, 1))[:-1, w:] == 85).all()
+    assert torch.int8 == q[0].dtype
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_ties_and_extremes(dtype):
+    """Ties go to the even integer; every magnitude that a type has."""
+    import ring_all_reduce_channelmask_amd as rar
+    small = {"float32": 2.0 ** -149, "bfloat16": 2.0 ** -133}[dtype]
+    large = {"float32": 2.0 ** 128 - 2.0 ** 104, "bfloat16": 2.0 ** 128 - 2.0 ** 120}[dtype]
+    rows = []
+    for size in (127.0, 254.0, 127 * 2.0 ** 100, 127 * 2.0 ** -100):  # steps of size / 127
+        rows.append([size] + [size / 127 * (k + 0.5) for k in (-3, -2, -1, 0, 1, 2, 3, 10, 11)])
+    rows.append([large, -large, large / 2, large / 256, small] + [0.0] * 5)
+    rows.append([small, -small, 0.0, -0.0] + [0.0] * 6)
+    rows.append([small * 100, small * 50, small, -small * 99] + [0.0] * 6)
+    rows.append([2.0 ** -60, 2.0 ** -61, -2.0 ** -67, 2.0 ** -68] + [0.0] * 6)
+    rows.append([2.0 ** 101, 2.0 ** 100, -2.0 ** 95, 2.0 ** 94] + [0.0] * 6)
+    rows.append([-3.0] * 10)
+    rows.append([0.0] * 10)
+    x, val = _tensor(np.array(rows), dtype)
+    q, scales = rar.quantize_rows([x])
+    want, want_scales, _ = model_ops.quantize_rows([val])
+    assert np.array_equal(q[0].cpu().numpy(), want[0])
+    # scales below fp32's normal numbers are rounded to its smallest step
+    assert (np.abs(scales.double().cpu().numpy() - want_scales) <= want_scales * 2.0 ** -24 + 2.0 ** -150).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_broken_rows(dtype):
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    r = np.random.default_rng(2)
+    xs = [r.standard_normal((6, 500)), r.standard_normal((6, 9000))]
+    xs[0][1, 3] = np.nan
+    xs[1][2, 8999] = np.inf
+    xs[1][4, 0] = -np.inf
+    xs[0][4, 1] = np.nan
+    dev = [_tensor(x, dtype) for x in xs]
+    q, scales = rar.quantize_rows([d[0] for d in dev])
+    want, want_scales, bad = model_ops.quantize_rows([d[1] for d in dev])
+    assert bad.tolist() == [False, True, True, False, True, False]
+    assert scales.isnan().cpu().tolist() == bad.tolist()
+    for g, w in zip(q, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    weights = [torch.ones((4, w.shape[1]), dtype=torch.int8, device="cuda") for w in want]
+    out = [torch.empty((6, 4), device="cuda")]
+    rar.int8_projection_allreduce(q, scales, weights, torch.ones(4, device="cuda"), out)
+    assert out[0].isnan().all(1).cpu().tolist() == bad.tolist() and torch.isfinite(out[0][[0, 3, 5]]).all()
+
+
+# ---- projection ----
+
+def _case(dtype, tokens, widths, outer, residual=True, pad=0, skip=0, seed=0, full=False):
+    import torch
+    r = np.random.default_rng(seed)
+    xs = [np.full((tokens, w), -128) if full else r.integers(-128, 128, (tokens, w)) for w in widths]
+    ws = [np.full((outer, w), -128) if full else r.integers(-128, 128, (outer, w)) for w in widths]
+    sx, sw = (0.01 + r.random(tokens)).astype(np.float32), (0.01 * r.random(outer)).astype(np.float32)
+    res = _tensor(r.standard_normal((tokens, outer)) * 50, dtype, pad, skip) if residual else (None, None)
+    dev = dict(xs=[_bytes(x, pad, skip) for x in xs], weights=[_bytes(w, pad, skip) for w in ws], x_scales=torch.from_numpy(sx).cuda(),
+               weight_scales=torch.from_numpy(sw).cuda(), residual=res[0])
+    want = model_ops.int8_projection(xs, sx.astype(float), ws, sw.astype(float), res[1], dtype)
+    return dev, want
+
+
+def _run(dev, tokens, outer, dtype, copies=1, recvs=None, pad=0, skip=0, stream=None):
+    import ring_all_reduce_channelmask_amd as rar
+    if recvs is None:
+        recvs = [_tensor(np.full((tokens, outer), np.nan), dtype, pad, skip)[0] for _ in range(copies)]
+    rar.int8_projection_allreduce(dev["xs"], dev["x_scales"], dev["weights"], dev["weight_scales"], recvs, residual=dev["residual"], stream=stream)
+    return recvs
+
+
+def _check(got, want, what=""):
+    y, bound = want
+    off = np.abs(got.double().cpu().numpy() - y) - bound
+    assert (off <= 0).all(), f"{what}: {np.nanmax(off)} over its bound"
+
+
+CASES = [
+    # tokens, widths, outer
+    (1, [1], 1),
+    (1, [0, 3, 0], 5),
+    (1, [64] * 2, 300),
+    (1, [1792] * 4, 515),
+    (2, [100, 28], 128),
+    (5, [15, 16, 17, 1], 33),
+    (15, [129], 64),
+    (16, [512, 512], 256),
+    (17, [1667] * 3, 77),
+    (31, [320], 1000),
+    (33, [63, 65], 129),
+    (64, [128], 128),
+    (65, [1000, 24], 260),
+    (100, [33] * 8, 640),
+    (127, [256, 256], 127),
+    (128, [384], 384),
+    (129, [200, 57], 257),
+    (250, [640, 641], 1100),
+    (300, [2048], 511),
+    (513, [130, 0, 126], 700),
+    (1030, [272, 240], 1290),
+]
+IDS = [f"t{c[0]}-k{sum(c[1])}-o{c[2]}" for c in CASES]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,widths,outer", CASES, ids=IDS)
+def test_projection(dtype, tokens, widths, outer):
+    # rows on multiples of 16 bytes or not; rows that follow each other
+    aligned = {w: (-w) % 16 for w in widths}
+    for k, (pad, skip) in enumerate(((0, 0), (3, 1), (16, 16))):
+        dev, want = _case(dtype, tokens, widths, outer, residual=k != 1, pad=pad, skip=skip, seed=tokens + k)
+        for y in _run(dev, tokens, outer, dtype, copies=1 + k, pad=pad, skip=skip):
+            _check(y, want, f"pad {pad}")
+    dev, want = _case(dtype, tokens, widths, outer, seed=tokens)
+    dev["xs"] = [_bytes(x.cpu().numpy(), aligned[x.shape[1]]) for x in dev["xs"]]
+    dev["weights"] = [_bytes(x.cpu().numpy(), aligned[x.shape[1]]) for x in dev["weights"]]
+    _check(_run(dev, tokens, outer, dtype)[0], want, "aligned")
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 100, 300])
+def test_the_largest_sums(tokens):
+    """131071 products of -128 and -128: the integer sum just fits."""
+    dev, want = _case("float32", tokens, [65536, 65535], 40, residual=False, full=True)
+    _check(_run(dev, tokens, 40, "float32")[0], want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_split_does_not_matter(dtype):
+    """The same columns over 1, 3 and 64 ranks: the same bits."""
+    import torch
+    r = np.random.default_rng(5)
+    for tokens in (1, 40, 300):
+        x, w = r.integers(-127, 128, (tokens, 1024)), r.integers(-127, 128, (200, 1024))
+        first = None
+        for cuts in ([], [100, 641], list(range(16, 1024, 16))):
+            dev = dict(xs=[_bytes(p) for p in np.split(x, cuts, 1)], weights=[_bytes(p) for p in np.split(w, cuts, 1)],
+                       x_scales=torch.full((tokens,), 0.01, device="cuda"), weight_scales=torch.full((200,), 0.02, device="cuda"), residual=None)
+            y = _run(dev, tokens, 200, dtype)[0]
+            first = y if first is None else first
+            assert torch.equal(y, first)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_in_place_over_the_residual(dtype):
+    for tokens in (1, 50, 400):
+        for pad in (0, 3):
+            dev, want = _case(dtype, tokens, [333, 100], 140, pad=pad, skip=pad, seed=tokens)
+            _check(_run(dev, tokens, 140, dtype, recvs=[dev["residual"]])[0], want, f"{tokens} tokens, pad {pad}")
+            if pad and tokens > 1:
+                assert dev["residual"].as_strided((tokens, 140 + pad), (140 + pad, 1))[:-1, 140:].isnan().all()
+
+
+def test_same_bits_streams_and_graph_replays():
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    for tokens in (1, 30, 200, 700):
+        g = torch.Generator(device="cuda").manual_seed(tokens)
+        xs = [torch.randn(tokens, 320, generator=g, device="cuda").bfloat16() for _ in range(2)]
+        weights, wscale = rar.quantize_rows([torch.randn(260, 320, generator=g, device="cuda").bfloat16() for _ in range(2)])
+        a, b = (torch.empty(tokens, 260, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+
+        def both(out, stream=None):
+            q, s = rar.quantize_rows(xs, stream=stream)
+            rar.int8_projection_allreduce(q, s, weights, wscale, [out], stream=stream)
+            return q
+        side = torch.cuda.Stream()
+        keep = both(a, side)
+        side.synchronize()
+        del keep
+        both(b)
+        assert torch.equal(a, b)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both(a)
+        for step in range(3):
+            for x in xs:
+                x.copy_(torch.randn(x.shape, device="cuda"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            both(b)
+            assert torch.equal(a, b), (tokens, step)
+
+
+def test_more_than_2_31_elements_between_rows():
+    """Row offsets beyond 32 bits in every strided operand."""
+    import torch
+    for tokens in (3, 40, 200):
+        dev, want = _case("bfloat16", tokens, [65, 64], 200, seed=tokens)
+        rows = max(tokens, 200)
+        stride = (1 << 32) // rows + 1_000_016
+        held = torch.empty(rows * stride, dtype=torch.int8, device="cuda")
+        column = 0
+
+        def far(t):
+            nonlocal column
+            view = held.as_strided(t.shape, (stride, 1), column)
+            column += (t.shape[1] + 31) // 16 * 16
+            return view.copy_(t)
+        dev["xs"] = [far(t) for t in dev["xs"]]
+        dev["weights"] = [far(t) for t in dev["weights"]]
+        stride2 = (1 << 31) // tokens + 1001
+        held2 = torch.empty(tokens * stride2, dtype=torch.bfloat16, device="cuda")
+        res = held2.as_strided((tokens, 200), (stride2, 1), 0).copy_(dev["residual"])
+        dev["residual"] = res
+        out = held2.as_strided((tokens, 200), (stride2, 1), 201)
+        _check(_run(dev, tokens, 200, "bfloat16", recvs=[out])[0], want, f"{tokens} tokens")
+        del held, held2, res, out, dev
+
+
+def test_no_tokens_and_no_columns():
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    e = torch.empty((0, 8), device="cuda")
+    q, s = rar.quantize_rows([e])
+    assert q[0].shape == (0, 8) and s.shape == (0,)
+    w = torch.ones((4, 8), dtype=torch.int8, device="cuda")
+    rar.int8_projection_allreduce(q, s, [w], torch.ones(4, device="cuda"), [torch.empty((0, 4), device="cuda")])
+    for tokens in (1, 70, 300):
+        none = torch.empty((tokens, 0), dtype=torch.int8, device="cuda")
+        res = torch.randn(tokens, 4, device="cuda")
+        out = torch.empty_like(res)
+        rar.int8_projection_allreduce([none], torch.ones(tokens, device="cuda"), [w[:, :0]], torch.ones(4, device="cuda"), [out], residual=res)
+        assert torch.equal(out, res)
+    q, s = rar.quantize_rows([torch.empty((3, 0), device="cuda")])
+    assert q[0].shape == (3, 0) and not s.any()
