@@ -140,18 +140,30 @@ struct ProjArgs {
   const void* residual;
   int64_t residual_stride;
   int64_t tokens, outer;
-  int32_t nranks, ndst, tiles_n;
+  int32_t nranks, ndst, tiles_m, tiles_n;
+  int32_t steps;  // of kDepth bytes of the inner dimension, each rank's rounded up
 };
 
-// 16 bytes of a row from p on, n (any number) of them there and zeros behind.
+// 16 bytes of a row from p on, n (1 or more) of them there and zeros behind.
+// Fewer than 16 come as two overlapping pieces, neither beyond the n bytes.
 __device__ __forceinline__ v4u load_bytes(const int8_t* p, int n) {
   typedef uint32_t v4u_byte __attribute__((ext_vector_type(4), aligned(1)));
+  typedef uint64_t u64_byte __attribute__((aligned(1)));
+  typedef uint32_t u32_byte __attribute__((aligned(1)));
+  typedef uint16_t u16_byte __attribute__((aligned(1)));
   if (n >= 16) return *reinterpret_cast<const v4u_byte*>(p);
-  v4u r = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 15; ++i)
-    if (i < n) r[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
-  return r;
+  uint64_t lo, hi = 0;
+  if (n >= 8) {
+    lo = *reinterpret_cast<const u64_byte*>(p);
+    if (n > 8) hi = *reinterpret_cast<const u64_byte*>(p + n - 8) >> (8 * (16 - n));
+  } else if (n >= 4) {
+    const uint64_t end = *reinterpret_cast<const u32_byte*>(p + n - 4);
+    lo = *reinterpret_cast<const u32_byte*>(p) | end << (8 * (n - 4));
+  } else {
+    lo = (uint8_t)p[0];
+    if (n >= 2) lo |= (uint64_t)*reinterpret_cast<const u16_byte*>(p + n - 2) << (8 * (n - 2));
+  }
+  return v4u{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 constexpr int kTile = 128;   // tokens and channels of a workgroup
@@ -231,6 +243,156 @@ __global__ void __launch_bounds__(256) tile_kernel(ProjArgs) {
         for (int c = 0; c < args.ndst; ++c) store4<T>(static_cast<typename T::bits*>(args.dst[c]) + m * args.dst_stride[c] + n, left, f);
       }
     }
+  }
+}
+
+// Many tokens: a tile of 256 tokens x 256 channels of a workgroup, whose
+// operands go from memory to LDS without passing through registers, 128 bytes
+// of the inner dimension at a time, while the step before is multiplied.
+constexpr int kBig = 256;
+
+// 16 bytes a lane from p to LDS, to 16 * lane behind `to`.  The caller waits
+// for it (vmcnt) before a barrier.
+__device__ __forceinline__ void to_lds(const int8_t* p, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(p) : "memory", "m0");
+}
+
+template <class T, int kWaves>
+__global__ void __launch_bounds__(64 * kWaves, 1) big_tile_kernel(ProjArgs) {
+  const ProjArgs& args = kernel_args<ProjArgs>();
+  constexpr int kStage = 2 * kBig * kDepth;              // weights, then tokens
+  constexpr int kWaveM = kBig * 2 / kWaves;              // tokens of a wave
+  constexpr int kWaveN = 128;                            // channels of a wave
+  constexpr int kFM = kWaveM / 32, kFN = kWaveN / 32;
+  constexpr int kLoads = kBig * kDepth / 16 / (64 * kWaves);  // 16-byte loads a thread, of each operand
+  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage + 8192];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tile = (int64_t)(blockIdx.x & 7) * ((gridDim.x + 7) / 8) + (blockIdx.x >> 3);
+  if (tile >= (int64_t)args.tiles_m * args.tiles_n) return;
+  const int64_t m0 = tile % args.tiles_m * kBig, n0 = tile / args.tiles_m * kBig;
+  v16i acc[kFN][kFM];
+#pragma unroll
+  for (int i = 0; i < kFN; ++i)
+#pragma unroll
+    for (int j = 0; j < kFM; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0;
+
+  // the next step to load: rank, its inner offset, this lane's rows there
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)lds;
+  const int row0 = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+  int rank = 0, k0 = 0;
+  const int8_t *pw[kLoads], *px[kLoads];
+  auto begin_rank = [&] {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int64_t row = row0 + i * 8 * kWaves;
+      pw[i] = args.w[rank] + std::min(n0 + row, args.outer - 1) * args.w_stride[rank] + chunk * 16;
+      px[i] = args.x[rank] + std::min(m0 + row, args.tokens - 1) * args.x_stride[rank] + chunk * 16;
+    }
+  };
+  auto load_step = [&](int stage) {
+    const int width = args.width[rank], left = width - k0;
+    if (left >= kDepth) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        to_lds(pw[i] + k0, lds0 + stage * kStage + (i * kWaves + wave) * 1024);
+        to_lds(px[i] + k0, lds0 + stage * kStage + kBig * kDepth + (i * kWaves + wave) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        v4u a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+        if (left > chunk * 16) a = load_bytes(pw[i] + k0, left - chunk * 16), b = load_bytes(px[i] + k0, left - chunk * 16);
+        *reinterpret_cast<v4u*>(&lds[stage * kStage + (i * kWaves + wave) * 1024 + lane * 16]) = a;
+        *reinterpret_cast<v4u*>(&lds[stage * kStage + kBig * kDepth + (i * kWaves + wave) * 1024 + lane * 16]) = b;
+      }
+    }
+    k0 += kDepth;
+    if (k0 >= width && rank + 1 < args.nranks) {
+      k0 = 0;
+      ++rank;
+      begin_rank();
+    }
+  };
+  const int wn = (wave & 1) * kWaveN, wm = (wave >> 1) * kWaveM;
+  if (args.steps > 0) {
+    begin_rank();
+    load_step(0);
+  }
+  for (int step = 0; step < args.steps; ++step) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (step + 1 < args.steps) load_step((step + 1) & 1);
+    const int8_t* tw = &lds[(step & 1) * kStage];
+    const int8_t* tx = tw + kBig * kDepth;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      v4i wf[kFN], xf[kFM];
+      // 32 rows apart the swizzle is the same
+      const int r = lane & 31, at = r * kDepth + (((s * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
+#pragma unroll
+      for (int i = 0; i < kFN; ++i) wf[i] = *reinterpret_cast<const v4i*>(&tw[(wn + i * 32) * kDepth + at]);
+#pragma unroll
+      for (int j = 0; j < kFM; ++j) xf[j] = *reinterpret_cast<const v4i*>(&tx[(wm + j * 32) * kDepth + at]);
+#pragma unroll
+      for (int i = 0; i < kFN; ++i)
+#pragma unroll
+        for (int j = 0; j < kFM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  // Out through LDS, 32 tokens x 128 channels of a wave at a time, so that
+  // each row of it is read, completed and written as whole lines.
+  constexpr int kPitch = kWaveN + 4;  // floats: rows start on different banks
+  __syncthreads();
+  float* own = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
+  const int64_t n = n0 + wn + (lane & 15) * 8;
+  const int left = (int)std::max<int64_t>(0, std::min<int64_t>(8, args.outer - n));
+  float ws[8];
+  load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n), left, ws);
+  load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n + 4), left - 4, ws + 4);
+#pragma unroll
+  for (int j = 0; j < kFM; ++j) {
+#pragma unroll
+    for (int i = 0; i < kFN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v4f f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = (float)acc[i][j][4 * q + e];
+        *reinterpret_cast<v4f*>(&own[(lane & 31) * kPitch + i * 32 + 8 * q + 4 * (lane >> 5)]) = f;
+      }
+    wave_lds_fence();
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int row = it * 4 + (lane >> 4);
+      const int64_t m = m0 + wm + j * 32 + row;
+      if (m >= args.tokens || left == 0) continue;
+      const float xs = args.x_scales[m];
+      float f[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4f v = *reinterpret_cast<const v4f*>(&own[row * kPitch + (lane & 15) * 8 + 4 * h]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[4 * h + e] = v[e] * xs * ws[4 * h + e];
+      }
+      if (args.residual) {
+        const typename T::bits* p = static_cast<const typename T::bits*>(args.residual) + m * args.residual_stride + n;
+#pragma unroll
+        for (int v = 0; v < 8 / T::kVec; ++v) {
+          float g[T::kVec];
+          T::widen(load_part<T>(p + v * T::kVec, std::max(0, left - v * T::kVec), 0), g);
+#pragma unroll
+          for (int e = 0; e < T::kVec; ++e) f[v * T::kVec + e] += g[e];
+        }
+      }
+      for (int c = 0; c < args.ndst; ++c) {
+        typename T::bits* p = static_cast<typename T::bits*>(args.dst[c]) + m * args.dst_stride[c] + n;
+#pragma unroll
+        for (int v = 0; v < 8 / T::kVec; ++v) store_part<T>(p + v * T::kVec, std::max(0, left - v * T::kVec), T::round(f + v * T::kVec));
+      }
+    }
+    wave_lds_fence();
   }
 }
 
@@ -342,10 +504,24 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
   a.tokens = tokens;
   a.outer = outer;
   a.ndst = nrecv;
-  a.tiles_n = (int32_t)((outer + kTile - 1) / kTile);
-  const int64_t tiles = (tokens + kTile - 1) / kTile * a.tiles_n;
-  if (tiles > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer is too large");
-  const void* fn = dtype == kFloat32 ? reinterpret_cast<const void*>(&tile_kernel<F32>) : reinterpret_cast<const void*>(&tile_kernel<BF16>);
+  bool aligned = true;  // every row begins on a multiple of 16 bytes
+  for (int r = 0; r < a.nranks; ++r) {
+    a.steps += (a.width[r] + kDepth - 1) / kDepth;
+    aligned = aligned && ((reinterpret_cast<uintptr_t>(a.x[r]) | reinterpret_cast<uintptr_t>(a.w[r]) | a.x_stride[r] | a.w_stride[r]) & 15) == 0;
+  }
+  const bool f32 = dtype == kFloat32;
+  const bool big = aligned && tokens > 128;
+  const int side = big ? kBig : kTile;
+  const int64_t tiles_m = (tokens + side - 1) / side, tiles_n = (outer + side - 1) / side, tiles = tiles_m * tiles_n;
+  if (tiles > 0x7FFFFFF0) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer is too large");
+  a.tiles_m = (int32_t)tiles_m;
+  a.tiles_n = (int32_t)tiles_n;
+  if (big) {
+    constexpr int kWaves = 8;
+    const void* fn = f32 ? reinterpret_cast<const void*>(&big_tile_kernel<F32, kWaves>) : reinterpret_cast<const void*>(&big_tile_kernel<BF16, kWaves>);
+    return launch_kernel(fn, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * kWaves), &a, stream);
+  }
+  const void* fn = f32 ? reinterpret_cast<const void*>(&tile_kernel<F32>) : reinterpret_cast<const void*>(&tile_kernel<BF16>);
   return launch_kernel(fn, dim3((unsigned)tiles), dim3(256), &a, stream);
 }
 
