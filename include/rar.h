@@ -636,8 +636,10 @@ rar_result_t rar_quantize_rows(const void* const* xs, const int64_t* widths,
  *              residual (in place).
  *   tokens 0..2^24 (0 launches nothing), outer 1..2^24, nranks, nrecv 1..64.
  *   workspace  16-byte aligned device memory, rar_int8_projection_workspace
- *              bytes (0: NULL allowed).
- * It is fastest where rows begin on multiples of 16 bytes. */
+ *              bytes (0: NULL allowed): less where `aligned` says that every
+ *              row of xs and weights begins on a multiple of 16 bytes and that
+ *              rows are less than 2^24 - 256 bytes apart.  Other rows are laid
+ *              out so first, in every call of more than 16 tokens. */
 rar_result_t rar_int8_projection_allreduce(const int8_t* const* xs, const int64_t* widths,
                                            const int64_t* x_strides, const float* x_scales,
                                            const int8_t* const* weights,
@@ -649,7 +651,8 @@ rar_result_t rar_int8_projection_allreduce(const int8_t* const* xs, const int64_
                                            int nrecv, void* workspace, size_t workspace_bytes,
                                            void* stream);
 rar_result_t rar_int8_projection_workspace(const int64_t* widths, int nranks, int64_t tokens,
-                                           int64_t outer, rar_dtype_t dtype, size_t* bytes);
+                                           int64_t outer, rar_dtype_t dtype, int aligned,
+                                           size_t* bytes);
 
 /* Watchdog status: RAR_ABORTED if a launch on this communicator timed out in
  * a wait, else RAR_SUCCESS.  Does not synchronize; reflects launches the

@@ -139,7 +139,7 @@ SIGNATURES = [
                                                  _c.c_int, _c.c_void_p, _c.c_size_t,
                                                  _c.c_void_p]),
     ("rar_int8_projection_workspace", _c.c_int, [_lp, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int,
-                                                 _c.POINTER(_c.c_size_t)]),
+                                                 _c.c_int, _c.POINTER(_c.c_size_t)]),
     ("rar_comm_get_async_error", _c.c_int, [_c.c_void_p]),
     ("rar_comm_query_state", _c.c_int, [_c.c_void_p, _c.POINTER(_c.c_int64), _c.c_size_t,
                                         _c.POINTER(_c.c_size_t)]),

@@ -9,6 +9,8 @@
 // result does not depend on how the columns are split.
 #include "op_common.h"
 
+#include <numeric>
+
 namespace rar {
 namespace {
 
@@ -28,101 +30,141 @@ struct QuantArgs {
   int64_t dst_stride[kMaxRanks];
   int64_t width[kMaxRanks];
   float* scales;
-  int32_t nranks;
+  int32_t nranks, pieces;
+  int32_t first[kMaxRanks];  // the pieces before a rank's
 };
 
-// rint(127 x / most), a tie to the even one as the quotient itself has it.
-// bf16: 127 x is exact in fp32, and a quotient that is no tie is at least
-// 2^-9 of itself away from one, far more than the division's rounding; both
-// are scaled by a power of two where 127 x would leave fp32's range.  fp32:
-// the same in 64 bits.
+// rint(127 x / most), a tie to the even integer as the quotient itself has it.
+// The product with 127 / most, 3 roundings, is within 127 * 3 * 2^-24 < 2^-15
+// of the quotient: unless it is as close to the middle of two integers, both
+// have the same nearest one, which adding 1.5 * 2^23 leaves in the low bits.
+// The others are divided in 64 bits, where 127 x is exact and a quotient of
+// 24-bit numbers that is no tie is much further from one than the rounding.
+// x and most are scaled by a power of two where the product would leave fp32's
+// range or lose bits.
 struct Quotient {
-  float most, power;
-  double most64;
-  __device__ __forceinline__ explicit Quotient(float m) : most64(m) {
-    power = m > 0x1p100f ? 0x1p-40f : m < 0x1p-60f ? 0x1p60f : 1.0f;
-    most = m * power;
+  float power, factor, most;
+  __device__ __forceinline__ explicit Quotient(float m) : most(m) {
+    power = m > 0x1p100f ? 0x1p-40f : m < 0x1p-60f ? 0x1p80f : 1.0f;
+    factor = 127.0f / (m * power);
   }
-  template <class T>
-  __device__ __forceinline__ int32_t of(float x) const {
-    if constexpr (T::kVec == 8) return (int32_t)__builtin_rintf(x * power * 127.0f / most);
-    else return (int32_t)__builtin_rint((double)x * 127.0 / most64);
+  // The integer's low 8 bits are those of the result.
+  template <bool kScaled>
+  __device__ __forceinline__ uint32_t of(float x, bool* near) const {
+    const float r = (kScaled ? x * power : x) * factor, shifted = r + 0x1.8p23f;
+    *near = *near || __builtin_fabsf((shifted - 0x1.8p23f) - r) >= 0.5f - 0x1p-15f;
+    return __float_as_uint(shifted);
   }
+  __device__ __forceinline__ uint32_t divided(float x) const { return (uint32_t)(int32_t)__builtin_rint((double)x * 127.0 / (double)most); }
 };
 
-// A workgroup takes a token: its columns of all ranks, in registers as far as
-// kKept vectors a thread go, read a second time beyond that.
+// A workgroup takes a token.  Its columns are counted in pieces of 64 vectors,
+// each of one rank; a wave keeps its first kKept pieces in registers, loaded
+// together, and reads those beyond a second time.
 constexpr int kKept = 4;
 
 template <class T>
-__global__ void __launch_bounds__(256) quantize_kernel(QuantArgs) {
+__global__ void __launch_bounds__(1024) quantize_kernel(QuantArgs) {
   const QuantArgs& args = kernel_args<QuantArgs>();
-  __shared__ uint32_t scratch[4];
+  __shared__ uint32_t scratch[16];
   const int64_t row = blockIdx.x;
-  // vectors are counted through the ranks: each starts on a multiple of 256
-  v4u kept[kKept];
-  uint32_t most = 0;  // bits of |x|, which order as the values do, NaN last
-  int n = 0;
-  for (int r = 0; r < args.nranks; ++r) {
-    const typename T::bits* p = static_cast<const typename T::bits*>(args.src[r]) + row * args.src_stride[r];
-    for (int64_t e0 = 0; e0 < args.width[r]; e0 += 256 * T::kVec, ++n) {
-      const int64_t e = e0 + threadIdx.x * T::kVec;
-      v4u x = {0, 0, 0, 0};
-      if (e < args.width[r]) x = load_part<T>(p + e, (int)(args.width[r] - e > T::kVec ? T::kVec : args.width[r] - e), 0);
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // this lane's elements of a piece: how many are there (0: none)
+  auto find = [&](int piece, int* rank, int64_t* e) {
+    int r = 0;
+    while (r + 1 < args.nranks && args.first[r + 1] <= piece) ++r;
+    *rank = r;
+    *e = ((int64_t)(piece - args.first[r]) * 64 + lane) * T::kVec;
+    return piece < args.pieces ? (int)std::max<int64_t>(0, std::min<int64_t>(args.width[r] - *e, T::kVec)) : 0;
+  };
+  auto load = [&](int rank, int64_t e, int left) {
+    return load_part<T>(static_cast<const typename T::bits*>(args.src[rank]) + row * args.src_stride[rank] + e, left, 0);
+  };
+  // the largest bits of |x|, which order as the values do, NaN last
+  typedef uint16_t v2s __attribute__((ext_vector_type(2)));
+  uint32_t most = 0;
+  auto look = [&](v4u x) {
 #pragma unroll
-      for (int j = 0; j < kKept; ++j)
-        if (n == j) kept[j] = x;
-      float f[T::kVec];
-      T::widen(x, f);
-#pragma unroll
-      for (int i = 0; i < T::kVec; ++i) most = std::max(most, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (T::kVec == 4) {
+        most = std::max(most, x[i] & 0x7FFFFFFFu);
+      } else {  // two at a time
+        const v2s a = __builtin_bit_cast(v2s, most), b = __builtin_bit_cast(v2s, x[i] & 0x7FFF7FFFu);
+        most = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+      }
     }
+  };
+  v4u kept[kKept];
+  int rank[kKept], left[kKept];
+  int64_t e[kKept];
+#pragma unroll
+  for (int j = 0; j < kKept; ++j) {
+    left[j] = find(wave + j * waves, &rank[j], &e[j]);
+    kept[j] = v4u{0, 0, 0, 0};
+    if (left[j] > 0) kept[j] = load(rank[j], e[j], left[j]);
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) most = std::max(most, (uint32_t)__shfl_xor((int)most, d));
-  if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = most;
-  __syncthreads();
+  for (int j = 0; j < kKept; ++j) look(kept[j]);
+  for (int piece = wave + kKept * waves; piece < args.pieces; piece += waves) {
+    int r;
+    int64_t at;
+    const int n = find(piece, &r, &at);
+    if (n > 0) look(load(r, at, n));
+  }
+  if constexpr (T::kVec == 8) most = std::max(most << 16, most & 0xFFFF0000u);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) most = std::max(most, scratch[w]);
+  for (int d = 1; d < 64; d <<= 1) most = std::max(most, (uint32_t)__shfl_xor((int)most, d));
+  if (lane == 0) scratch[wave] = most;
+  __syncthreads();
+  for (int w = 0; w < waves; ++w) most = std::max(most, scratch[w]);
   const bool finite = most < 0x7F800000u;
   const float m = __uint_as_float(most);
   if (threadIdx.x == 0) args.scales[row] = finite ? m / 127.0f : __uint_as_float(0x7FC00000u);
   const bool zero = !finite || most == 0;
   const Quotient quotient(m);
-  n = 0;
-  for (int r = 0; r < args.nranks; ++r) {
-    const typename T::bits* p = static_cast<const typename T::bits*>(args.src[r]) + row * args.src_stride[r];
-    int8_t* out = args.dst[r] + row * args.dst_stride[r];
-    for (int64_t e0 = 0; e0 < args.width[r]; e0 += 256 * T::kVec, ++n) {
-      const int64_t e = e0 + threadIdx.x * T::kVec;
-      if (e >= args.width[r]) continue;
-      const int left = (int)(args.width[r] - e > T::kVec ? T::kVec : args.width[r] - e);
-      v4u x = {0, 0, 0, 0};
-      if (n < kKept) {
+  auto store = [&](v4u x, int r, int64_t at, int n) {
+    int8_t* out = args.dst[r] + row * args.dst_stride[r] + at;
+    float f[T::kVec];
+    T::widen(x, f);
+    uint32_t b[T::kVec], q[T::kVec / 4];
+    bool near = false;
+    if (zero) {
 #pragma unroll
-        for (int j = 0; j < kKept; ++j)
-          if (n == j) x = kept[j];
-      } else {
-        x = load_part<T>(p + e, left, 0);
-      }
-      float f[T::kVec];
-      T::widen(x, f);
-      uint32_t q[T::kVec / 4];
+      for (int i = 0; i < T::kVec; ++i) b[i] = 0;
+    } else if (quotient.power == 1.0f) {
 #pragma unroll
-      for (int i = 0; i < T::kVec; ++i) {
-        const uint32_t b = zero ? 0 : (uint32_t)quotient.of<T>(f[i]) & 0xFFu;
-        q[i / 4] = i & 3 ? q[i / 4] | b << (8 * (i & 3)) : b;
-      }
-      if (left == T::kVec) {
-        typedef uint32_t u32_user __attribute__((aligned(1)));
+      for (int i = 0; i < T::kVec; ++i) b[i] = quotient.of<false>(f[i], &near);
+    } else {
 #pragma unroll
-        for (int i = 0; i < T::kVec / 4; ++i) *reinterpret_cast<u32_user*>(out + e + 4 * i) = q[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i)
-          if (i < left) out[e + i] = (int8_t)(q[i / 4] >> (8 * (i & 3)));
-      }
+      for (int i = 0; i < T::kVec; ++i) b[i] = quotient.of<true>(f[i], &near);
     }
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) b[i] = quotient.divided(f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kVec / 4; ++i)  // the low bytes of four
+      q[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0C0C0400u),
+                                   __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0C0C0400u), 0x05040100u);
+    if (n == T::kVec) {
+      typedef uint32_t u32_user __attribute__((aligned(1)));
+      typedef uint64_t u64_user __attribute__((aligned(1)));
+      if constexpr (T::kVec == 8) *reinterpret_cast<u64_user*>(out) = (uint64_t)q[T::kVec / 4 - 1] << 32 | q[0];
+      else *reinterpret_cast<u32_user*>(out) = q[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i)
+        if (i < n) out[i] = (int8_t)(q[i / 4] >> (8 * (i & 3)));
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < kKept; ++j)
+    if (left[j] > 0) store(kept[j], rank[j], e[j], left[j]);
+  for (int piece = wave + kKept * waves; piece < args.pieces; piece += waves) {
+    int r;
+    int64_t at;
+    const int n = find(piece, &r, &at);
+    if (n > 0) store(load(r, at, n), r, at, n);
   }
 }
 
@@ -140,8 +182,12 @@ struct ProjArgs {
   const void* residual;
   int64_t residual_stride;
   int64_t tokens, outer;
-  int32_t nranks, ndst, tiles_m, tiles_n;
+  int32_t nranks, ndst;
+  int32_t tiles_m, tiles_n;  // of the launch's (last) kind of tile
+  int32_t wide_n;            // tiles of 256 channels in front of those of 192
   int32_t steps;  // of kDepth bytes of the inner dimension, each rank's rounded up
+  int32_t splits;
+  int32_t* partial;  // [splits][tokens][outer]
 };
 
 // 16 bytes of a row from p on, n (1 or more) of them there and zeros behind.
@@ -166,234 +212,373 @@ __device__ __forceinline__ v4u load_bytes(const int8_t* p, int n) {
   return v4u{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-constexpr int kTile = 128;   // tokens and channels of a workgroup
-constexpr int kDepth = 128;  // bytes of the inner dimension at a time
+constexpr int kDepth = 128;  // bytes of the inner dimension that a step has
 
+// The results of token m, channels n ... n + left - 1 (up to T::kVec), from
+// their integer sums.
 template <class T>
-__global__ void __launch_bounds__(256) tile_kernel(ProjArgs) {
-  const ProjArgs& args = kernel_args<ProjArgs>();
-  __shared__ __attribute__((aligned(16))) int8_t tile[2][kTile * kDepth];  // weights, tokens
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = (int64_t)(blockIdx.x / args.tiles_n) * kTile, n0 = (int64_t)(blockIdx.x % args.tiles_n) * kTile;
-  v16i acc[2][2];
+__device__ __forceinline__ void finish(const ProjArgs& args, int64_t m, int64_t n, int left, const int32_t* sum, const float* ws) {
+  const float xs = args.x_scales[m];
+  float f[T::kVec];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int e = 0; e < T::kVec; ++e) f[e] = (float)sum[e] * xs * ws[e];
+  if (args.residual) {
+    float g[T::kVec];
+    T::widen(load_part<T>(static_cast<const typename T::bits*>(args.residual) + m * args.residual_stride + n, left, 0), g);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0;
-  for (int r = 0; r < args.nranks; ++r) {
-    const int width = args.width[r];
-    for (int k0 = 0; k0 < width; k0 += kDepth) {
-      v4u a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = threadIdx.x + 256 * i, row = c >> 3, k = k0 + (c & 7) * 16;
-        a[i] = b[i] = v4u{0, 0, 0, 0};
-        if (k < width && n0 + row < args.outer) a[i] = load_bytes(args.w[r] + (n0 + row) * args.w_stride[r] + k, width - k);
-        if (k < width && m0 + row < args.tokens) b[i] = load_bytes(args.x[r] + (m0 + row) * args.x_stride[r] + k, width - k);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = threadIdx.x + 256 * i, row = c >> 3, at = row * kDepth + (((c & 7) ^ (row >> 1 & 7)) << 4);
-        *reinterpret_cast<v4u*>(&tile[0][at]) = a[i];
-        *reinterpret_cast<v4u*>(&tile[1][at]) = b[i];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        v4i wf[2], xf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int wr = (wave & 1) * 64 + i * 32 + (lane & 31), xr = (wave >> 1) * 64 + i * 32 + (lane & 31), ch = s * 2 + (lane >> 5);
-          wf[i] = *reinterpret_cast<const v4i*>(&tile[0][wr * kDepth + ((ch ^ (wr >> 1 & 7)) << 4)]);
-          xf[i] = *reinterpret_cast<const v4i*>(&tile[1][xr * kDepth + ((ch ^ (xr >> 1 & 7)) << 4)]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
-      }
-    }
+    for (int e = 0; e < T::kVec; ++e) f[e] += g[e];
   }
-  // lane l of a product has token l & 31 and channels 8 q + 4 (l >> 5) + 0..3
+  const v4u y = T::round(f);
+  for (int c = 0; c < args.ndst; ++c) store_part<T>(static_cast<typename T::bits*>(args.dst[c]) + m * args.dst_stride[c] + n, left, y);
+}
+// The scales of channels n ... n + left - 1.
+template <class T>
+__device__ __forceinline__ void load_scales(const ProjArgs& args, int64_t n, int left, float* ws) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t m = m0 + (wave >> 1) * 64 + j * 32 + (lane & 31);
-    if (m >= args.tokens) continue;
-    const float xs = args.x_scales[m];
+  for (int v = 0; v < T::kVec; v += 4) load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n + v), left - v, ws + v);
+}
+__device__ __forceinline__ void store_words(int32_t* p, int n, v4i v) {
+  typedef int32_t v4i_user __attribute__((ext_vector_type(4), aligned(4)));
+  if (n >= 4) {
+    *reinterpret_cast<v4i_user*>(p) = v;
+  } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + (wave & 1) * 64 + i * 32 + 8 * q + 4 * (lane >> 5);
-        const int left = (int)(args.outer - n > 4 ? 4 : args.outer - n);
-        if (left <= 0) continue;
-        float f[4], ws[4];
-        load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n), left, ws);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = (float)acc[i][j][4 * q + e] * xs * ws[e];
-        if (args.residual) {
-          float g[4];
-          load4<T>(static_cast<const typename T::bits*>(args.residual) + m * args.residual_stride + n, left, g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] += g[e];
-        }
-        for (int c = 0; c < args.ndst; ++c) store4<T>(static_cast<typename T::bits*>(args.dst[c]) + m * args.dst_stride[c] + n, left, f);
-      }
-    }
+    for (int i = 0; i < 3; ++i)
+      if (i < n) p[i] = v[i];
   }
 }
-
-// Many tokens: a tile of 256 tokens x 256 channels of a workgroup, whose
-// operands go from memory to LDS without passing through registers, 128 bytes
-// of the inner dimension at a time, while the step before is multiplied.
-constexpr int kBig = 256;
-
-// 16 bytes a lane from p to LDS, to 16 * lane behind `to`.  The caller waits
-// for it (vmcnt) before a barrier.
-__device__ __forceinline__ void to_lds(const int8_t* p, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(p) : "memory", "m0");
+__device__ __forceinline__ v4i load_words(const int32_t* p, int n) {
+  typedef int32_t v4i_user __attribute__((ext_vector_type(4), aligned(4)));
+  if (n >= 4) return *reinterpret_cast<const v4i_user*>(p);
+  v4i v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i < n) v[i] = p[i];
+  return v;
 }
 
-template <class T, int kWaves>
-__global__ void __launch_bounds__(64 * kWaves, 1) big_tile_kernel(ProjArgs) {
-  const ProjArgs& args = kernel_args<ProjArgs>();
-  constexpr int kStage = 2 * kBig * kDepth;              // weights, then tokens
-  constexpr int kWaveM = kBig * 2 / kWaves;              // tokens of a wave
-  constexpr int kWaveN = 128;                            // channels of a wave
-  constexpr int kFM = kWaveM / 32, kFN = kWaveN / 32;
-  constexpr int kLoads = kBig * kDepth / 16 / (64 * kWaves);  // 16-byte loads a thread, of each operand
-  __shared__ __attribute__((aligned(16))) int8_t lds[2 * kStage + 8192];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tile = (int64_t)(blockIdx.x & 7) * ((gridDim.x + 7) / 8) + (blockIdx.x >> 3);
-  if (tile >= (int64_t)args.tiles_m * args.tiles_n) return;
-  const int64_t m0 = tile % args.tiles_m * kBig, n0 = tile / args.tiles_m * kBig;
-  v16i acc[kFN][kFM];
-#pragma unroll
-  for (int i = 0; i < kFN; ++i)
-#pragma unroll
-    for (int j = 0; j < kFM; ++j)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0;
+// Tile (n, m) of workgroup b, of tiles_n x tiles_m; false: none.  Workgroups
+// go to the 8 XCDs in turn: each XCD gets a run of tiles, in which any 32 that
+// follow each other, which it runs at a time, share the operands of 8 x 4
+// (8192^3: 496 -> 467 us against m fastest).
+__device__ __forceinline__ bool tile_of(int64_t b, int64_t tiles_m, int64_t tiles_n, int64_t* n, int64_t* m) {
+  const int64_t tiles = tiles_m * tiles_n, tile = (b & 7) * ((tiles + 7) / 8) + (b >> 3);
+  if (tile >= tiles) return false;
+  const int64_t group = tile / (4 * tiles_m), in_group = tile - group * 4 * tiles_m;
+  const int columns = (int)std::min<int64_t>(4, tiles_n - group * 4);
+  *m = in_group / columns;
+  *n = group * 4 + in_group % columns;
+  return true;
+}
 
-  // the next step to load: rank, its inner offset, this lane's rows there
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)lds;
-  const int row0 = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
-  int rank = 0, k0 = 0;
-  const int8_t *pw[kLoads], *px[kLoads];
-  auto begin_rank = [&] {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int64_t row = row0 + i * 8 * kWaves;
-      pw[i] = args.w[rank] + std::min(n0 + row, args.outer - 1) * args.w_stride[rank] + chunk * 16;
-      px[i] = args.x[rank] + std::min(m0 + row, args.tokens - 1) * args.x_stride[rank] + chunk * 16;
-    }
-  };
-  auto load_step = [&](int stage) {
-    const int width = args.width[rank], left = width - k0;
-    if (left >= kDepth) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        to_lds(pw[i] + k0, lds0 + stage * kStage + (i * kWaves + wave) * 1024);
-        to_lds(px[i] + k0, lds0 + stage * kStage + kBig * kDepth + (i * kWaves + wave) * 1024);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        v4u a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        if (left > chunk * 16) a = load_bytes(pw[i] + k0, left - chunk * 16), b = load_bytes(px[i] + k0, left - chunk * 16);
-        *reinterpret_cast<v4u*>(&lds[stage * kStage + (i * kWaves + wave) * 1024 + lane * 16]) = a;
-        *reinterpret_cast<v4u*>(&lds[stage * kStage + kBig * kDepth + (i * kWaves + wave) * 1024 + lane * 16]) = b;
-      }
-    }
-    k0 += kDepth;
-    if (k0 >= width && rank + 1 < args.nranks) {
-      k0 = 0;
-      ++rank;
-      begin_rank();
-    }
-  };
-  const int wn = (wave & 1) * kWaveN, wm = (wave >> 1) * kWaveM;
-  if (args.steps > 0) {
-    begin_rank();
-    load_step(0);
-  }
-  for (int step = 0; step < args.steps; ++step) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    if (step + 1 < args.steps) load_step((step + 1) & 1);
-    const int8_t* tw = &lds[(step & 1) * kStage];
-    const int8_t* tx = tw + kBig * kDepth;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4i wf[kFN], xf[kFM];
-      // 32 rows apart the swizzle is the same
-      const int r = lane & 31, at = r * kDepth + (((s * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
-#pragma unroll
-      for (int i = 0; i < kFN; ++i) wf[i] = *reinterpret_cast<const v4i*>(&tw[(wn + i * 32) * kDepth + at]);
-#pragma unroll
-      for (int j = 0; j < kFM; ++j) xf[j] = *reinterpret_cast<const v4i*>(&tx[(wm + j * 32) * kDepth + at]);
-#pragma unroll
-      for (int i = 0; i < kFN; ++i)
-#pragma unroll
-        for (int j = 0; j < kFM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  // Out through LDS, 32 tokens x 128 channels of a wave at a time, so that
-  // each row of it is read, completed and written as whole lines.
-  constexpr int kPitch = kWaveN + 4;  // floats: rows start on different banks
-  __syncthreads();
-  float* own = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
-  const int64_t n = n0 + wn + (lane & 15) * 8;
-  const int left = (int)std::max<int64_t>(0, std::min<int64_t>(8, args.outer - n));
-  float ws[8];
-  load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n), left, ws);
-  load4<F32>(reinterpret_cast<const uint32_t*>(args.w_scales + n + 4), left - 4, ws + 4);
-#pragma unroll
-  for (int j = 0; j < kFM; ++j) {
+// 16 bytes a lane from base + offset to LDS, to 16 * lane behind `to`.  The
+// caller waits for it (vmcnt) before a barrier.
+__device__ __forceinline__ void to_lds(const int8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+
+// A workgroup's tile: kWN x kWM waves, each with kFN x kFM products of 32
+// channels x 32 tokens.  The operands of a step are in LDS, rows of 128 bytes
+// whose 16-byte pieces are swapped by row so that the lanes of a read meet
+// different banks.  Aligned rows (on multiples of 16 bytes) go there from
+// memory directly, others through registers.
+template <class T, int kWN, int kWM, int kFN, int kFM, int kStages>
+struct Tile {
+  static constexpr int kWaves = kWN * kWM, kThreads = 64 * kWaves;
+  static constexpr int kN = kWN * kFN * 32, kM = kWM * kFM * 32;  // channels, tokens
+  static constexpr int kLoadsW = kN * 8 / kThreads, kLoadsX = kM * 8 / kThreads, kLoads = kLoadsW + kLoadsX;
+  static constexpr int kStage = (kN + kM) * kDepth;
+  static constexpr int kPitch = kFN * 32 + 4;  // floats of a result's row: rows start on different banks
+  static constexpr int kOut = kWaves * 32 * kPitch * 4;
+  static constexpr int kLds = kStages * kStage > kOut ? kStages * kStage : kOut;
+
+  static __device__ __forceinline__ void run(const ProjArgs& args, int8_t* lds, int64_t n0, int64_t m0, int split) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    v16i acc[kFN][kFM];
 #pragma unroll
     for (int i = 0; i < kFN; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v4f f;
+      for (int j = 0; j < kFM; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = (float)acc[i][j][4 * q + e];
-        *reinterpret_cast<v4f*>(&own[(lane & 31) * kPitch + i * 32 + 8 * q + 4 * (lane >> 5)]) = f;
+        for (int k = 0; k < 16; ++k) acc[i][j][k] = 0;
+
+    // the next step to load: rank, its inner offset, this lane's rows there
+    // (from the tile's first row on; beyond the last row, the last row again)
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)lds;
+    const int row0 = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+    const int last_w = (int)std::min<int64_t>(args.outer - n0, kN) - 1, last_x = (int)std::min<int64_t>(args.tokens - m0, kM) - 1;
+    int rank = 0, k0 = 0;
+    const int8_t *w0 = nullptr, *x0 = nullptr;
+    uint32_t ow[kLoadsW], ox[kLoadsX];
+    auto begin_rank = [&] {
+      w0 = args.w[rank] + n0 * args.w_stride[rank];
+      x0 = args.x[rank] + m0 * args.x_stride[rank];
+#pragma unroll
+      for (int i = 0; i < kLoadsW; ++i) ow[i] = (uint32_t)std::min(row0 + i * 8 * kWaves, last_w) * (uint32_t)args.w_stride[rank] + chunk * 16;
+#pragma unroll
+      for (int i = 0; i < kLoadsX; ++i) ox[i] = (uint32_t)std::min(row0 + i * 8 * kWaves, last_x) * (uint32_t)args.x_stride[rank] + chunk * 16;
+    };
+    auto next = [&] {
+      k0 += kDepth;
+      if (k0 >= args.width[rank] && rank + 1 < args.nranks) {
+        k0 = 0;
+        ++rank;
+        begin_rank();
       }
-    wave_lds_fence();
+    };
+    auto load_step = [&](int stage) {
+      const int left = args.width[rank] - k0;
+      if (left >= kDepth) {
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int row = it * 4 + (lane >> 4);
-      const int64_t m = m0 + wm + j * 32 + row;
-      if (m >= args.tokens || left == 0) continue;
-      const float xs = args.x_scales[m];
-      float f[8];
+        for (int i = 0; i < kLoadsW; ++i) to_lds(w0 + k0, ow[i], lds0 + stage * kStage + (i * kWaves + wave) * 1024);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4f v = *reinterpret_cast<const v4f*>(&own[row * kPitch + (lane & 15) * 8 + 4 * h]);
+        for (int i = 0; i < kLoadsX; ++i) to_lds(x0 + k0, ox[i], lds0 + stage * kStage + kN * kDepth + (i * kWaves + wave) * 1024);
+      } else {  // a rank's last bytes, zeros behind
+        const int mine = left - chunk * 16;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 * h + e] = v[e] * xs * ws[4 * h + e];
-      }
-      if (args.residual) {
-        const typename T::bits* p = static_cast<const typename T::bits*>(args.residual) + m * args.residual_stride + n;
-#pragma unroll
-        for (int v = 0; v < 8 / T::kVec; ++v) {
-          float g[T::kVec];
-          T::widen(load_part<T>(p + v * T::kVec, std::max(0, left - v * T::kVec), 0), g);
-#pragma unroll
-          for (int e = 0; e < T::kVec; ++e) f[v * T::kVec + e] += g[e];
+        for (int i = 0; i < kLoads; ++i) {
+          const int8_t* from = i < kLoadsW ? w0 + ow[i < kLoadsW ? i : 0] : x0 + ox[i < kLoadsW ? 0 : i - kLoadsW];
+          const int at = i < kLoadsW ? i * kWaves : kN / 8 + (i - kLoadsW) * kWaves;
+          *reinterpret_cast<v4u*>(&lds[stage * kStage + (at + wave) * 1024 + lane * 16]) = mine > 0 ? load_bytes(from + k0, mine) : v4u{0, 0, 0, 0};
         }
       }
-      for (int c = 0; c < args.ndst; ++c) {
-        typename T::bits* p = static_cast<typename T::bits*>(args.dst[c]) + m * args.dst_stride[c] + n;
+      next();
+    };
+    const int r = lane & 31, wn = (wave % kWN) * kFN * 32, wm = (wave / kWN) * kFM * 32;
+    v4i wf[2][kFN], xf[2][kFM];
+    auto read_fragments = [&](int stage, int s, int to) {
+      // 32 rows apart the swizzle is the same
+      const int at = r * kDepth + (((s * 2 + (lane >> 5)) ^ (r >> 1 & 7)) << 4);
+      const int8_t* tw = &lds[stage * kStage + wn * kDepth + at];
+      const int8_t* tx = &lds[stage * kStage + (kN + wm) * kDepth + at];
 #pragma unroll
-        for (int v = 0; v < 8 / T::kVec; ++v) store_part<T>(p + v * T::kVec, std::max(0, left - v * T::kVec), T::round(f + v * T::kVec));
-      }
+      for (int i = 0; i < kFN; ++i) wf[to][i] = *reinterpret_cast<const v4i*>(tw + i * 32 * kDepth);
+#pragma unroll
+      for (int j = 0; j < kFM; ++j) xf[to][j] = *reinterpret_cast<const v4i*>(tx + j * 32 * kDepth);
+    };
+    auto multiply = [&](int from) {
+#pragma unroll
+      for (int i = 0; i < kFN; ++i)
+#pragma unroll
+        for (int j = 0; j < kFM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[from][i], xf[from][j], acc[i][j], 0, 0, 0);
+    };
+    // A quarter of a step is multiplied while the next one's fragments are
+    // read.  The workgroup meets before the last quarter: then no wave reads
+    // the step any more, its place takes the step kStages further on, and the
+    // next one is there.  Loads to LDS arrive in order: all but the youngest
+    // kStages - 2 steps' have when as many are outstanding at most.  (A rank's
+    // last step may come through registers; what was issued before it has
+    // arrived when it is stored.)
+    auto meet = [](bool all) {
+      if (kStages == 2 || all) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * kLoads) : "memory");
+      __builtin_amdgcn_s_barrier();
+    };
+    const int begin = (int)((int64_t)args.steps * split / args.splits), steps = (int)((int64_t)args.steps * (split + 1) / args.splits) - begin;
+    if (steps > 0) {
+      k0 = begin * kDepth;
+      for (int n; k0 >= (n = (args.width[rank] + kDepth - 1) / kDepth * kDepth); ++rank) k0 -= n;
+      begin_rank();
+      load_step(0);
+#pragma unroll
+      for (int i = 1; i < kStages; ++i)
+        if (i < steps) load_step(i);
+      if (steps >= kStages) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 1) * kLoads) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      read_fragments(0, 0, 0);
     }
-    wave_lds_fence();
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        read_fragments(stage, s + 1, (s + 1) & 1);
+        multiply(s & 1);
+#pragma unroll
+        for (int g = 0; g < kFN + kFM && g < kFN * kFM; ++g) {  // one read, one product
+          __builtin_amdgcn_sched_group_barrier(0x100, kFN * kFM < kFN + kFM ? 2 : 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
+      }
+      meet(step + kStages > steps);
+      const int after = stage + 1 == kStages ? 0 : stage + 1;
+      if (step + kStages < steps) load_step(stage);
+      if (step + 1 < steps) read_fragments(after, 0, 0);
+      multiply(1);
+      stage = after;
+    }
+    // Out through LDS, 32 tokens of a wave at a time, so that its rows are
+    // completed and written as whole lines.
+    __syncthreads();
+    constexpr int kLanes = kFN * 32 / T::kVec, kRows = 64 / kLanes;  // lanes of a row, rows at a time
+    int32_t* own = reinterpret_cast<int32_t*>(lds) + wave * 32 * kPitch;
+    const int column = lane % kLanes * T::kVec;
+    const int64_t n = n0 + wn + column;
+    const int left = lane < kLanes * kRows ? (int)std::max<int64_t>(0, std::min<int64_t>(T::kVec, args.outer - n)) : 0;
+    float ws[T::kVec];
+    load_scales<T>(args, n, left, ws);
+#pragma unroll
+    for (int j = 0; j < kFM; ++j) {
+#pragma unroll
+      for (int i = 0; i < kFN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // lane l has token l & 31 and channels 8 q + 4 (l >> 5) + 0..3
+          v4i f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = acc[i][j][4 * q + e];
+          *reinterpret_cast<v4i*>(&own[(lane & 31) * kPitch + i * 32 + 8 * q + 4 * (lane >> 5)]) = f;
+        }
+      wave_lds_fence();
+#pragma unroll
+      for (int it = 0; it < (32 + kRows - 1) / kRows; ++it) {
+        const int row = it * kRows + lane / kLanes;
+        const int64_t m = m0 + wm + j * 32 + row;
+        if (row >= 32 || m >= args.tokens || left == 0) continue;
+        int32_t sum[T::kVec];
+#pragma unroll
+        for (int h = 0; h < T::kVec; h += 4) {
+          const v4i v = *reinterpret_cast<const v4i*>(&own[row * kPitch + column + h]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[h + e] = v[e];
+          if (args.splits > 1) store_words(args.partial + (split * args.tokens + m) * args.outer + n + h, left - h, v);
+        }
+        if (args.splits == 1) finish<T>(args, m, n, left, sum, ws);
+      }
+      wave_lds_fence();
+    }
   }
+};
+
+// How many of the channels go in tiles of 256, the others in tiles of 192.
+template <class T>
+__global__ void __launch_bounds__(512, 1) big_tiles_kernel(ProjArgs) {
+  typedef Tile<T, 2, 4, 4, 2, 2> Wide;
+  typedef Tile<T, 2, 4, 3, 2, 2> Narrow;
+  const ProjArgs& args = kernel_args<ProjArgs>();
+  __shared__ __attribute__((aligned(16))) int8_t lds[Wide::kLds > Narrow::kLds ? Wide::kLds : Narrow::kLds];
+  int64_t n, m;
+  const int64_t wide = (args.tiles_m * args.wide_n + 7) / 8 * 8;
+  if (blockIdx.x < wide) {
+    if (tile_of(blockIdx.x, args.tiles_m, args.wide_n, &n, &m)) Wide::run(args, lds, n * 256, m * 256, 0);
+  } else {
+    if (tile_of(blockIdx.x - wide, args.tiles_m, args.tiles_n, &n, &m)) Narrow::run(args, lds, args.wide_n * 256 + n * 192, m * 256, 0);
+  }
+}
+
+// Fewer tiles than CUs: `splits` workgroups a tile, each with a part of the
+// inner dimension, and sum_kernel behind them.
+template <class T, int kWN, int kWM, int kFN, int kFM, int kStages>
+__global__ void __launch_bounds__(64 * kWN * kWM) tiles_kernel(ProjArgs) {
+  typedef Tile<T, kWN, kWM, kFN, kFM, kStages> Own;
+  const ProjArgs& args = kernel_args<ProjArgs>();
+  __shared__ __attribute__((aligned(16))) int8_t lds[Own::kLds];
+  int64_t n, m;
+  if (tile_of(blockIdx.x, args.tiles_m, args.tiles_n, &n, &m)) Own::run(args, lds, n * Own::kN, m * Own::kM, blockIdx.y);
+}
+
+// The sums over the splits, a vector of a token's results a thread.
+template <class T>
+__global__ void __launch_bounds__(256) sum_kernel(ProjArgs) {
+  const ProjArgs& args = kernel_args<ProjArgs>();
+  const int64_t m = blockIdx.y, n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * T::kVec;
+  if (n >= args.outer) return;
+  const int left = (int)std::min<int64_t>(T::kVec, args.outer - n);
+  const int32_t* p = args.partial + m * args.outer + n;
+  int32_t sum[T::kVec];
+#pragma unroll
+  for (int e = 0; e < T::kVec; ++e) sum[e] = 0;
+#pragma unroll 4
+  for (int s = 0; s < args.splits; ++s)
+#pragma unroll
+    for (int h = 0; h < T::kVec; h += 4) {
+      const v4i v = load_words(p + s * args.tokens * args.outer + h, left - h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[h + e] += v[e];
+    }
+  float ws[T::kVec];
+  load_scales<T>(args, n, left, ws);
+  finish<T>(args, m, n, left, sum, ws);
+}
+
+// Up to 16 tokens: a workgroup takes 16 channels; its 8 waves share the inner
+// dimension, 64 bytes at a time, and read both operands into registers.
+constexpr int kFewTokens = 16;
+template <class T>
+__global__ void __launch_bounds__(512, 4) few_kernel(ProjArgs) {
+  constexpr int kBatch = 7;  // pieces whose loads are issued together
+  const ProjArgs& args = kernel_args<ProjArgs>();
+  __shared__ __attribute__((aligned(16))) int32_t sums[8][kFewTokens][16 + 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16, row = std::min<int64_t>(n0 + (lane & 15), args.outer - 1);
+  const int tokens = (int)args.tokens, part = (lane >> 4) * 16;
+  v4i acc = {0, 0, 0, 0};
+  for (int r = 0; r < args.nranks; ++r) {
+    const int width = args.width[r];
+    const int8_t* w = args.w[r] + row * args.w_stride[r] + part;
+    const int8_t* x = args.x[r] + std::min(lane & 15, tokens - 1) * args.x_stride[r] + part;
+    for (int k0 = wave * 64; k0 < width; k0 += 8 * 64 * kBatch) {
+      v4u a[kBatch], b[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int k = k0 + i * 8 * 64;
+        a[i] = b[i] = v4u{0, 0, 0, 0};
+        if (k + 64 <= width) {
+          a[i] = load_bytes(w + k, 16);
+          b[i] = load_bytes(x + k, 16);
+        } else if (k + part < width) {
+          a[i] = load_bytes(w + k, width - k - part);
+          b[i] = load_bytes(x + k, width - k - part);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a[i]), __builtin_bit_cast(v4i, b[i]), acc, 0, 0, 0);
+    }
+  }
+  // lane l has token l & 15 and channels 4 (l >> 4) + 0..3
+  *reinterpret_cast<v4i*>(&sums[wave][lane & 15][4 * (lane >> 4)]) = acc;
+  __syncthreads();
+  constexpr int kLanes = 16 / T::kVec;  // threads of a token
+  const int m = threadIdx.x / kLanes, column = threadIdx.x % kLanes * T::kVec;
+  const int left = (int)std::min<int64_t>(T::kVec, args.outer - n0 - column);
+  if (m >= tokens || left <= 0) return;
+  int32_t sum[T::kVec];
+#pragma unroll
+  for (int e = 0; e < T::kVec; ++e) sum[e] = 0;
+#pragma unroll
+  for (int v = 0; v < 8; ++v)
+#pragma unroll
+    for (int h = 0; h < T::kVec; h += 4) {
+      const v4i part_sum = *reinterpret_cast<const v4i*>(&sums[v][m][column + h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[h + e] += part_sum[e];
+    }
+  float ws[T::kVec];
+  load_scales<T>(args, n0 + column, left, ws);
+  finish<T>(args, m, n0 + column, left, sum, ws);
+}
+
+// Rows that do not begin on multiples of 16 bytes, laid out so that they do;
+// 16 bytes a thread.
+struct AlignArgs {
+  const int8_t* src[kMaxRanks];
+  int64_t stride[kMaxRanks];
+  int8_t* dst[kMaxRanks];
+  int32_t first[kMaxRanks + 1];  // workgroups before a rank's
+  int32_t width[kMaxRanks];
+  int64_t rows;
+  int32_t nranks;
+};
+__global__ void __launch_bounds__(256) align_kernel(AlignArgs) {
+  const AlignArgs& args = kernel_args<AlignArgs>();
+  int i = 0;
+  while (i + 1 < args.nranks && args.first[i + 1] <= (int)blockIdx.x) ++i;
+  const int width = args.width[i], pieces = (width + 15) / 16;
+  const int64_t at = (int64_t)((int)blockIdx.x - args.first[i]) * 256 + threadIdx.x, row = at / pieces;
+  if (row >= args.rows) return;
+  const int k = (int)(at - row * pieces) * 16;
+  *reinterpret_cast<v4u*>(args.dst[i] + at * 16) = load_bytes(args.src[i] + row * args.stride[i] + k, width - k);
 }
 
 // ---- host --------------------------------------------------------------------
@@ -439,7 +624,13 @@ rar_result_t quantize(const void* const* xs, const int64_t* widths, const int64_
   a.scales = scales;
   a.nranks = nranks;
   const void* fn = dtype == kFloat32 ? reinterpret_cast<const void*>(&quantize_kernel<F32>) : reinterpret_cast<const void*>(&quantize_kernel<BF16>);
-  return launch_kernel(fn, dim3((unsigned)rows), dim3(256), &a, stream);
+  const int piece = 64 * (dtype == kFloat32 ? F32::kVec : BF16::kVec);
+  for (int r = 0; r < nranks; ++r) {
+    a.first[r] = a.pieces;
+    a.pieces += (int32_t)((widths[r] + piece - 1) / piece);
+  }
+  const int waves = rows < 1024 ? std::max(1, std::min(16, a.pieces)) : 4;
+  return launch_kernel(fn, dim3((unsigned)rows), dim3(64 * waves), &a, stream);
 }
 
 rar_result_t check_sizes(int64_t tokens, int64_t outer, int dtype) {
@@ -447,6 +638,56 @@ rar_result_t check_sizes(int64_t tokens, int64_t outer, int dtype) {
   if (tokens < 0 || tokens > kMaxTokens) return set_error(RAR_INVALID_ARGUMENT, "tokens must be in [0, 2^24]");
   if (outer < 1 || outer > kMaxOuter) return set_error(RAR_INVALID_ARGUMENT, "outer must be in [1, 2^24]");
   return RAR_SUCCESS;
+}
+
+// The kinds of kernel, and which a call takes.
+enum { kFew, kBig, k128x128, k64x128, k128x64 };
+struct Plan {
+  int kind, splits = 1;
+  int64_t align_x = 0, align_w = 0, partial = 0;  // bytes of workspace, in this order
+};
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+Plan plan_of(const int64_t* widths, int nranks, int64_t tokens, int64_t outer, bool align_x, bool align_w) {
+  Plan p;
+  int64_t steps = 0, padded = 0;
+  for (int r = 0; r < nranks; ++r) steps += (widths[r] + kDepth - 1) / kDepth, padded += round_up(widths[r], 16);
+  auto tiles = [&](int64_t m, int64_t n) { return (tokens + m - 1) / m * ((outer + n - 1) / n); };
+  if (tokens <= kFewTokens) p.kind = kFew;
+  else if (tokens <= 64) p.kind = k64x128;
+  else if (tiles(256, 256) >= 160) p.kind = kBig;
+  else if (tiles(128, 128) >= 300) p.kind = k128x128;
+  else p.kind = k128x64;
+  if (p.kind == kFew) return p;
+  const int64_t small = p.kind == k64x128 ? tiles(64, 128) : tiles(128, 64);
+  if (p.kind == k64x128 || p.kind == k128x64) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / small, steps / 6, 16}));
+  if (align_x && padded) p.align_x = round_up(tokens * padded, 256);
+  if (align_w && padded) p.align_w = round_up(outer * padded, 256);
+  if (p.splits > 1) p.partial = round_up(p.splits * tokens * outer * 4, 256);
+  return p;
+}
+// Whether tiles read an operand as it is: rows on multiples of 16 bytes, with
+// offsets of 32 bits within a tile.
+bool is_aligned(const int8_t* p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | stride) & 15) == 0 && stride < (1 << 24) - 256; }
+
+struct Kind {
+  int n, m, threads;
+  const void* fn;
+};
+template <class T, int kWN, int kWM, int kFN, int kFM, int kStages>
+Kind kind_of() {
+  typedef Tile<T, kWN, kWM, kFN, kFM, kStages> Own;
+  return {Own::kN, Own::kM, Own::kThreads, reinterpret_cast<const void*>(&tiles_kernel<T, kWN, kWM, kFN, kFM, kStages>)};
+}
+template <class T>
+Kind tile_kernel(int kind) {
+  switch (kind) {
+    case kFew: return {16, kFewTokens, 512, reinterpret_cast<const void*>(&few_kernel<T>)};
+    case kBig: return {256, 256, 512, reinterpret_cast<const void*>(&big_tiles_kernel<T>)};
+    case k64x128: return kind_of<T, 2, 2, 2, 1, 3>();
+    case k128x64: return kind_of<T, 2, 2, 1, 2, 3>();
+    default: return kind_of<T, 2, 2, 2, 2, 2>();
+  }
 }
 
 rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64_t* x_strides, const float* x_scales,
@@ -495,8 +736,6 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
     a.dst[k] = recvbufs[k];
     writes.push_back({recvbufs[k], tokens, outer * es, a.dst_stride[k] * es, "output"});
   }
-  if (rar_result_t r = check_blocks(reads, writes)) return r;
-  (void)workspace, (void)workspace_bytes;
   a.x_scales = x_scales;
   a.w_scales = weight_scales;
   a.residual = residual;
@@ -504,25 +743,69 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
   a.tokens = tokens;
   a.outer = outer;
   a.ndst = nrecv;
-  bool aligned = true;  // every row begins on a multiple of 16 bytes
+  bool align_x = false, align_w = false;
   for (int r = 0; r < a.nranks; ++r) {
     a.steps += (a.width[r] + kDepth - 1) / kDepth;
-    aligned = aligned && ((reinterpret_cast<uintptr_t>(a.x[r]) | reinterpret_cast<uintptr_t>(a.w[r]) | a.x_stride[r] | a.w_stride[r]) & 15) == 0;
+    align_x = align_x || !is_aligned(a.x[r], a.x_stride[r]);
+    align_w = align_w || !is_aligned(a.w[r], a.w_stride[r]);
   }
+  const Plan plan = plan_of(widths, nranks, tokens, outer, align_x, align_w);
+  const int64_t need = plan.align_x + plan.align_w + plan.partial;
+  if (need) {
+    if (rar_result_t r = check_pointer(workspace, 1, "workspace")) return r;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15) return set_error(RAR_INVALID_ARGUMENT, "workspace is not aligned to 16 bytes");
+    if (workspace_bytes < (size_t)need) return set_error(RAR_INVALID_ARGUMENT, "workspace is too small");
+    writes.push_back({workspace, 1, need, need, "workspace"});
+  }
+  if (rar_result_t r = check_blocks(reads, writes)) return r;
   const bool f32 = dtype == kFloat32;
-  const bool big = aligned && tokens > 128;
-  const int side = big ? kBig : kTile;
-  const int64_t tiles_m = (tokens + side - 1) / side, tiles_n = (outer + side - 1) / side, tiles = tiles_m * tiles_n;
-  if (tiles > 0x7FFFFFF0) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer is too large");
-  a.tiles_m = (int32_t)tiles_m;
-  a.tiles_n = (int32_t)tiles_n;
-  if (big) {
-    constexpr int kWaves = 8;
-    const void* fn = f32 ? reinterpret_cast<const void*>(&big_tile_kernel<F32, kWaves>) : reinterpret_cast<const void*>(&big_tile_kernel<BF16, kWaves>);
-    return launch_kernel(fn, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * kWaves), &a, stream);
+  const Kind k = f32 ? tile_kernel<F32>(plan.kind) : tile_kernel<BF16>(plan.kind);
+  a.tiles_m = (int32_t)((tokens + k.m - 1) / k.m);
+  int64_t tiles_n = (outer + k.n - 1) / k.n, grid = 0;
+  if (plan.kind == kBig) {
+    // as many columns of 256 channels as make whole rounds of the CUs, the
+    // rest in the size that leaves fewer of them idle
+    const int64_t round = 256 / std::gcd<int64_t>(256, a.tiles_m), all = tiles_n;
+    a.wide_n = (int32_t)(all / round * round);
+    const int64_t rest = outer - a.wide_n * 256;
+    auto cost = [&](int64_t width) { return (a.tiles_m * ((rest + width - 1) / width) + 255) / 256 * width; };
+    if (rest > 0 && cost(192) >= cost(256)) a.wide_n = (int32_t)all;
+    tiles_n = a.wide_n == all ? 0 : (rest + 191) / 192;
+    grid = (a.tiles_m * (int64_t)a.wide_n + 7) / 8 * 8;
   }
-  const void* fn = f32 ? reinterpret_cast<const void*>(&tile_kernel<F32>) : reinterpret_cast<const void*>(&tile_kernel<BF16>);
-  return launch_kernel(fn, dim3((unsigned)tiles), dim3(256), &a, stream);
+  a.tiles_n = (int32_t)tiles_n;
+  grid += (a.tiles_m * tiles_n + 7) / 8 * 8;
+  if (plan.kind == kFew) grid = tiles_n;
+  if (grid > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer is too large");
+  a.splits = plan.splits;
+  char* work = static_cast<char*>(workspace);
+  a.partial = reinterpret_cast<int32_t*>(work + plan.align_x + plan.align_w);
+  auto align = [&](const int8_t** p, int64_t* stride, int64_t rows, char* to) {
+    AlignArgs g{};
+    int64_t groups = 0;
+    for (int r = 0; r < a.nranks; ++r) {
+      const int64_t pitch = round_up(a.width[r], 16);
+      g.src[r] = p[r], g.stride[r] = stride[r], g.dst[r] = reinterpret_cast<int8_t*>(to);
+      g.width[r] = a.width[r];
+      p[r] = reinterpret_cast<int8_t*>(to), stride[r] = pitch;
+      to += rows * pitch;
+      groups += (rows * (pitch / 16) + 255) / 256;
+      if (groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens or outer times the widths is too large");
+      g.first[r + 1] = (int32_t)groups;
+    }
+    g.rows = rows;
+    g.nranks = a.nranks;
+    return launch_kernel(reinterpret_cast<const void*>(&align_kernel), dim3((unsigned)groups), dim3(256), &g, stream);
+  };
+  if (plan.align_x)
+    if (rar_result_t r = align(a.x, a.x_stride, tokens, work)) return r;
+  if (plan.align_w)
+    if (rar_result_t r = align(a.w, a.w_stride, outer, work + plan.align_x)) return r;
+  if (rar_result_t r = launch_kernel(k.fn, dim3((unsigned)grid, (unsigned)a.splits), dim3(k.threads), &a, stream)) return r;
+  if (a.splits == 1) return RAR_SUCCESS;
+  const int vec = f32 ? F32::kVec : BF16::kVec;
+  return launch_kernel(f32 ? reinterpret_cast<const void*>(&sum_kernel<F32>) : reinterpret_cast<const void*>(&sum_kernel<BF16>),
+                       dim3((unsigned)((outer + 256 * vec - 1) / (256 * vec)), (unsigned)tokens), dim3(256), &a, stream);
 }
 
 }  // namespace
@@ -548,13 +831,14 @@ rar_result_t rar_int8_projection_allreduce(const int8_t* const* xs, const int64_
 }
 
 rar_result_t rar_int8_projection_workspace(const int64_t* widths, int nranks, int64_t tokens, int64_t outer, rar_dtype_t dtype,
-                                           size_t* bytes) {
+                                           int aligned, size_t* bytes) {
   return rar::guarded([&]() -> rar_result_t {
     if (!bytes) return rar::set_error(RAR_INVALID_ARGUMENT, "bytes is NULL");
     int64_t total;
     if (rar_result_t r = rar::check_widths(widths, nranks, &total)) return r;
     if (rar_result_t r = rar::check_sizes(tokens, outer, dtype)) return r;
-    *bytes = 0;
+    const rar::Plan p = rar::plan_of(widths, nranks, tokens, outer, !aligned, !aligned);
+    *bytes = tokens ? (size_t)(p.align_x + p.align_w + p.partial) : 0;
     return RAR_SUCCESS;
   });
 }

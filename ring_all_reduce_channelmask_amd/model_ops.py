@@ -513,17 +513,39 @@ def quantize_rows(xs, quantized=None, scales=None, stream=None):
     handle, other = _on(dev, stream)
     int8, f32, device = _torch.int8, _torch.float32, like.device
     if quantized is None:
-        quantized = _new(other, lambda: [_torch.empty((rows, (k + 15) // 16 * 16), dtype=int8, device=device)[:, :k]
-                                         for k in widths])
+        # one buffer, the ranks' columns side by side
+        pitches, pitch, even = _pitches(widths)
+        held = _new(other, lambda: _torch.empty((rows, pitch), dtype=int8, device=device))
+        quantized = list(held.split(pitches, 1))
+        if not even:
+            quantized = [t[:, :k] for t, k in zip(quantized, widths)]
+        q_strides = (pitch,) * len(xs)
+    else:
+        q_widths, q_strides = _rows(quantized, rows, int8, dev, "quantized", False)
+        if q_widths != widths:
+            raise ValueError("quantized must have the widths of xs")
     if scales is None:
         scales = _new(other, lambda: _torch.empty(rows, dtype=f32, device=device))
-    q_widths, q_strides = _rows(quantized, rows, int8, dev, "quantized", False)
-    if q_widths != widths:
-        raise ValueError("quantized must have the widths of xs")
     _lib.check(_lib.load().rar_quantize_rows(
         _pointers(xs), _longs(widths), _longs(strides), len(xs), rows, dt, _pointers(quantized),
         _longs(q_strides), _vector(scales, rows, f32, dev, "scales", False), handle))
     return quantized, scales
+
+
+@functools.lru_cache(maxsize=1024)
+def _pitches(widths):
+    """Widths rounded up to multiples of 16, their sum, and whether all were."""
+    pitches = [(k + 15) // 16 * 16 for k in widths]
+    return pitches, sum(pitches), pitches == list(widths)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bits(strides):
+    """The low bits that strides have, all where one is beyond what tiles take."""
+    bits = 15 if max(strides) >= (1 << 24) - 256 else 0
+    for s in strides:
+        bits |= s & 15
+    return bits
 
 
 def int8_projection_allreduce(xs, x_scales, weights, weight_scales, recvs, residual=None,
@@ -551,12 +573,19 @@ def int8_projection_allreduce(xs, x_scales, weights, weight_scales, recvs, resid
     recv_ptrs, r_strides, copies = _copies(recvs, tokens, outer, dtype, dev, "recvs", False)
     res, res_stride = _single(residual, tokens, outer, dtype, dev, "residual", True)
     handle, other = _on(dev, stream)
-    need = _workspace("rar_int8_projection_workspace", widths, tokens, outer, dt)
+    x_ptrs, w_ptrs = _pointers(xs), _pointers(weights)
+    bits = _bits(x_strides) | _bits(w_strides)  # odd where too far apart
+    for p in x_ptrs:
+        bits |= p or 0
+    for p in w_ptrs:
+        bits |= p or 0
+    need = _workspace("rar_int8_projection_workspace", widths, tokens, outer, dt,
+                      int(bits & 15 == 0))
     work = None
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
     _lib.check(_lib.load().rar_int8_projection_allreduce(
-        _pointers(xs), _longs(widths), _longs(x_strides),
-        _vector(x_scales, tokens, f32, dev, "x_scales"), _pointers(weights), _longs(w_strides),
+        x_ptrs, _longs(widths), _longs(x_strides),
+        _vector(x_scales, tokens, f32, dev, "x_scales"), w_ptrs, _longs(w_strides),
         _vector(weight_scales, outer, f32, dev, "weight_scales"), len(xs), tokens, outer, dt, res,
         res_stride, recv_ptrs, r_strides, copies, work.data_ptr() if need else None, need, handle))

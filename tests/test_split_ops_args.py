@@ -217,11 +217,11 @@ def test_projection_refusals():
 
 def test_projection_workspace():
     lib, n = _lib.load(), ctypes.c_size_t()
-    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, BF16, ctypes.byref(n)) == OK
-    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, BF16, None) == BAD
-    assert lib.rar_int8_projection_workspace(None, 1, 5, 64, BF16, ctypes.byref(n)) == BAD
-    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 0, BF16, ctypes.byref(n)) == BAD
-    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, I32, ctypes.byref(n)) == BAD
+    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, BF16, 1, ctypes.byref(n)) == OK
+    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, BF16, 1, None) == BAD
+    assert lib.rar_int8_projection_workspace(None, 1, 5, 64, BF16, 1, ctypes.byref(n)) == BAD
+    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 0, BF16, 1, ctypes.byref(n)) == BAD
+    assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, I32, 1, ctypes.byref(n)) == BAD
 
 
 def test_the_binding_refuses_host_tensors_and_shapes():
