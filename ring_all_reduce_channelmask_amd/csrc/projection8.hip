@@ -190,26 +190,46 @@ struct ProjArgs {
   int32_t* partial;  // [splits][tokens][outer]
 };
 
-// 16 bytes of a row from p on, n (1 or more) of them there and zeros behind.
-// Fewer than 16 come as two overlapping pieces, neither beyond the n bytes.
-__device__ __forceinline__ v4u load_bytes(const int8_t* p, int n) {
-  typedef uint32_t v4u_byte __attribute__((ext_vector_type(4), aligned(1)));
+// n bytes (1 to 15) at several places, loaded together, zeros behind: two
+// pieces of each that overlap, neither beyond the n bytes.
+template <int kCount>
+__device__ __forceinline__ void load_ends(const int8_t* const* p, int n, v4u* to) {
   typedef uint64_t u64_byte __attribute__((aligned(1)));
   typedef uint32_t u32_byte __attribute__((aligned(1)));
   typedef uint16_t u16_byte __attribute__((aligned(1)));
-  if (n >= 16) return *reinterpret_cast<const v4u_byte*>(p);
-  uint64_t lo, hi = 0;
+  uint64_t lo[kCount], hi[kCount];
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) lo[i] = hi[i] = 0;
   if (n >= 8) {
-    lo = *reinterpret_cast<const u64_byte*>(p);
-    if (n > 8) hi = *reinterpret_cast<const u64_byte*>(p + n - 8) >> (8 * (16 - n));
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] = *reinterpret_cast<const u64_byte*>(p[i]), hi[i] = *reinterpret_cast<const u64_byte*>(p[i] + n - 8);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) hi[i] = n > 8 ? hi[i] >> (8 * (16 - n)) : 0;
   } else if (n >= 4) {
-    const uint64_t end = *reinterpret_cast<const u32_byte*>(p + n - 4);
-    lo = *reinterpret_cast<const u32_byte*>(p) | end << (8 * (n - 4));
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] = *reinterpret_cast<const u32_byte*>(p[i]), hi[i] = *reinterpret_cast<const u32_byte*>(p[i] + n - 4);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] |= hi[i] << (8 * (n - 4)), hi[i] = 0;
+  } else if (n >= 2) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] = (uint8_t)p[i][0], hi[i] = *reinterpret_cast<const u16_byte*>(p[i] + n - 2);
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] |= hi[i] << (8 * (n - 2)), hi[i] = 0;
   } else {
-    lo = (uint8_t)p[0];
-    if (n >= 2) lo |= (uint64_t)*reinterpret_cast<const u16_byte*>(p + n - 2) << (8 * (n - 2));
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) lo[i] = (uint8_t)p[i][0];
   }
-  return v4u{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) to[i] = v4u{(uint32_t)lo[i], (uint32_t)(lo[i] >> 32), (uint32_t)hi[i], (uint32_t)(hi[i] >> 32)};
+}
+
+// 16 bytes of a row from p on, n (1 or more) of them there and zeros behind.
+__device__ __forceinline__ v4u load_bytes(const int8_t* p, int n) {
+  typedef uint32_t v4u_byte __attribute__((ext_vector_type(4), aligned(1)));
+  if (n >= 16) return *reinterpret_cast<const v4u_byte*>(p);
+  v4u r;
+  load_ends<1>(&p, n, &r);
+  return r;
 }
 
 constexpr int kDepth = 128;  // bytes of the inner dimension that a step has
@@ -335,11 +355,23 @@ struct Tile {
         for (int i = 0; i < kLoadsX; ++i) to_lds(x0 + k0, ox[i], lds0 + stage * kStage + kN * kDepth + (i * kWaves + wave) * 1024);
       } else {  // a rank's last bytes, zeros behind
         const int mine = left - chunk * 16;
+        v4u some[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) some[i] = v4u{0, 0, 0, 0};
+        const int8_t* from[kLoads];
+        uint32_t to[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          const int8_t* from = i < kLoadsW ? w0 + ow[i < kLoadsW ? i : 0] : x0 + ox[i < kLoadsW ? 0 : i - kLoadsW];
-          const int at = i < kLoadsW ? i * kWaves : kN / 8 + (i - kLoadsW) * kWaves;
-          *reinterpret_cast<v4u*>(&lds[stage * kStage + (at + wave) * 1024 + lane * 16]) = mine > 0 ? load_bytes(from + k0, mine) : v4u{0, 0, 0, 0};
+          from[i] = i < kLoadsW ? w0 + k0 + ow[i < kLoadsW ? i : 0] : x0 + k0 + ox[i < kLoadsW ? 0 : i - kLoadsW];
+          to[i] = stage * kStage + ((i < kLoadsW ? i * kWaves : kN / 8 + (i - kLoadsW) * kWaves) + wave) * 1024;
+        }
+        if (mine >= 16) {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) to_lds(i < kLoadsW ? w0 + k0 : x0 + k0, i < kLoadsW ? ow[i < kLoadsW ? i : 0] : ox[i < kLoadsW ? 0 : i - kLoadsW], lds0 + to[i]);
+        } else {
+          if (mine > 0) load_ends<kLoads>(from, left & 15, some);
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) *reinterpret_cast<v4u*>(&lds[to[i] + lane * 16]) = some[i];
         }
       }
       next();
@@ -367,8 +399,8 @@ struct Tile {
     // the step any more, its place takes the step kStages further on, and the
     // next one is there.  Loads to LDS arrive in order: all but the youngest
     // kStages - 2 steps' have when as many are outstanding at most.  (A rank's
-    // last step may come through registers; what was issued before it has
-    // arrived when it is stored.)
+    // last step has as many, or bytes that come through registers: then what
+    // was issued before has arrived when they are stored.)
     auto meet = [](bool all) {
       if (kStages == 2 || all) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kStages - 2) * kLoads) : "memory");
@@ -629,7 +661,9 @@ rar_result_t quantize(const void* const* xs, const int64_t* widths, const int64_
     a.first[r] = a.pieces;
     a.pieces += (int32_t)((widths[r] + piece - 1) / piece);
   }
-  const int waves = rows < 1024 ? std::max(1, std::min(16, a.pieces)) : 4;
+  // as many waves as the device holds (8192), a wave for every kKept pieces
+  const int64_t most = std::max<int64_t>((a.pieces + kKept - 1) / kKept, 8192 / rows);
+  const int waves = (int)std::max<int64_t>(1, std::min<int64_t>({most, a.pieces, 16}));
   return launch_kernel(fn, dim3((unsigned)rows), dim3(64 * waves), &a, stream);
 }
 
