@@ -25,7 +25,7 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxNormWidth = 32768;
 constexpr int kMaxThreads = 1024;
-constexpr int kGroups = 512;  // workgroups of the gradient, at most
+typedef float v4f_user __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float wave_sum(float v) {
@@ -221,19 +221,45 @@ struct BackwardArgs {
   float eps, scale;
 };
 
-// Workgroup b takes pieces b, b + workgroups, ...; the sums over rows stay in
-// registers, a gate's until its piece ends, the weights' until the workgroup
-// ends.
+// A row's address, the same in all lanes, kept out of vector registers: the
+// lanes' offsets are added to it in the access.
+__device__ __forceinline__ char* row_at(const char* p, int64_t offset) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p) + offset;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return reinterpret_cast<char*>((uint64_t)hi << 32 | lo);
+}
+
+// This thread's elements of a row of sums.
+template <class T, int kVecs>
+__device__ __forceinline__ void store_sums(float* p, int width, const float (&sum)[kVecs][T::kVec]) {
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int e = (j * blockDim.x + threadIdx.x) * T::kVec;
+#pragma unroll
+    for (int i = 0; i < T::kVec; i += 4)
+      if (e + i < width) store4<F32>(reinterpret_cast<uint32_t*>(p + e + i), width - e - i, sum[j] + i);
+  }
+}
+
+// Workgroup b takes pieces b, b + workgroups, ...; the sums over rows stay on
+// the chip: dw_pre's in registers until the workgroup ends, and of a piece the
+// sum of d s q alone, from which come dg (times w_post) and dw_post (times g,
+// which is the same for all rows of a piece), the latter in LDS until the
+// workgroup ends.
 template <class T, int kVecs>
 __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
   __shared__ v2f scratch[2][kMaxThreads / 64];
+  __shared__ v4f dpost[T::kVec / 4 * kVecs][kMaxThreads];
   const int width = args.width, waves = blockDim.x >> 6;
-  float dpost[kVecs][T::kVec], dpre[kVecs][T::kVec], dgate[kVecs][T::kVec];
+  float dpre[kVecs][T::kVec], both[kVecs][T::kVec];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j)
+  for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
-    for (int i = 0; i < T::kVec; ++i) dpost[j][i] = dpre[j][i] = 0.0f;
+    for (int i = 0; i < T::kVec; ++i) dpre[j][i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T::kVec / 4; ++i) dpost[j * (T::kVec / 4) + i][threadIdx.x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   const bool need_s = args.post || args.dgate;
   for (int64_t piece = blockIdx.x; piece < args.pieces; piece += args.groups) {
     const int64_t group = piece / args.group_pieces, first = (piece - group * args.group_pieces) * args.piece_rows;
@@ -242,10 +268,10 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-      for (int i = 0; i < T::kVec; ++i) dgate[j][i] = 0.0f;
+      for (int i = 0; i < T::kVec; ++i) both[j][i] = 0.0f;
     for (int64_t row = row0; row < row1; ++row) {
       float d[kVecs][T::kVec];
-      Row<T, kVecs> s, w;
+      Row<T, kVecs> s, w, g;
       if (need_s) s.load(args.total, args.total_stride, row, width);
       sum_rows<T, kVecs>(args.grad_hidden, args.grad_hidden_stride, args.ngrad_hidden, row, width, d);
       if (args.ngrad_out) {
@@ -262,8 +288,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           w.widen(j, k);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            squares += f[i] * f[i];
-            dot += n[j][i] * k[i] * f[i];
+            squares = __builtin_fmaf(f[i], f[i], squares);
+            dot = __builtin_fmaf(n[j][i] * k[i], f[i], dot);
           }
         }
         block_sum2(squares, dot, scratch[0], waves);
@@ -276,8 +302,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           w.widen(j, k);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            dpre[j][i] += n[j][i] * f[i] * r;
-            d[j][i] += r * (n[j][i] * k[i] - f[i] * c);
+            dpre[j][i] = __builtin_fmaf(n[j][i], f[i] * r, dpre[j][i]);
+            d[j][i] = __builtin_fmaf(r, __builtin_fmaf(-f[i], c, n[j][i] * k[i]), d[j][i]);
           }
         }
       }
@@ -293,7 +319,6 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
         o.store(args.dresidual, args.dresidual_stride, row, width);
       }
       // d becomes v w_post (or v)
-      Row<T, kVecs> g;
       if (args.gate) g.load_shared(args.gate, args.gate_stride, group, width);
       if (args.post) {
         w.load_shared(args.post, 0, 0, width);
@@ -306,8 +331,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           if (args.gate) g.widen(j, a);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            squares += f[i] * f[i];
-            dot += d[j][i] * (args.gate ? a[i] : 1.0f) * k[i] * f[i];
+            squares = __builtin_fmaf(f[i], f[i], squares);
+            dot = __builtin_fmaf(d[j][i] * (args.gate ? a[i] : 1.0f) * k[i], f[i], dot);
           }
         }
         block_sum2(squares, dot, scratch[1], waves);
@@ -321,10 +346,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           if (args.gate) g.widen(j, a);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            const float v = d[j][i] * (args.gate ? a[i] : 1.0f), z = f[i] * q;
-            dgate[j][i] += d[j][i] * z * k[i];
-            dpost[j][i] += v * z;
-            d[j][i] = q * (v * k[i] - f[i] * c);
+            both[j][i] = __builtin_fmaf(d[j][i], f[i] * q, both[j][i]);
+            d[j][i] = q * __builtin_fmaf(-f[i], c, d[j][i] * (args.gate ? a[i] : 1.0f) * k[i]);
           }
         }
       } else if (args.gate) {
@@ -335,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           g.widen(j, a);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            if (args.dgate) dgate[j][i] += d[j][i] * f[i];
+            if (args.dgate) both[j][i] = __builtin_fmaf(d[j][i], f[i], both[j][i]);
             d[j][i] *= a[i];
           }
         }
@@ -350,35 +373,229 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
       // scratch, unless there is only one of the two
       if ((args.ngrad_out > 0) != (args.post != nullptr) && waves > 1) __syncthreads();
     }
+    if (args.dpost) {
+      Row<T, kVecs> g;
+      if (args.gate) g.load_shared(args.gate, args.gate_stride, group, width);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        float a[T::kVec];
+        if (args.gate) g.widen(j, a);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) dpost[(j * T::kVec + i) / 4][threadIdx.x][i % 4] += args.gate ? a[i] * both[j][i] : both[j][i];
+      }
+    }
     if (args.dgate) {
+      if (args.post) {
+        Row<T, kVecs> w;
+        w.load_shared(args.post, 0, 0, width);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+          float k[T::kVec];
+          w.widen(j, k);
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) both[j][i] *= k[i];
+        }
+      }
       if (args.group_pieces == 1) {
         Row<T, kVecs> o;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) o.set(j, dgate[j]);
+        for (int j = 0; j < kVecs; ++j) o.set(j, both[j]);
         o.store(args.dgate, args.dgate_stride, group, width);
       } else {
-        float* p = args.partial + (2 * args.groups + piece) * width;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          const int e = (j * blockDim.x + threadIdx.x) * T::kVec;
-#pragma unroll
-          for (int i = 0; i < T::kVec; i += 4)
-            if (e + i < width) store4<F32>(reinterpret_cast<uint32_t*>(p + e + i), width - e - i, dgate[j] + i);
-        }
+        store_sums<T, kVecs>(args.partial + (2 * args.groups + piece) * width, width, both);
       }
     }
   }
+  if (args.dpre) store_sums<T, kVecs>(args.partial + (2 * (int64_t)blockIdx.x + 1) * width, width, dpre);
+  if (args.dpost) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (which == 0 ? !args.dpost : !args.dpre) continue;
-    float* p = args.partial + (2 * (int64_t)blockIdx.x + which) * width;
+    for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int e = (j * blockDim.x + threadIdx.x) * T::kVec;
+      for (int i = 0; i < T::kVec; ++i) both[j][i] = dpost[(j * T::kVec + i) / 4][threadIdx.x][i % 4];
+    store_sums<T, kVecs>(args.partial + 2 * (int64_t)blockIdx.x * width, width, both);
+  }
+}
+
+// The same for rows of whole vectors, one a thread, and up to 4 gradients of
+// outs and one of hidden: the next row's loads are issued before a row is
+// reduced and none of them depends on a condition, so that the compiler's
+// waits are for the row in hand alone.  An absent input is another one read
+// again, and a thread behind the row's end has its last vector.
+template <class T>
+__global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(BackwardArgs) {
+  const BackwardArgs& args = kernel_args<BackwardArgs>();
+  constexpr int kOuts = 4;
+  typedef typename T::bits Bits;
+  struct Inputs {
+    v4u s, h, e, n[kOuts];
+  };
+  __shared__ v2f scratch[2][kMaxThreads / 64];
+  // a thread's own: pre, post, gate and its part of dpost (registers are needed
+  // for the rows)
+  extern __shared__ v4u own_lds[];
+  v4u* weights = own_lds + threadIdx.x;
+  v4f* dpost = reinterpret_cast<v4f*>(own_lds + 3 * blockDim.x) + threadIdx.x;
+  const int width = args.width, waves = blockDim.x >> 6;
+  const bool there = (int)threadIdx.x * T::kVec < width;
+  const uint32_t at = (there ? threadIdx.x * T::kVec : width - T::kVec) * (uint32_t)sizeof(Bits);
+  const bool has_out = args.ngrad_out > 0, has_hidden = args.ngrad_hidden > 0, need_s = args.post || args.dgate;
+  struct Source {
+    const char* p;
+    int64_t step;  // bytes
+  };
+  // some input that is there stands for those that are not
+  const Source some = has_out ? Source{static_cast<const char*>(args.grad_out[0]), args.grad_out_stride[0]}
+                              : Source{static_cast<const char*>(args.grad_hidden[0]), args.grad_hidden_stride[0]};
+  auto source = [&](bool is, const void* p, int64_t stride) {
+    return Source{is ? static_cast<const char*>(p) : some.p, (is ? stride : some.step) * (int64_t)sizeof(Bits)};
+  };
+  const Source from_s = source(need_s, args.total, args.total_stride), from_h = source(has_out, args.hidden, args.hidden_stride),
+               from_e = source(has_hidden, args.grad_hidden[0], args.grad_hidden_stride[0]),
+               from_n[kOuts] = {source(args.ngrad_out > 0, args.grad_out[0], args.grad_out_stride[0]),
+                                source(args.ngrad_out > 1, args.grad_out[1], args.grad_out_stride[1]),
+                                source(args.ngrad_out > 2, args.grad_out[2], args.grad_out_stride[2]),
+                                source(args.ngrad_out > 3, args.grad_out[3], args.grad_out_stride[3])};
+  auto load = [&](int64_t row, Inputs& in) {
+    in.h = load_nt(row_at(from_h.p, row * from_h.step) + at);
 #pragma unroll
-      for (int i = 0; i < T::kVec; i += 4)
-        if (e + i < width) store4<F32>(reinterpret_cast<uint32_t*>(p + e + i), width - e - i, (which == 0 ? dpost[j] : dpre[j]) + i);
+    for (int k = 0; k < kOuts; ++k) in.n[k] = load_nt(row_at(from_n[k].p, row * from_n[k].step) + at);
+    in.e = load_nt(row_at(from_e.p, row * from_e.step) + at);
+    in.s = load_nt(row_at(from_s.p, row * from_s.step) + at);
+  };
+  // 1 for weights that are not there
+  auto weight = [&](const void* p, int64_t offset) {
+    float one[T::kVec];
+#pragma unroll
+    for (int i = 0; i < T::kVec; ++i) one[i] = 1.0f;
+    return p ? load_16(reinterpret_cast<const char*>(static_cast<const Bits*>(p) + offset) + at) : T::round(one);
+  };
+  weights[0] = weight(has_out ? args.pre : nullptr, 0);
+  weights[blockDim.x] = weight(args.post, 0);
+  float dpre[T::kVec], both[T::kVec];
+#pragma unroll
+  for (int i = 0; i < T::kVec; ++i) dpre[i] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < T::kVec / 4; ++i) dpost[i * blockDim.x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t piece = blockIdx.x; piece < args.pieces; piece += args.groups) {
+    const int64_t group = piece / args.group_pieces, first = (piece - group * args.group_pieces) * args.piece_rows;
+    const int64_t row0 = group * args.group_rows + first;
+    const int64_t row1 = group * args.group_rows + std::min(args.group_rows, first + args.piece_rows);
+    weights[2 * blockDim.x] = weight(args.gate, group * args.gate_stride);
+#pragma unroll
+    for (int i = 0; i < T::kVec; ++i) both[i] = 0.0f;
+    auto one_row = [&](int64_t row, const Inputs& now, Inputs& ahead) {
+      load(std::min(row + 1, row1 - 1), ahead);
+      __builtin_amdgcn_sched_barrier(0);
+      float d[T::kVec], g[T::kVec];
+      if (has_out) {
+        float n[T::kVec], f[T::kVec], k[T::kVec];
+        T::widen(now.n[0], n);
+#pragma unroll
+        for (int o = 1; o < kOuts; ++o) {
+          float x[T::kVec];
+          T::widen(now.n[o], x);
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) n[i] = o < args.ngrad_out ? n[i] + x[i] : n[i];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        T::widen(now.h, f);
+        T::widen(weights[0], k);
+        float squares = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          squares = __builtin_fmaf(f[i], f[i], squares);
+          dot = __builtin_fmaf(n[i] * k[i], f[i], dot);
+        }
+        squares = there ? squares : 0.0f, dot = there ? dot : 0.0f;
+        block_sum2(squares, dot, scratch[0], waves);
+        const float r = rstd_of(squares, (float)width, args.eps);
+        const float c = dot / (float)width * r * r;
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          dpre[i] = __builtin_fmaf(n[i], f[i] * r, dpre[i]);
+          n[i] = __builtin_fmaf(-f[i], c, n[i] * k[i]);
+        }
+        T::widen(now.e, d);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(r, n[i], has_hidden ? d[i] : 0.0f);
+      } else {
+        T::widen(now.e, d);
+      }
+      if (args.dresidual && there) {
+        float f[T::kVec];
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) f[i] = args.scale * d[i];
+        store_nt(row_at(static_cast<char*>(args.dresidual), row * args.dresidual_stride * (int64_t)sizeof(Bits)) + at, T::round(f));
+      }
+      T::widen(weights[2 * blockDim.x], g);
+      float f[T::kVec];
+      T::widen(now.s, f);
+      if (args.post) {
+        float k[T::kVec];
+        T::widen(weights[blockDim.x], k);
+        float squares = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          squares = __builtin_fmaf(f[i], f[i], squares);
+          dot = __builtin_fmaf(d[i] * g[i] * k[i], f[i], dot);
+        }
+        squares = there ? squares : 0.0f, dot = there ? dot : 0.0f;
+        block_sum2(squares, dot, scratch[1], waves);
+        const float q = rstd_of(squares, (float)width, args.eps);
+        const float c = dot / (float)width * q * q;
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          both[i] = __builtin_fmaf(d[i], f[i] * q, both[i]);
+          d[i] = q * __builtin_fmaf(-f[i], c, d[i] * g[i] * k[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          both[i] = __builtin_fmaf(d[i], f[i], both[i]);
+          d[i] *= g[i];
+        }
+      }
+      if (there) {
+        const v4u o = T::round(d);
+        for (int k = 0; k < args.ndsrc; ++k) store_nt(row_at(static_cast<char*>(args.dsrc[k]), row * args.dsrc_stride[k] * (int64_t)sizeof(Bits)) + at, o);
+      }
+      // with several waves the barrier of one reduction frees the other's
+      // scratch, unless there is only one of the two
+      if (has_out != (args.post != nullptr) && waves > 1) __syncthreads();
+    };
+    Inputs in[2];
+    load(row0, in[0]);
+    for (int64_t row = row0; row < row1; row += 2) {
+      one_row(row, in[0], in[1]);
+      if (row + 1 < row1) one_row(row + 1, in[1], in[0]);
     }
+    if (!there) continue;
+    if (args.dpost) {
+      float g[T::kVec];
+      T::widen(weights[2 * blockDim.x], g);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) dpost[i / 4 * blockDim.x][i % 4] += g[i] * both[i];
+    }
+    if (args.dgate) {
+      float k[T::kVec];
+      T::widen(weights[blockDim.x], k);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
+      if (args.group_pieces == 1) {
+        store_nt(reinterpret_cast<char*>(static_cast<Bits*>(args.dgate) + group * args.dgate_stride) + at, T::round(both));
+      } else {
+        float* p = args.partial + (2 * args.groups + piece) * width + threadIdx.x * T::kVec;
+#pragma unroll
+        for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), 4, both + i);
+      }
+    }
+  }
+  if (!there) return;
+  float* p = args.partial + 2 * (int64_t)blockIdx.x * width + threadIdx.x * T::kVec;
+#pragma unroll
+  for (int i = 0; i < T::kVec; i += 4) {
+    if (args.dpre) store4<F32>(reinterpret_cast<uint32_t*>(p + width + i), 4, dpre + i);
+    if (args.dpost) *reinterpret_cast<v4f_user*>(p + i) = dpost[i / 4 * blockDim.x];
   }
 }
 
@@ -456,8 +673,7 @@ rar_result_t check_norm(const rar_norm_t* n) {
   return RAR_SUCCESS;
 }
 
-// Pieces of the rows: up to kGroups in all where a group has more than one,
-// at least 4 rows each.
+// Pieces of the rows.
 struct Pieces {
   int64_t group_rows, piece_rows, group_pieces, pieces, groups, bytes;
 };
@@ -465,11 +681,15 @@ Pieces pieces_of(const rar_norm_t& n) {
   Pieces p;
   const int64_t gates = n.gate ? n.gate_groups : 1;
   p.group_rows = n.rows / gates;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kGroups / gates, p.group_rows / 4));
+  // as many workgroups as the device holds (16 waves a CU), their pieces of 8
+  // rows or more where there are many
+  const int waves = launch_of(n.width, n.dtype).threads / 64;
+  const int64_t most = 256 * (16 / waves), least = n.rows <= 512 ? 1 : n.rows <= 1024 ? 2 : n.rows <= 2048 ? 4 : 8;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most / gates, p.group_rows / least));
   p.piece_rows = (p.group_rows + want - 1) / want;
   p.group_pieces = p.piece_rows ? (p.group_rows + p.piece_rows - 1) / p.piece_rows : 1;
   p.pieces = gates * p.group_pieces;
-  p.groups = std::min<int64_t>(p.pieces, kGroups);
+  p.groups = std::min<int64_t>(p.pieces, most);
   p.bytes = (2 * p.groups + (p.group_pieces > 1 ? p.pieces : 0)) * n.width * 4;
   return p;
 }
@@ -618,8 +838,13 @@ rar_result_t backward(const rar_norm_t* norm, const void* const* grad_hidden, co
   a.eps = n.eps, a.scale = n.residual_scale;
   if (n.rows > 0) {
     const Launch l = launch_of(n.width, n.dtype);
-    if (rar_result_t r = launch_kernel(n.dtype == kFloat32 ? norm_kernel<F32>(l.vecs, true) : norm_kernel<BF16>(l.vecs, true),
-                                       dim3((unsigned)p.groups), dim3(l.threads), &a, stream)) return r;
+    const bool f32 = n.dtype == kFloat32;
+    const bool ahead = l.vecs == 1 && n.width % (f32 ? F32::kVec : BF16::kVec) == 0 && ngrad_hidden <= 1 && ngrad_outs <= 4;
+    const void* fn = f32 ? norm_kernel<F32>(l.vecs, true) : norm_kernel<BF16>(l.vecs, true);
+    if (ahead) fn = f32 ? reinterpret_cast<const void*>(&norms_backward_ahead_kernel<F32>) : reinterpret_cast<const void*>(&norms_backward_ahead_kernel<BF16>);
+    const unsigned lds = ahead ? l.threads * (unsigned)(3 + (f32 ? F32::kVec : BF16::kVec) / 4) * 16 : 0;
+    if (rar_result_t r = launch_kernel(fn,
+                                       dim3((unsigned)p.groups), dim3(l.threads), &a, stream, lds)) return r;
   }
   // Without rows the sums over them are zero, the join's over no parts.
   const bool join_gate = dgate && (n.rows == 0 || p.group_pieces > 1);

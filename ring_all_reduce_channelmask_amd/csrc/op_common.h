@@ -106,9 +106,9 @@ rar_result_t guarded(F&& body) {
   }
 }
 
-inline rar_result_t launch_kernel(const void* fn, dim3 grid, dim3 block, void* args, void* stream) {
+inline rar_result_t launch_kernel(const void* fn, dim3 grid, dim3 block, void* args, void* stream, unsigned lds_bytes = 0) {
   void* params[] = {args};
-  const hipError_t e = hipLaunchKernel(fn, grid, block, params, 0, reinterpret_cast<hipStream_t>(stream));
+  const hipError_t e = hipLaunchKernel(fn, grid, block, params, lds_bytes, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return set_error(RAR_HIP_ERROR, std::string("kernel launch failed: ") + hipGetErrorString(e));
   return RAR_SUCCESS;
 }
