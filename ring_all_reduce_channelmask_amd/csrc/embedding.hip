@@ -17,9 +17,10 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 constexpr int64_t kMaxWidth = int64_t(1) << 24;
+typedef float v4f_user __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kRow = 512;        // 16-bit elements of a wave's piece of a row (256 of 32 bits)
 constexpr int kSmallTokens = 1024;  // up to here a group's positions are found by looking at all ids
-constexpr int kRankTokens = 16384;  // up to here the order comes from comparing all pairs
+constexpr int kRankTokens = 8192;  // up to here the order comes from comparing all pairs
 
 // Where the ranks' rows begin in the vocabulary; first[nranks] is its size.
 struct Split {
@@ -91,14 +92,14 @@ struct BackwardArgs {
   const int64_t* ids;
   int32_t* keys[2];    // ids in order, those outside the vocabulary last as its size
   int32_t* places[2];  // their positions
-  uint32_t* counts;    // of the radix sort: [blocks][256]
+  uint32_t* counts;    // of the radix sort: [blocks][kDigits]
   float* partial;      // [2 * chunks][width]: groups cut by a chunk's start, its end
   int64_t tokens, width;
   int64_t slices;      // pieces of a row, one a wave
   int64_t sum_groups;  // workgroups that sum; the others fill
   float scale;
   int32_t ngrads, accumulate, chunk, chunks, sorted;  // sorted: which of keys/places is in order
-  int32_t shift, blocks;
+  int32_t shift, blocks, fill_rows;
   Split split;
 };
 
@@ -133,30 +134,35 @@ struct TableRow {
   }
 };
 
-// Add the rows `place` (n of them, lane i holds the i-th) of every gradient to
-// sum, in that order, this lane's n_elems elements from e on.
-template <class T, int kBatch>
-__device__ __forceinline__ void add_rows(const BackwardArgs& args, int32_t place, int begin, int end, int64_t e, int n_elems, float* sum) {
-  for (int i0 = begin; i0 < end; i0 += kBatch) {
-    for (int k = 0; k < args.ngrads; ++k) {
-      const typename T::bits* src = static_cast<const typename T::bits*>(args.grad[k]);
-      const int64_t stride = args.grad_stride[k];
-      v4u x[kBatch];
+// Add up rows begin to end - 1 of a list (place_of gives the i-th's position)
+// of every gradient, in that order, this lane's n elements from e on; `done`
+// gets each row's end.  Loads are issued kBatch at a time, whatever the rows
+// belong to.
+template <class T, int kBatch, class P, class F>
+__device__ __forceinline__ void add_rows(const BackwardArgs& args, int begin, int end, int64_t e, int n, float* sum, P place_of, F done) {
+  int i = begin, k = 0;
+  while (i < end) {
+    v4u x[kBatch];
+    int at = i, copy = k;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        x[i] = v4u{0, 0, 0, 0};
-        if (i0 + i < end) {
-          const int64_t row = __builtin_amdgcn_readlane(place, i0 + i);
-          if (n_elems > 0) x[i] = load_part<T>(src + row * stride + e, n_elems, 0);
-        }
+    for (int j = 0; j < kBatch; ++j) {
+      x[j] = v4u{0, 0, 0, 0};
+      if (at < end) {
+        const typename T::bits* src = static_cast<const typename T::bits*>(args.grad[copy]) + place_of(at) * args.grad_stride[copy];
+        if (n > 0) x[j] = load_part<T>(src + e, n, 0);
+        if (++copy == args.ngrads) copy = 0, ++at;
       }
+    }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (i0 + i < end) {
-          float f[T::kVec];
-          T::widen(x[i], f);
+    for (int j = 0; j < kBatch; ++j) {
+      if (i < end) {
+        float f[T::kVec];
+        T::widen(x[j], f);
 #pragma unroll
-          for (int c = 0; c < T::kVec; ++c) sum[c] += f[c];
+        for (int c = 0; c < T::kVec; ++c) sum[c] += f[c];
+        if (++k == args.ngrads) {
+          done(i);
+          k = 0, ++i;
         }
       }
     }
@@ -172,62 +178,81 @@ __device__ __forceinline__ void zero_row(const BackwardArgs& args, int32_t v, in
     store_part<G>(p + e, (int)(args.width - e > G::kVec ? G::kVec : args.width - e), v4u{0, 0, 0, 0});
 }
 
-constexpr int kFillRows = 64;  // table rows that a filling workgroup looks at
+constexpr int kFillRows = 64;  // table rows that a filling workgroup looks at, at most
 
-// Few tokens, one launch.  A summing wave takes a token and a piece of its
-// row: if no earlier token is the same, it adds up all that are.  A filling
-// workgroup zeroes those of its rows that no token has.
+// Few tokens, one launch.  A summing workgroup takes a token and a piece of
+// its row: if no earlier token is the same, it lists all that are, and each
+// wave adds up a run of them.  A filling workgroup zeroes those of its rows
+// that no token has.
 template <class T, class G>
 __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kRounds = kSmallTokens / 256;
+  __shared__ int32_t list[kSmallTokens];
+  __shared__ int32_t counts[kRounds][4];
+  __shared__ float parts[3][64 * T::kVec];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t vocab = args.split.first[args.split.nranks], tokens = (int32_t)args.tokens;
+  int32_t keys[kRounds];  // of tokens threadIdx.x, 256 + threadIdx.x, ...; loaded together
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int32_t u = i * 256 + threadIdx.x;
+    keys[i] = u < tokens ? key_of(args.ids[u], vocab) : vocab;
+  }
   if (blockIdx.x >= args.sum_groups) {
-    __shared__ uint32_t used[kFillRows];
-    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * kFillRows;
+    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
+    int32_t* used = list;
     if (threadIdx.x < kFillRows) used[threadIdx.x] = 0;
     __syncthreads();
-    for (int t = threadIdx.x; t < tokens; t += 256) {
-      const int32_t key = key_of(args.ids[t], vocab);
-      if (key >= r0 && key < r0 + kFillRows && key < vocab) used[key - r0] = 1;
-    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (keys[i] >= r0 && keys[i] < r1) used[keys[i] - r0] = 1;
     __syncthreads();
-    for (int i = wave; i < kFillRows && r0 + i < vocab; i += 4)
+    for (int i = wave; r0 + i < r1; i += 4)
       if (!used[i]) zero_row<G>(args, r0 + i, lane);
     return;
   }
-  const int64_t item = (int64_t)blockIdx.x * 4 + wave;
-  const int32_t t = (int32_t)(item / args.slices);
-  if (t >= tokens) return;
-  const int64_t e = (item - t * args.slices) * (64 * T::kVec) + lane * T::kVec;
-  const int n = (int)(args.width - e >= T::kVec ? T::kVec : args.width - e < 0 ? 0 : args.width - e);
+  const int32_t t = (int32_t)(blockIdx.x / args.slices);
   const int32_t key = key_of(args.ids[t], vocab);
   if (key == vocab) return;
-  for (int32_t u0 = 0; u0 < t; u0 += 64) {
-    const int32_t u = u0 + lane;
-    if (__ballot(u < t && key_of(args.ids[u], vocab) == key)) return;
+  uint64_t same[kRounds];
+  bool earlier = false;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    same[i] = __ballot(keys[i] == key);
+    earlier = earlier || (keys[i] == key && i * 256 + (int32_t)threadIdx.x < t);
+    if (lane == 0) counts[i][wave] = __popcll(same[i]);
   }
+  if (__syncthreads_or(earlier)) return;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w == wave && (same[i] >> lane & 1)) list[total + __popcll(same[i] & ((uint64_t(1) << lane) - 1))] = i * 256 + threadIdx.x;
+      total += counts[i][w];
+    }
+  __syncthreads();
+  const int64_t e = (blockIdx.x - t * args.slices) * (64 * T::kVec) + lane * T::kVec;
+  const int n = (int)(args.width - e >= T::kVec ? T::kVec : args.width - e < 0 ? 0 : args.width - e);
   float sum[T::kVec];
 #pragma unroll
   for (int c = 0; c < T::kVec; ++c) sum[c] = 0.0f;
-  // the group's positions, 64 at a time: lane i gets the i-th
-  int32_t place = t, have = 1;
-  for (int32_t u0 = t + 1; u0 < tokens; u0 += 64) {
-    const int32_t u = u0 + lane;
-    uint64_t same = __ballot(u < tokens && key_of(args.ids[u < tokens ? u : t], vocab) == key);
-    while (same) {
-      const int i = __builtin_ctzll(same);
-      same &= same - 1;
-      if (have == 64) {
-        add_rows<T, 8>(args, place, 0, 64, e, n, sum);
-        have = 0;
-      }
-      if (lane == have) place = u0 + i;
-      ++have;
+  total = __builtin_amdgcn_readfirstlane(total);
+  add_rows<T, 16>(args, (total * wave + 3) / 4, (total * (wave + 1) + 3) / 4, e, n, sum,
+                 [&](int i) { return (int64_t)__builtin_amdgcn_readfirstlane(list[i]); }, [](int) {});
+  if (total > 1) {  // otherwise the first wave has the only row
+    if (wave > 0) {
+#pragma unroll
+      for (int c = 0; c < T::kVec; ++c) parts[wave - 1][c * 64 + lane] = sum[c];
     }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int c = 0; c < T::kVec; ++c) sum[c] += parts[w][c * 64 + lane];
   }
-  add_rows<T, 8>(args, place, 0, have, e, n, sum);
-  TableRow<T, G>::put(args, TableRow<T, G>::at(args, key, e), n, sum);
+  if (wave == 0) TableRow<T, G>::put(args, TableRow<T, G>::at(args, key, e), n, sum);
 }
 
 // The order of up to kRankTokens tokens: each one's place is the number of
@@ -273,81 +298,101 @@ __global__ void __launch_bounds__(1024) rank_kernel(BackwardArgs) {
   }
 }
 
-// More tokens: a radix sort, 8 bits of the key a pass.  `blocks` workgroups
+// More tokens: a radix sort, 9 bits of the key a pass.  `blocks` workgroups
 // each take a run of tokens; count_kernel counts their digits, place_kernel
 // puts each token behind the smaller digits, the same digit of earlier runs
 // and of earlier tokens of its own.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits, kSortThreads = 1024;
+
 __device__ __forceinline__ void run_of(const BackwardArgs& args, int64_t* begin, int64_t* end) {
-  const int64_t len = ((args.tokens + args.blocks - 1) / args.blocks + 255) & ~int64_t(255);
+  const int64_t len = (args.tokens + args.blocks - 1) / args.blocks;
   *begin = std::min<int64_t>(args.tokens, blockIdx.x * len);
   *end = std::min<int64_t>(args.tokens, *begin + len);
 }
 __device__ __forceinline__ int32_t sort_key(const BackwardArgs& args, int64_t t, int32_t vocab) {
   return args.shift == 0 ? key_of(args.ids[t], vocab) : args.keys[1 - args.sorted][t];
 }
-__global__ void __launch_bounds__(256) count_kernel(BackwardArgs) {
+__global__ void __launch_bounds__(kSortThreads) count_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
-  __shared__ uint32_t counts[256];
+  __shared__ uint32_t counts[kDigits];
   const int32_t vocab = args.split.first[args.split.nranks];
-  counts[threadIdx.x] = 0;
+  if (threadIdx.x < kDigits) counts[threadIdx.x] = 0;
   __syncthreads();
   int64_t begin, end;
   run_of(args, &begin, &end);
-  for (int64_t t = begin + threadIdx.x; t < end; t += 256)
-    atomicAdd(&counts[(sort_key(args, t, vocab) >> args.shift) & 255], 1u);
+#pragma unroll 4
+  for (int64_t t = begin + threadIdx.x; t < end; t += kSortThreads)
+    atomicAdd(&counts[(sort_key(args, t, vocab) >> args.shift) & (kDigits - 1)], 1u);
   __syncthreads();
-  args.counts[blockIdx.x * 256 + threadIdx.x] = counts[threadIdx.x];
+  if (threadIdx.x < kDigits) args.counts[blockIdx.x * kDigits + threadIdx.x] = counts[threadIdx.x];
 }
-__global__ void __launch_bounds__(256) place_kernel(BackwardArgs) {
+__global__ void __launch_bounds__(kSortThreads) place_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
-  __shared__ uint32_t next[256], seen[4][256], sums[4];
+  constexpr int kWaves = kSortThreads / 64, kHalves = kSortThreads / kDigits;
+  __shared__ uint32_t next[kDigits], seen[kWaves][kDigits], sums[kWaves], half[kHalves][2][kDigits];
   const int32_t vocab = args.split.first[args.split.nranks];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t before = 0, total = 0;
-#pragma unroll 8
-  for (int b = 0; b < args.blocks; ++b) {
-    const uint32_t c = args.counts[b * 256 + threadIdx.x];
-    before += b < (int)blockIdx.x ? c : 0;
-    total += c;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mine = threadIdx.x % kDigits;
+  {  // digit `mine`: in the runs before this one, and in all; each half of the threads takes every other run
+    uint32_t before = 0, total = 0;
+#pragma unroll 16
+    for (int b = threadIdx.x / kDigits; b < args.blocks; b += kHalves) {
+      const uint32_t c = args.counts[b * kDigits + mine];
+      before += b < (int)blockIdx.x ? c : 0;
+      total += c;
+    }
+    half[threadIdx.x / kDigits][0][mine] = before;
+    half[threadIdx.x / kDigits][1][mine] = total;
   }
-  uint32_t upto = total;
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t other = __shfl_up(upto, d);
-    if (lane >= d) upto += other;
-  }
-  if (lane == 63) sums[wave] = upto;
   __syncthreads();
-  uint32_t start = upto - total + before;
-  for (int w = 0; w < wave; ++w) start += sums[w];
-  next[threadIdx.x] = start;
+  uint32_t before = 0, total = 0, upto = 0;
+  if (threadIdx.x < kDigits) {
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) before += half[h][0][mine], total += half[h][1][mine];
+    upto = total;
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t other = __shfl_up(upto, d);
+      if (lane >= d) upto += other;
+    }
+    if (lane == 63) sums[wave] = upto;
+  }
+  __syncthreads();
+  if (threadIdx.x < kDigits) {
+    uint32_t start = upto - total + before;
+    for (int w = 0; w < wave; ++w) start += sums[w];
+    next[mine] = start;
+  }
   int64_t begin, end;
   run_of(args, &begin, &end);
-  for (int64_t t0 = begin; t0 < end; t0 += 256) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) seen[w][threadIdx.x] = 0;
+  for (int64_t t0 = begin; t0 < end; t0 += kSortThreads) {
+    for (int i = threadIdx.x; i < kWaves * kDigits; i += kSortThreads) seen[0][i] = 0;
     __syncthreads();
     const int64_t t = t0 + threadIdx.x;
     const bool in = t < end;
     const int32_t key = in ? sort_key(args, t, vocab) : 0;
     const int32_t place = !in ? 0 : args.shift == 0 ? (int32_t)t : args.places[1 - args.sorted][t];
-    const int digit = (key >> args.shift) & 255;
+    const int digit = (key >> args.shift) & (kDigits - 1);
     uint64_t same = __ballot(in);
 #pragma unroll
-    for (int bit = 0; bit < 8; ++bit) {
+    for (int bit = 0; bit < kDigitBits; ++bit) {
       const uint64_t ones = __ballot(digit >> bit & 1);
       same &= digit >> bit & 1 ? ones : ~ones;
     }
-    const int mine = __popcll(same & ((uint64_t(1) << lane) - 1));
-    if (in && mine == 0) seen[wave][digit] = __popcll(same);
+    const int above = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (in && above == 0) seen[wave][digit] = __popcll(same);
     __syncthreads();
-    uint32_t at = 0;
-    if (in) {
-      at = next[digit] + mine;
-      for (int w = 0; w < wave; ++w) at += seen[w][digit];
+    if (threadIdx.x < kDigits) {  // where each wave's tokens of the digit begin
+      uint32_t at = next[mine];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const uint32_t c = seen[w][mine];
+        seen[w][mine] = at;
+        at += c;
+      }
+      next[mine] = at;
     }
     __syncthreads();
-    next[threadIdx.x] += seen[0][threadIdx.x] + seen[1][threadIdx.x] + seen[2][threadIdx.x] + seen[3][threadIdx.x];
     if (in) {
+      const uint32_t at = seen[wave][digit] + above;
       args.keys[args.sorted][at] = key;
       args.places[args.sorted][at] = place;
     }
@@ -381,16 +426,15 @@ __global__ void __launch_bounds__(256) sum_kernel(BackwardArgs) {
   const int32_t* keys = args.keys[args.sorted];
   if (blockIdx.x >= args.sum_groups) {
     __shared__ uint32_t used[kFillRows];
-    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * kFillRows;
+    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
     if (threadIdx.x < kFillRows) used[threadIdx.x] = 0;
     __syncthreads();
     if (wave == 0) {
-      const int32_t r1 = std::min(vocab, r0 + kFillRows);
       const int64_t end = lower_bound(keys, args.tokens, r1, lane);
       for (int64_t i = lower_bound(keys, args.tokens, r0, lane) + lane; i < end; i += 64) used[keys[i] - r0] = 1;
     }
     __syncthreads();
-    for (int i = wave; i < kFillRows && r0 + i < vocab; i += 4)
+    for (int i = wave; r0 + i < r1; i += 4)
       if (!used[i]) zero_row<G>(args, r0 + i, lane);
     return;
   }
@@ -404,44 +448,48 @@ __global__ void __launch_bounds__(256) sum_kernel(BackwardArgs) {
   const int32_t key = lane < len ? keys[i0 + lane] : vocab;
   const int32_t place = lane < len ? args.places[args.sorted][i0 + lane] : 0;
   const int32_t last = i0 > 0 ? keys[i0 - 1] : -1, next = i0 + len < args.tokens ? keys[i0 + len] : -1;
-  const int32_t up = __shfl_up(key, 1);
-  // lane i starts a group, or the rest that is outside the vocabulary
-  uint64_t starts = __ballot(lane < len && (lane == 0 || key != up));
-  while (starts) {
-    const int begin = __builtin_ctzll(starts);
-    starts &= starts - 1;
-    const int end = starts ? __builtin_ctzll(starts) : len;
-    const int32_t v = __builtin_amdgcn_readlane(key, begin);
-    if (v == vocab) break;
-    float sum[T::kVec];
+  // lanes that end a group, the chunk's last token among them; those outside
+  // the vocabulary are behind all others
+  const int32_t down = __shfl_down(key, 1);
+  const int used = __popcll(__ballot(lane < len && key != vocab));
+  const uint64_t ends = __ballot(lane < used && (lane == used - 1 || key != down));
+  float sum[T::kVec];
 #pragma unroll
-    for (int i = 0; i < T::kVec; ++i) sum[i] = 0.0f;
-    add_rows<T, 8>(args, place, begin, end, e, n, sum);
-    const bool from = begin == 0 && last == v, on = end == len && next == v;
-    if (from || on) {
-      float* p = args.partial + (2 * c + !from) * args.width + e;
+  for (int i = 0; i < T::kVec; ++i) sum[i] = 0.0f;
+  int begin = 0;
+  add_rows<T, 8>(args, 0, used, e, n, sum, [&](int i) { return (int64_t)__builtin_amdgcn_readlane(place, i); },
+                 [&](int i) {
+                   if (!(ends >> i & 1)) return;
+                   const int32_t v = __builtin_amdgcn_readlane(key, i);
+                   const bool from = begin == 0 && last == v, on = i + 1 == len && next == v;
+                   if (from || on) {
+                     float* p = args.partial + (2 * c + !from) * args.width + e;
 #pragma unroll
-      for (int j = 0; j < T::kVec / 4; ++j) store4<F32>(reinterpret_cast<uint32_t*>(p + 4 * j), n - 4 * j, sum + 4 * j);
-    } else {
-      TableRow<T, G>::put(args, TableRow<T, G>::at(args, v, e), n, sum);
-    }
-  }
+                     for (int j = 0; j < T::kVec / 4; ++j) store4<F32>(reinterpret_cast<uint32_t*>(p + 4 * j), n - 4 * j, sum + 4 * j);
+                   } else {
+                     TableRow<T, G>::put(args, TableRow<T, G>::at(args, v, e), n, sum);
+                   }
+#pragma unroll
+                   for (int j = 0; j < T::kVec; ++j) sum[j] = 0.0f;
+                   begin = i + 1;
+                 });
 }
 
 // The groups cut by chunks: the workgroup of the chunk where one begins adds
-// up its parts for 256 columns, each of 16 waves a run of them.
+// up its parts for kJoinColumns columns, each of kJoinWaves waves a run of them.
+constexpr int kJoinWaves = 4, kJoinColumns = 512, kJoinVecs = kJoinColumns / 256;
 template <class T, class G>
-__global__ void __launch_bounds__(1024) join_kernel(BackwardArgs) {
+__global__ void __launch_bounds__(64 * kJoinWaves) join_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
-  __shared__ float parts[16][256];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float parts[kJoinWaves][kJoinColumns];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t vocab = args.split.first[args.split.nranks];
   const int32_t* keys = args.keys[args.sorted];
-  const int64_t slices = (args.width + 255) / 256;
-  const int64_t c = blockIdx.x / slices, e = (blockIdx.x - c * slices) * 256 + lane * 4;
+  const int64_t slices = (args.width + kJoinColumns - 1) / kJoinColumns;
+  const int64_t c = blockIdx.x / slices, e = (blockIdx.x - c * slices) * kJoinColumns + lane * 4;
   const int64_t i0 = c * args.chunk, i1 = i0 + args.chunk;  // not the last chunk
-  const int32_t v = keys[i1 - 1];
-  if (v == vocab || keys[i1] != v || (keys[i0] == v && i0 > 0 && keys[i0 - 1] == v)) return;
+  const int32_t v = keys[i1 - 1], first = keys[i0], before = i0 > 0 ? keys[i0 - 1] : -1;
+  if (v == vocab || keys[i1] != v || (first == v && before == v)) return;
   // chunks c + 1 ... c + more hold the rest of the group
   int64_t more = 0;
   for (;; more += 64) {
@@ -452,30 +500,46 @@ __global__ void __launch_bounds__(1024) join_kernel(BackwardArgs) {
       break;
     }
   }
-  const int n = (int)(args.width - e >= 4 ? 4 : args.width - e < 0 ? 0 : args.width - e);
   // part 0 is the chunk's own, part j that of chunk c + j
-  const int64_t each = (more + 1 + 15) / 16, j0 = wave * each, j1 = std::min<int64_t>(more + 1, j0 + each);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int64_t j = j0; j < j1; ++j) {
-    float f[4];
-    load4<F32>(reinterpret_cast<const uint32_t*>(args.partial + (j == 0 ? 2 * c + 1 : 2 * (c + j)) * args.width + e), n, f);
+  const int64_t each = (more + kJoinWaves) / kJoinWaves, j0 = wave * each, j1 = std::min<int64_t>(more + 1, j0 + each);
+  float sum[kJoinVecs * 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] += f[i];
+  for (int i = 0; i < kJoinVecs * 4; ++i) sum[i] = 0.0f;
+  constexpr int kBatch = 8;
+  for (int64_t b = j0; b < j1; b += kBatch) {
+    v4f_user x[kBatch][kJoinVecs];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t j = std::min(b + i, j1 - 1);
+      const float* p = args.partial + (j == 0 ? 2 * c + 1 : 2 * (c + j)) * args.width;
+      // beyond the row's end there is the next one, or the slack behind the last
+#pragma unroll
+      for (int h = 0; h < kJoinVecs; ++h) x[i][h] = *reinterpret_cast<const v4f_user*>(p + (e + h * 256 < args.width ? e + h * 256 : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (b + i < j1)
+#pragma unroll
+        for (int h = 0; h < kJoinVecs; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[h * 4 + k] += x[i][h][k];
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) parts[wave][lane * 4 + i] = sum[i];
-  __syncthreads();
-  if (threadIdx.x >= 256) return;
-  float all = 0.0f;
+  for (int h = 0; h < kJoinVecs; ++h)
 #pragma unroll
-  for (int w = 0; w < 16; ++w) all += parts[w][threadIdx.x];
-  const int64_t column = (blockIdx.x % slices) * 256 + threadIdx.x;
-  if (column >= args.width) return;
-  typename G::bits* p = TableRow<T, G>::at(args, v, column);
-  float f = all * args.scale;
-  if (args.accumulate) f += G::widen1(*p);
-  *p = G::round1(f);
+    for (int i = 0; i < 4; ++i) parts[wave][h * 256 + lane * 4 + i] = sum[h * 4 + i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kJoinColumns; i += 64 * kJoinWaves) {
+    const int64_t column = (blockIdx.x - c * slices) * kJoinColumns + i;
+    if (column >= args.width) return;
+    float all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) all += parts[w][i];
+    typename G::bits* p = TableRow<T, G>::at(args, v, column);
+    float f = all * args.scale;
+    if (args.accumulate) f += G::widen1(*p);
+    *p = G::round1(f);
+  }
 }
 
 // ---- host --------------------------------------------------------------------
@@ -496,10 +560,10 @@ Shape shape_of(int64_t tokens, int64_t width, int64_t vocab) {
   while (s.chunk > 8 && tokens / s.chunk * slices < 8192) s.chunk /= 2;
   s.chunks = (int32_t)((tokens + s.chunk - 1) / s.chunk);
   while ((vocab >> s.bits) != 0) ++s.bits;
-  s.blocks = (int32_t)std::min<int64_t>(256, (tokens + 1023) / 1024);
+  s.blocks = (int32_t)std::min<int64_t>(256, (tokens + kSortThreads - 1) / kSortThreads);
   s.keys = align_up(tokens * 4);
-  s.counts = align_up(256 * 256 * 4);
-  s.partial = align_up(2 * (int64_t)s.chunks * width * 4);
+  s.counts = align_up((int64_t)s.blocks * kDigits * 4);
+  s.partial = align_up(2 * (int64_t)s.chunks * width * 4 + 16);
   s.bytes = 4 * s.keys + s.counts + s.partial;
   return s;
 }
@@ -573,15 +637,14 @@ template <class T, class G>
 rar_result_t launch_sums(BackwardArgs& a, int64_t fill_groups, void* stream) {
   const bool small = a.tokens <= kSmallTokens;
   a.slices = (a.width + 64 * T::kVec - 1) / (64 * T::kVec);
-  const int64_t items = (small ? a.tokens : a.chunks) * a.slices;
-  a.sum_groups = (items + 3) / 4;
+  a.sum_groups = small ? a.tokens * a.slices : (a.chunks * a.slices + 3) / 4;
   if (a.sum_groups + fill_groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
   const dim3 grid((unsigned)(a.sum_groups + fill_groups));
   if (small) return launch_kernel(reinterpret_cast<const void*>(&few_tokens_kernel<T, G>), grid, dim3(256), &a, stream);
   if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&sum_kernel<T, G>), grid, dim3(256), &a, stream)) return r;
-  const int64_t joins = (int64_t)(a.chunks - 1) * ((a.width + 255) / 256);
+  const int64_t joins = (int64_t)(a.chunks - 1) * ((a.width + kJoinColumns - 1) / kJoinColumns);
   if (joins > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
-  return launch_kernel(reinterpret_cast<const void*>(&join_kernel<T, G>), dim3((unsigned)joins), dim3(1024), &a, stream);
+  return launch_kernel(reinterpret_cast<const void*>(&join_kernel<T, G>), dim3((unsigned)joins), dim3(64 * kJoinWaves), &a, stream);
 }
 
 rar_result_t backward(const void* const* grads, const int64_t* grad_strides, int ngrads, int64_t tokens, int64_t width, int dtype,
@@ -645,14 +708,16 @@ rar_result_t backward(const void* const* grads, const int64_t* grad_strides, int
     if (tokens <= kRankTokens) {
       if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&rank_kernel), dim3((unsigned)((tokens + 63) / 64)), dim3(1024), &a, stream)) return r;
     } else {
-      for (a.shift = 0; a.shift < s.bits; a.shift += 8) {
-        a.sorted = (a.shift / 8) & 1;
-        if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&count_kernel), dim3(s.blocks), dim3(256), &a, stream)) return r;
-        if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&place_kernel), dim3(s.blocks), dim3(256), &a, stream)) return r;
+      for (a.shift = 0; a.shift < s.bits; a.shift += kDigitBits) {
+        a.sorted = (a.shift / kDigitBits) & 1;
+        if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&count_kernel), dim3(s.blocks), dim3(kSortThreads), &a, stream)) return r;
+        if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&place_kernel), dim3(s.blocks), dim3(kSortThreads), &a, stream)) return r;
       }
     }
   }
-  const int64_t fill = accumulate ? 0 : (vocab + kFillRows - 1) / kFillRows;
+  // enough workgroups for all CUs where the vocabulary is small
+  a.fill_rows = (int32_t)std::max<int64_t>(4, std::min<int64_t>(kFillRows, vocab / 2048));
+  const int64_t fill = accumulate ? 0 : (vocab + a.fill_rows - 1) / a.fill_rows;
   if (dtype == kFloat32) return launch_sums<F32, F32>(a, fill, stream);
   return table_dtype == kFloat32 ? launch_sums<BF16, F32>(a, fill, stream) : launch_sums<BF16, BF16>(a, fill, stream);
 }
