@@ -309,13 +309,14 @@ def _table_rows(ts, width, dtype, dev, what, read=True):
         raise ValueError(f"{what} must be a list of tensors")
     rows, strides = [], []
     for t in ts:
-        if t.dim() != 2 or t.shape[1] != width:
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != width:
             raise ValueError(f"{what} must be [rows, {width}] tensors")
-        rows.append(t.shape[0])
-        if t.shape[0] == 0 and t.dtype is dtype and t.get_device() == dev:
+        rows.append(shape[0])
+        if shape[0] == 0 and t.dtype is dtype and t.get_device() == dev:
             strides.append(width)  # a rank without rows: its strides mean nothing
         else:
-            strides.append(_rows((t,), t.shape[0], dtype, dev, what, read)[1][0])
+            strides.append(_rows((t,), shape[0], dtype, dev, what, read)[1][0])
     return tuple(rows), tuple(strides)
 
 
@@ -331,14 +332,11 @@ def embedding_allreduce(tables, ids, recvs, scale=1.0, stream=None):
         raise ValueError("tables must be [rows, width] tensors and ids a [tokens] one")
     dtype, width, tokens = like.dtype, like.size(1), ids.size(0)
     rows, strides = _table_rows(tables, width, dtype, dev, "tables")
-    widths, r_strides = _rows(recvs, tokens, dtype, dev, "recvs", False)
-    if widths != (width,) * len(recvs):
-        raise ValueError(f"recvs must be [{tokens}, {width}] tensors")
     handle, _ = _on(dev, stream)
     _lib.check(_lib.load().rar_embedding_allreduce(
         _pointers(tables), _longs(rows), _longs(strides), len(tables), width, dt,
-        _vector(ids, tokens, _torch.int64, dev, "ids", False), tokens, scale, _pointers(recvs),
-        _longs(r_strides), len(recvs), handle))
+        _vector(ids, tokens, _torch.int64, dev, "ids", False), tokens, scale,
+        *_copies(recvs, tokens, width, dtype, dev, "recvs", False), handle))
 
 
 def embedding_allreduce_backward(grads, ids, dtables, scale=1.0, accumulate=False, stream=None):
@@ -353,9 +351,7 @@ def embedding_allreduce_backward(grads, ids, dtables, scale=1.0, accumulate=Fals
     if like.dim() != 2:
         raise ValueError("grads must be [tokens, width] tensors")
     dtype, (tokens, width) = like.dtype, like.shape
-    widths, g_strides = _rows(grads, tokens, dtype, dev, "grads")
-    if widths != (width,) * len(grads):
-        raise ValueError(f"grads must be [{tokens}, {width}] tensors")
+    grad_args = _copies(grads, tokens, width, dtype, dev, "grads", True)
     if not isinstance(dtables, (list, tuple)) or not dtables or \
             dtables[0].dtype not in (dtype, _torch.float32):
         raise ValueError(f"dtables must be a list of {dtype} or float32 tensors")
@@ -367,23 +363,21 @@ def embedding_allreduce_backward(grads, ids, dtables, scale=1.0, accumulate=Fals
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
     _lib.check(_lib.load().rar_embedding_allreduce_backward(
-        _pointers(grads), _longs(g_strides), len(grads), tokens, width, dt,
+        *grad_args, tokens, width, dt,
         _vector(ids, tokens, _torch.int64, dev, "ids", False), scale, _pointers(dtables),
         _longs(rows), _longs(strides), len(dtables), _DTYPE[out_dtype], int(bool(accumulate)),
         work.data_ptr() if need else None, need, handle))
 
 
 def _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, pre_weight):
-    """The arguments that a norm and its gradient share; the second value
-    keeps a reshaped gate alive."""
+    """The arguments that a norm and its gradient share."""
     def weight(t, what):
         return None if t is None else _vector(t, width, dtype, dev, what)
-    n = _lib.Norm(rows=rows, width=width, dtype=dt, eps=eps, residual_scale=residual_scale,
-                  post_weight=weight(post_weight, "post_weight"),
-                  pre_weight=weight(pre_weight, "pre_weight"))
+    at, groups, stride = None, 0, 0
     if gate is not None and rows:
-        n.gate, n.gate_groups, n.gate_stride = _gate(gate, width, dtype, dev, "gate")
-    return n
+        at, groups, stride = _gate(gate, width, dtype, dev, "gate")
+    return _lib.Norm(rows, width, dt, eps, residual_scale, 0, weight(post_weight, "post_weight"),
+                     weight(pre_weight, "pre_weight"), at, groups, stride)
 
 
 def _gate(t, width, dtype, dev, what, read=True):
@@ -399,12 +393,23 @@ def _copies(ts, rows, width, dtype, dev, what, read):
     """Addresses, strides and number of [rows, width] tensors (none allowed)."""
     if not isinstance(ts, (list, tuple)):
         raise ValueError(f"{what} must be a list of tensors")
-    if not ts:
+    n = len(ts)
+    if n == 0:
         return None, None, 0
+    if n > 64:
+        raise ValueError("at most 64 tensors of a kind")
+    # what most calls have, checked at once; _rows says what is wrong with others
+    shape, strides, recorded = (rows, width), (width, 1), read and _torch.is_grad_enabled()
+    for t in ts:
+        if t.stride() != strides or t.shape != shape or t.dtype is not dtype or \
+                t.get_device() != dev or (recorded and t.requires_grad):
+            break
+    else:
+        return _ARRAYS[n](*[t.data_ptr() for t in ts]), _longs((width,) * n), n
     widths, strides = _rows(ts, rows, dtype, dev, what, read)
-    if widths != (width,) * len(ts):
+    if widths != (width,) * n:
         raise ValueError(f"{what} must be [{rows}, {width}] tensors")
-    return _pointers(ts), _longs(strides), len(ts)
+    return _pointers(ts), _longs(strides), n
 
 
 def _single(t, rows, width, dtype, dev, what, read):
@@ -415,6 +420,15 @@ def _single(t, rows, width, dtype, dev, what, read):
     if widths != (width,):
         raise ValueError(f"{what} must be a [{rows}, {width}] tensor")
     return t.data_ptr(), strides[0]
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(rows, width, dt, groups):
+    """Bytes of workspace of a norm's gradient."""
+    need = ctypes.c_size_t()
+    n = _lib.Norm(rows, width, dt, 1.0, 1.0, 0, None, None, 1 << 40 if groups else None, groups, 0)
+    _lib.check(_lib.load().rar_norm_workspace(ctypes.byref(n), ctypes.byref(need)))
+    return need.value
 
 
 def norm_allreduce(partials, hidden, outs, residual=None, residual_scale=1.0, post_weight=None,
@@ -482,9 +496,7 @@ def norm_allreduce_backward(grad_hidden, grad_outs, dpartials, total=None, hidde
         else:
             dgate.zero_()
     handle, other = _on(dev, stream)
-    lib, need = _lib.load(), ctypes.c_size_t()
-    _lib.check(lib.rar_norm_workspace(ctypes.byref(n), ctypes.byref(need)))
-    need = need.value
+    lib, need = _lib.load(), _norm_workspace(rows, width, dt, n.gate_groups)
     work = None
     if need:
         work = _new(other, lambda: _torch.empty(need, dtype=_torch.uint8, device=like.device))
