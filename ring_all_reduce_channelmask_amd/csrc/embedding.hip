@@ -59,13 +59,11 @@ __global__ void __launch_bounds__(256) embedding_kernel(ForwardArgs) {
     const int r = args.split.rank_of((int32_t)id);
     const typename T::bits* src = static_cast<const typename T::bits*>(args.table[r]) + (id - args.split.first[r]) * args.table_stride[r];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int64_t e = e0 + j * (256 * T::kVec);
-      if (e < args.width) v[j] = load_part<T>(src + e, (int)(args.width - e > T::kVec ? T::kVec : args.width - e), 0);
-    }
+    for (int j = 0; j < kVecs; ++j) v[j] = RowEdge<T>(e0 + j * (256 * T::kVec), args.width).load_shared(src);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       float f[T::kVec];
+      RowEdge<T>(e0 + j * (256 * T::kVec), args.width).fix(v[j]);
       T::widen(v[j], f);
 #pragma unroll
       for (int i = 0; i < T::kVec; ++i) f[i] *= args.scale;
@@ -135,11 +133,12 @@ struct TableRow {
 };
 
 // Add up rows begin to end - 1 of a list (place_of gives the i-th's position)
-// of every gradient, in that order, this lane's n elements from e on; `done`
+// of every gradient, in that order, this lane's elements from e on; `done`
 // gets each row's end.  Loads are issued kBatch at a time, whatever the rows
 // belong to.
 template <class T, int kBatch, class P, class F>
-__device__ __forceinline__ void add_rows(const BackwardArgs& args, int begin, int end, int64_t e, int n, float* sum, P place_of, F done) {
+__device__ __forceinline__ void add_rows(const BackwardArgs& args, int begin, int end, int64_t e, float* sum, P place_of, F done) {
+  const RowEdge<T> edge(e, args.width);
   int i = begin, k = 0;
   while (i < end) {
     v4u x[kBatch];
@@ -148,8 +147,7 @@ __device__ __forceinline__ void add_rows(const BackwardArgs& args, int begin, in
     for (int j = 0; j < kBatch; ++j) {
       x[j] = v4u{0, 0, 0, 0};
       if (at < end) {
-        const typename T::bits* src = static_cast<const typename T::bits*>(args.grad[copy]) + place_of(at) * args.grad_stride[copy];
-        if (n > 0) x[j] = load_part<T>(src + e, n, 0);
+        x[j] = edge.load(static_cast<const typename T::bits*>(args.grad[copy]) + place_of(at) * args.grad_stride[copy]);
         if (++copy == args.ngrads) copy = 0, ++at;
       }
     }
@@ -157,6 +155,7 @@ __device__ __forceinline__ void add_rows(const BackwardArgs& args, int begin, in
     for (int j = 0; j < kBatch; ++j) {
       if (i < end) {
         float f[T::kVec];
+        edge.fix(x[j]);
         T::widen(x[j], f);
 #pragma unroll
         for (int c = 0; c < T::kVec; ++c) sum[c] += f[c];
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
   for (int i = 0; i < kRounds; ++i)
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (w == wave && (same[i] >> lane & 1)) list[total + __popcll(same[i] & ((uint64_t(1) << lane) - 1))] = i * 256 + threadIdx.x;
+      if (w == wave && keys[i] == key) list[total + bits_below(same[i])] = i * 256 + threadIdx.x;
       total += counts[i][w];
     }
   __syncthreads();
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
 #pragma unroll
   for (int c = 0; c < T::kVec; ++c) sum[c] = 0.0f;
   total = __builtin_amdgcn_readfirstlane(total);
-  add_rows<T, 16>(args, (total * wave + 3) / 4, (total * (wave + 1) + 3) / 4, e, n, sum,
+  add_rows<T, 16>(args, (total * wave + 3) / 4, (total * (wave + 1) + 3) / 4, e, sum,
                  [&](int i) { return (int64_t)__builtin_amdgcn_readfirstlane(list[i]); }, [](int) {});
   if (total > 1) {  // otherwise the first wave has the only row
     if (wave > 0) {
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kSortThreads) place_kernel(BackwardArgs) {
       const uint64_t ones = __ballot(digit >> bit & 1);
       same &= digit >> bit & 1 ? ones : ~ones;
     }
-    const int above = __popcll(same & ((uint64_t(1) << lane) - 1));
+    const int above = bits_below(same);
     if (in && above == 0) seen[wave][digit] = __popcll(same);
     __syncthreads();
     if (threadIdx.x < kDigits) {  // where each wave's tokens of the digit begin
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(256) sum_kernel(BackwardArgs) {
 #pragma unroll
   for (int i = 0; i < T::kVec; ++i) sum[i] = 0.0f;
   int begin = 0;
-  add_rows<T, 8>(args, 0, used, e, n, sum, [&](int i) { return (int64_t)__builtin_amdgcn_readlane(place, i); },
+  add_rows<T, 8>(args, 0, used, e, sum, [&](int i) { return (int64_t)__builtin_amdgcn_readlane(place, i); },
                  [&](int i) {
                    if (!(ends >> i & 1)) return;
                    const int32_t v = __builtin_amdgcn_readlane(key, i);

@@ -25,7 +25,6 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxNormWidth = 32768;
 constexpr int kMaxThreads = 1024;
-typedef float v4f_user __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float wave_sum(float v) {
@@ -50,24 +49,22 @@ __device__ __forceinline__ float rstd_of(float squares, float width, float eps) 
 template <class T, int kVecs>
 struct Row {
   v4u v[kVecs];
+  static __device__ __forceinline__ RowEdge<T> edge(int j, int width) { return RowEdge<T>((j * blockDim.x + threadIdx.x) * T::kVec, width); }
   __device__ __forceinline__ void load(const void* buf, int64_t stride, int64_t row, int width) {
     const typename T::bits* p = static_cast<const typename T::bits*>(buf) + row * stride;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int e = (j * blockDim.x + threadIdx.x) * T::kVec;
-      v[j] = e < width ? load_part<T>(p + e, width - e, 0) : v4u{0, 0, 0, 0};
-    }
+    for (int j = 0; j < kVecs; ++j) v[j] = edge(j, width).load(p);
   }
   // data that other workgroups read too
   __device__ __forceinline__ void load_shared(const void* buf, int64_t stride, int64_t row, int width) {
     const typename T::bits* p = static_cast<const typename T::bits*>(buf) + row * stride;
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const int e = (j * blockDim.x + threadIdx.x) * T::kVec;
-      v[j] = v4u{0, 0, 0, 0};
-      if (e + T::kVec <= width) v[j] = load_16(p + e);
-      else if (e < width) v[j] = load_part<T>(p + e, width - e, 0);
-    }
+    for (int j = 0; j < kVecs; ++j) v[j] = edge(j, width).load_shared(p);
+  }
+  // Once, between a load and the first use.
+  __device__ __forceinline__ void fix(int width) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) edge(j, width).fix(v[j]);
   }
   __device__ __forceinline__ void widen(int j, float* f) const { T::widen(v[j], f); }
   __device__ __forceinline__ void set(int j, const float* f) { v[j] = T::round(f); }
@@ -98,6 +95,7 @@ __device__ __forceinline__ void sum_rows(const void* const* bufs, const int64_t*
 #pragma unroll
     for (int r = 0; r < kBatch; ++r) {
       if (r0 + r < n) {
+        x[r].fix(width);
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float f[T::kVec];
@@ -151,6 +149,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
       for (int i = 0; i < T::kVec; ++i) squares += h[j][i] * h[j][i];
     block_sum2(squares, none, scratch[0], waves);
     const float q = rstd_of(squares, (float)width, args.eps);
+    w.fix(width);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       float f[T::kVec];
@@ -160,6 +159,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
     }
   }
   if (args.gate) {
+    g.fix(width);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       float f[T::kVec];
@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
     }
   }
   if (args.residual) {
+    x.fix(width);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       float f[T::kVec];
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
     for (int i = 0; i < T::kVec; ++i) squares += h[j][i] * h[j][i];
   block_sum2(squares, none, scratch[1], waves);
   const float r = rstd_of(squares, (float)width, args.eps);
+  w.fix(width);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     float f[T::kVec];
@@ -220,14 +222,6 @@ struct BackwardArgs {
   int32_t width, ngrad_hidden, ngrad_out, ndsrc;
   float eps, scale;
 };
-
-// A row's address, the same in all lanes, kept out of vector registers: the
-// lanes' offsets are added to it in the access.
-__device__ __forceinline__ char* row_at(const char* p, int64_t offset) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p) + offset;
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return reinterpret_cast<char*>((uint64_t)hi << 32 | lo);
-}
 
 // This thread's elements of a row of sums.
 template <class T, int kVecs>
@@ -280,6 +274,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
         float n[kVecs][T::kVec];
         sum_rows<T, kVecs>(args.grad_out, args.grad_out_stride, args.ngrad_out, row, width, n);
         w.load_shared(args.pre, 0, 0, width);
+        h.fix(width);
+        w.fix(width);
         float squares = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
@@ -320,8 +316,11 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
       }
       // d becomes v w_post (or v)
       if (args.gate) g.load_shared(args.gate, args.gate_stride, group, width);
+      if (args.gate) g.fix(width);
+      if (need_s) s.fix(width);
       if (args.post) {
         w.load_shared(args.post, 0, 0, width);
+        w.fix(width);
         float squares = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
@@ -376,6 +375,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
     if (args.dpost) {
       Row<T, kVecs> g;
       if (args.gate) g.load_shared(args.gate, args.gate_stride, group, width);
+      if (args.gate) g.fix(width);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
         float a[T::kVec];
@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
       if (args.post) {
         Row<T, kVecs> w;
         w.load_shared(args.post, 0, 0, width);
+        w.fix(width);
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float k[T::kVec];
@@ -416,12 +417,13 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
   }
 }
 
-// The same for rows of whole vectors, one a thread, and up to 4 gradients of
-// outs and one of hidden: the next row's loads are issued before a row is
-// reduced and none of them depends on a condition, so that the compiler's
+// The same for rows of one vector a thread: the next row's loads (of total,
+// hidden, a gradient of hidden and up to 4 of outs) are issued before a row is
+// reduced, and none of them depends on a condition, so that the compiler's
 // waits are for the row in hand alone.  An absent input is another one read
-// again, and a thread behind the row's end has its last vector.
-template <class T>
+// again, and the row's end is as RowEdge has it (kEdge: it is not where a
+// wave's vectors end).  Further gradients (kMore) are read where they are added.
+template <class T, bool kEdge, bool kMore>
 __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
   constexpr int kOuts = 4;
@@ -436,8 +438,18 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
   v4u* weights = own_lds + threadIdx.x;
   v4f* dpost = reinterpret_cast<v4f*>(own_lds + 3 * blockDim.x) + threadIdx.x;
   const int width = args.width, waves = blockDim.x >> 6;
-  const bool there = (int)threadIdx.x * T::kVec < width;
-  const uint32_t at = (there ? threadIdx.x * T::kVec : width - T::kVec) * (uint32_t)sizeof(Bits);
+  const int e = threadIdx.x * T::kVec, at_e = std::min(e, width - T::kVec), shift = std::min(e - at_e, T::kVec);
+  const bool there = e < width;
+  const int left = width - e;  // of it, more than a vector in all threads but the last
+  const uint32_t at = at_e * (uint32_t)sizeof(Bits);
+  // only waves with the row's end have something to shift
+  const bool edge = kEdge && __ballot(shift > 0) != 0;
+  auto fix = [&](v4u v) { return shift_elements<T>(v, shift); };
+  auto put = [&](void* p, int64_t offset, const float* f) {
+    char* row = row_at(static_cast<char*>(p), offset * (int64_t)sizeof(Bits));
+    if (!kEdge || left >= T::kVec) store_nt(row + at, T::round(f));
+    else if (there) store_part<T>(reinterpret_cast<Bits*>(row) + e, left, T::round(f));
+  };
   const bool has_out = args.ngrad_out > 0, has_hidden = args.ngrad_hidden > 0, need_s = args.post || args.dgate;
   struct Source {
     const char* p;
@@ -467,7 +479,26 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
     float one[T::kVec];
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) one[i] = 1.0f;
-    return p ? load_16(reinterpret_cast<const char*>(static_cast<const Bits*>(p) + offset) + at) : T::round(one);
+    const v4u v = p ? load_16(reinterpret_cast<const char*>(static_cast<const Bits*>(p) + offset) + at) : T::round(one);
+    return edge ? fix(v) : v;
+  };
+  // sum += what the k-th and further buffers have in a row
+  auto add_more = [&](const void* const* bufs, const int64_t* strides, int k, int n, int64_t row, float* sum) {
+    for (; k < n; k += kOuts) {
+      v4u x[kOuts];
+#pragma unroll
+      for (int o = 0; o < kOuts; ++o) {
+        const int from = std::min(k + o, n - 1);
+        x[o] = load_nt(row_at(static_cast<const char*>(bufs[from]), row * strides[from] * (int64_t)sizeof(Bits)) + at);
+      }
+#pragma unroll
+      for (int o = 0; o < kOuts; ++o) {
+        float f[T::kVec];
+        T::widen(edge ? fix(x[o]) : x[o], f);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) sum[i] = k + o < n ? sum[i] + f[i] : sum[i];
+      }
+    }
   };
   weights[0] = weight(has_out ? args.pre : nullptr, 0);
   weights[blockDim.x] = weight(args.post, 0);
@@ -483,9 +514,20 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
     weights[2 * blockDim.x] = weight(args.gate, group * args.gate_stride);
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) both[i] = 0.0f;
-    auto one_row = [&](int64_t row, const Inputs& now, Inputs& ahead) {
+    auto one_row = [&](int64_t row, Inputs& now, Inputs& ahead) {
+      float more[T::kVec];  // of the gradients of outs
+      if (kMore && args.ngrad_out > kOuts) {
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) more[i] = 0.0f;
+        add_more(args.grad_out, args.grad_out_stride, kOuts, args.ngrad_out, row, more);
+      }
       load(std::min(row + 1, row1 - 1), ahead);
       __builtin_amdgcn_sched_barrier(0);
+      if (edge) {
+        now.s = fix(now.s), now.h = fix(now.h), now.e = fix(now.e);
+#pragma unroll
+        for (int k = 0; k < kOuts; ++k) now.n[k] = fix(now.n[k]);
+      }
       float d[T::kVec], g[T::kVec];
       if (has_out) {
         float n[T::kVec], f[T::kVec], k[T::kVec];
@@ -498,6 +540,10 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
           for (int i = 0; i < T::kVec; ++i) n[i] = o < args.ngrad_out ? n[i] + x[i] : n[i];
         }
         __builtin_amdgcn_sched_barrier(0);
+        if (kMore && args.ngrad_out > kOuts) {
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) n[i] += more[i];
+        }
         T::widen(now.h, f);
         T::widen(weights[0], k);
         float squares = 0.0f, dot = 0.0f;
@@ -506,7 +552,6 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
           squares = __builtin_fmaf(f[i], f[i], squares);
           dot = __builtin_fmaf(n[i] * k[i], f[i], dot);
         }
-        squares = there ? squares : 0.0f, dot = there ? dot : 0.0f;
         block_sum2(squares, dot, scratch[0], waves);
         const float r = rstd_of(squares, (float)width, args.eps);
         const float c = dot / (float)width * r * r;
@@ -517,15 +562,19 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
         }
         T::widen(now.e, d);
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(r, n[i], has_hidden ? d[i] : 0.0f);
+        for (int i = 0; i < T::kVec; ++i) d[i] = has_hidden ? d[i] : 0.0f;
+        if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(r, n[i], d[i]);
       } else {
         T::widen(now.e, d);
+        if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
       }
-      if (args.dresidual && there) {
+      if (args.dresidual) {
         float f[T::kVec];
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) f[i] = args.scale * d[i];
-        store_nt(row_at(static_cast<char*>(args.dresidual), row * args.dresidual_stride * (int64_t)sizeof(Bits)) + at, T::round(f));
+        put(args.dresidual, row * args.dresidual_stride, f);
       }
       T::widen(weights[2 * blockDim.x], g);
       float f[T::kVec];
@@ -539,7 +588,6 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
           squares = __builtin_fmaf(f[i], f[i], squares);
           dot = __builtin_fmaf(d[i] * g[i] * k[i], f[i], dot);
         }
-        squares = there ? squares : 0.0f, dot = there ? dot : 0.0f;
         block_sum2(squares, dot, scratch[1], waves);
         const float q = rstd_of(squares, (float)width, args.eps);
         const float c = dot / (float)width * q * q;
@@ -555,10 +603,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
           d[i] *= g[i];
         }
       }
-      if (there) {
-        const v4u o = T::round(d);
-        for (int k = 0; k < args.ndsrc; ++k) store_nt(row_at(static_cast<char*>(args.dsrc[k]), row * args.dsrc_stride[k] * (int64_t)sizeof(Bits)) + at, o);
-      }
+      for (int k = 0; k < args.ndsrc; ++k) put(args.dsrc[k], row * args.dsrc_stride[k], d);
       // with several waves the barrier of one reduction frees the other's
       // scratch, unless there is only one of the two
       if (has_out != (args.post != nullptr) && waves > 1) __syncthreads();
@@ -582,20 +627,23 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
 #pragma unroll
       for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
       if (args.group_pieces == 1) {
-        store_nt(reinterpret_cast<char*>(static_cast<Bits*>(args.dgate) + group * args.dgate_stride) + at, T::round(both));
+        put(args.dgate, group * args.dgate_stride, both);
       } else {
-        float* p = args.partial + (2 * args.groups + piece) * width + threadIdx.x * T::kVec;
+        float* p = args.partial + (2 * args.groups + piece) * width + e;
 #pragma unroll
-        for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), 4, both + i);
+        for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, both + i);
       }
     }
   }
   if (!there) return;
-  float* p = args.partial + 2 * (int64_t)blockIdx.x * width + threadIdx.x * T::kVec;
+  float* p = args.partial + 2 * (int64_t)blockIdx.x * width + e;
 #pragma unroll
   for (int i = 0; i < T::kVec; i += 4) {
-    if (args.dpre) store4<F32>(reinterpret_cast<uint32_t*>(p + width + i), 4, dpre + i);
-    if (args.dpost) *reinterpret_cast<v4f_user*>(p + i) = dpost[i / 4 * blockDim.x];
+    if (args.dpre) store4<F32>(reinterpret_cast<uint32_t*>(p + width + i), left - i, dpre + i);
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = dpost[i / 4 * blockDim.x][k];
+    if (args.dpost) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, f);
   }
 }
 
@@ -661,6 +709,12 @@ const void* norm_kernel(int vecs, bool backward) {
   return backward ? reinterpret_cast<const void*>(&norms_backward_kernel<T, kMost>) : reinterpret_cast<const void*>(&norms_kernel<T, kMost>);
 }
 
+template <class T>
+const void* ahead_kernel(bool edge, bool more) {
+  if (edge) return more ? reinterpret_cast<const void*>(&norms_backward_ahead_kernel<T, true, true>) : reinterpret_cast<const void*>(&norms_backward_ahead_kernel<T, true, false>);
+  return more ? reinterpret_cast<const void*>(&norms_backward_ahead_kernel<T, false, true>) : reinterpret_cast<const void*>(&norms_backward_ahead_kernel<T, false, false>);
+}
+
 rar_result_t check_norm(const rar_norm_t* n) {
   if (!n) return set_error(RAR_INVALID_ARGUMENT, "norm is NULL");
   if (rar_result_t r = check_float_dtype(n->dtype)) return r;
@@ -684,7 +738,7 @@ Pieces pieces_of(const rar_norm_t& n) {
   // as many workgroups as the device holds (16 waves a CU), their pieces of 8
   // rows or more where there are many
   const int waves = launch_of(n.width, n.dtype).threads / 64;
-  const int64_t most = 256 * (16 / waves), least = n.rows <= 512 ? 1 : n.rows <= 1024 ? 2 : n.rows <= 2048 ? 4 : 8;
+  const int64_t most = 256 * (16 / waves), least = n.rows <= 512 ? 1 : n.rows <= 1024 ? 2 : n.rows <= 8192 ? 4 : 8;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most / gates, p.group_rows / least));
   p.piece_rows = (p.group_rows + want - 1) / want;
   p.group_pieces = p.piece_rows ? (p.group_rows + p.piece_rows - 1) / p.piece_rows : 1;
@@ -839,9 +893,12 @@ rar_result_t backward(const rar_norm_t* norm, const void* const* grad_hidden, co
   if (n.rows > 0) {
     const Launch l = launch_of(n.width, n.dtype);
     const bool f32 = n.dtype == kFloat32;
-    const bool ahead = l.vecs == 1 && n.width % (f32 ? F32::kVec : BF16::kVec) == 0 && ngrad_hidden <= 1 && ngrad_outs <= 4;
+    const bool ahead = l.vecs == 1 && n.width >= (f32 ? F32::kVec : BF16::kVec);
     const void* fn = f32 ? norm_kernel<F32>(l.vecs, true) : norm_kernel<BF16>(l.vecs, true);
-    if (ahead) fn = f32 ? reinterpret_cast<const void*>(&norms_backward_ahead_kernel<F32>) : reinterpret_cast<const void*>(&norms_backward_ahead_kernel<BF16>);
+    if (ahead) {
+      const bool edge = n.width % (64 * (f32 ? F32::kVec : BF16::kVec)) != 0, more = ngrad_outs > 4 || ngrad_hidden > 1;
+      fn = f32 ? ahead_kernel<F32>(edge, more) : ahead_kernel<BF16>(edge, more);
+    }
     const unsigned lds = ahead ? l.threads * (unsigned)(3 + (f32 ? F32::kVec : BF16::kVec) / 4) * 16 : 0;
     if (rar_result_t r = launch_kernel(fn,
                                        dim3((unsigned)p.groups), dim3(l.threads), &a, stream, lds)) return r;

@@ -230,6 +230,19 @@ __device__ __forceinline__ float group_reduce(float v, Op op) {
   return v;
 }
 
+// How many of the mask's bits are below this lane's.
+__device__ __forceinline__ int bits_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// A row's address, the same in all lanes, kept out of vector registers: the
+// lanes' offsets are added to it in the access.
+__device__ __forceinline__ char* row_at(const char* p, int64_t offset) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p) + offset;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return reinterpret_cast<char*>((uint64_t)hi << 32 | lo);
+}
+
 // Between a wave's stores to LDS and its own loads: LDS keeps a wave's order,
 // so only the compiler has to.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -237,17 +250,56 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// A vector without its first n (0 or more) elements, zeros behind.
+// A vector without its first n (0 to kVec) elements, zeros behind.  In 32-bit
+// steps: 64-bit shifts by a lane's own amount gave wrong results here where the
+// amount was in the wave's last vector register.
 template <class T>
 __device__ __forceinline__ v4u shift_elements(v4u v, int n) {
-  const int bits = n * (128 / T::kVec);
-  uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
-  if (bits >= 64) lo = hi, hi = 0;
-  const int b = bits & 63;
-  lo = b ? lo >> b | hi << (64 - b) : lo;
-  hi >>= b;
-  return bits >= 128 ? v4u{0, 0, 0, 0} : v4u{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  if constexpr (T::kVec == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = n & 1 ? __builtin_amdgcn_alignbit(i < 3 ? v[i + 1] : 0, v[i], 16) : v[i];
+    n >>= 1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n & 1 ? (i < 3 ? v[i + 1] : 0) : v[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n & 2 ? (i < 2 ? v[i + 2] : 0) : v[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n & 4 ? 0 : v[i];
+  return v;
 }
+
+// The vector of a row's elements from e on, zeros behind the row's end: a row
+// of a vector or more is read where a whole one ends with it, so that no load
+// depends on a condition, and `fix` shifts the elements in front of e out.
+// `fix` waits for the vector; only waves with the row's end have more to do.
+template <class T>
+struct RowEdge {
+  int64_t at;  // first element read
+  int shift;   // elements in front of e
+  int n;       // elements there, where the row is shorter than a vector; -1: it is not
+  __device__ __forceinline__ RowEdge(int64_t e, int64_t width) {
+    if (width >= T::kVec) {
+      at = e < width - T::kVec ? e : width - T::kVec;
+      shift = e - at < T::kVec ? (int)(e - at) : T::kVec;
+      n = -1;
+    } else {
+      at = 0, shift = 0, n = e == 0 ? (int)width : 0;
+    }
+  }
+  __device__ __forceinline__ v4u load(const typename T::bits* row) const {
+    if (n < 0) return load_nt(row + at);
+    return load_part<T>(row, n, 0);
+  }
+  // data that other workgroups read too
+  __device__ __forceinline__ v4u load_shared(const typename T::bits* row) const {
+    if (n < 0) return load_16(row + at);
+    return load_part<T>(row, n, 0);
+  }
+  __device__ __forceinline__ void fix(v4u& v) const {
+    if (__ballot(shift > 0)) v = shift_elements<T>(v, shift);
+  }
+};
 
 // Four neighbouring elements, `n` of them there, as fp32.
 template <class T>

@@ -194,33 +194,38 @@ struct ProjArgs {
 // pieces of each that overlap, neither beyond the n bytes.
 template <int kCount>
 __device__ __forceinline__ void load_ends(const int8_t* const* p, int n, v4u* to) {
-  typedef uint64_t u64_byte __attribute__((aligned(1)));
+  typedef uint32_t v2u_byte __attribute__((ext_vector_type(2), aligned(1)));
   typedef uint32_t u32_byte __attribute__((aligned(1)));
   typedef uint16_t u16_byte __attribute__((aligned(1)));
-  uint64_t lo[kCount], hi[kCount];
+  v2u lo[kCount], hi[kCount];
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) lo[i] = hi[i] = 0;
+  for (int i = 0; i < kCount; ++i) lo[i] = hi[i] = v2u{0, 0};
   if (n >= 8) {
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] = *reinterpret_cast<const u64_byte*>(p[i]), hi[i] = *reinterpret_cast<const u64_byte*>(p[i] + n - 8);
+    for (int i = 0; i < kCount; ++i) lo[i] = *reinterpret_cast<const v2u_byte*>(p[i]), hi[i] = *reinterpret_cast<const v2u_byte*>(p[i] + n - 8);
+    // without its first 16 - n bytes, 1 to 8
+    const int drop = 16 - n, bits = 8 * (drop & 3);
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) hi[i] = n > 8 ? hi[i] >> (8 * (16 - n)) : 0;
+    for (int i = 0; i < kCount; ++i) {
+      v2u h = drop >= 8 ? v2u{0, 0} : drop >= 4 ? v2u{hi[i][1], 0} : hi[i];
+      hi[i] = v2u{__builtin_amdgcn_alignbit(h[1], h[0], bits), h[1] >> bits};
+    }
   } else if (n >= 4) {
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] = *reinterpret_cast<const u32_byte*>(p[i]), hi[i] = *reinterpret_cast<const u32_byte*>(p[i] + n - 4);
+    for (int i = 0; i < kCount; ++i) lo[i][0] = *reinterpret_cast<const u32_byte*>(p[i]), lo[i][1] = *reinterpret_cast<const u32_byte*>(p[i] + n - 4);
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] |= hi[i] << (8 * (n - 4)), hi[i] = 0;
+    for (int i = 0; i < kCount; ++i) lo[i][1] = n > 4 ? lo[i][1] >> (8 * (8 - n)) : 0;
   } else if (n >= 2) {
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] = (uint8_t)p[i][0], hi[i] = *reinterpret_cast<const u16_byte*>(p[i] + n - 2);
+    for (int i = 0; i < kCount; ++i) lo[i][0] = (uint8_t)p[i][0], lo[i][1] = *reinterpret_cast<const u16_byte*>(p[i] + n - 2);
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] |= hi[i] << (8 * (n - 2)), hi[i] = 0;
+    for (int i = 0; i < kCount; ++i) lo[i] = v2u{lo[i][0] | lo[i][1] << (8 * (n - 2)), 0};
   } else {
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) lo[i] = (uint8_t)p[i][0];
+    for (int i = 0; i < kCount; ++i) lo[i][0] = (uint8_t)p[i][0];
   }
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) to[i] = v4u{(uint32_t)lo[i], (uint32_t)(lo[i] >> 32), (uint32_t)hi[i], (uint32_t)(hi[i] >> 32)};
+  for (int i = 0; i < kCount; ++i) to[i] = v4u{lo[i][0], lo[i][1], hi[i][0], hi[i][1]};
 }
 
 // 16 bytes of a row from p on, n (1 or more) of them there and zeros behind.
@@ -230,6 +235,18 @@ __device__ __forceinline__ v4u load_bytes(const int8_t* p, int n) {
   v4u r;
   load_ends<1>(&p, n, &r);
   return r;
+}
+
+// 16 bytes without the first n (0 or more), zeros behind.
+__device__ __forceinline__ v4u shift_bytes(v4u v, int n) {
+  const int bits = 8 * (n & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbit(i < 3 ? v[i + 1] : 0, v[i], bits);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n & 4 ? (i < 3 ? v[i + 1] : 0) : v[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = n & 8 ? (i < 2 ? v[i + 2] : 0) : v[i];
+  return n < 16 ? v : v4u{0, 0, 0, 0};
 }
 
 constexpr int kDepth = 128;  // bytes of the inner dimension that a step has
@@ -291,10 +308,13 @@ __device__ __forceinline__ bool tile_of(int64_t b, int64_t tiles_m, int64_t tile
   return true;
 }
 
-// 16 bytes a lane from base + offset to LDS, to 16 * lane behind `to`.  The
+// 16 bytes a lane from base + offset to LDS, to 16 * lane behind `to` (both the
+// same in all lanes).  The
 // caller waits for it (vmcnt) before a barrier.
 __device__ __forceinline__ void to_lds(const int8_t* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)),
+               "v"(offset), "s"(row_at(reinterpret_cast<const char*>(base), 0))
+               : "memory");
 }
 
 // A workgroup's tile: kWN x kWM waves, each with kFN x kFM products of 32
@@ -544,28 +564,39 @@ __global__ void __launch_bounds__(512, 4) few_kernel(ProjArgs) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * 16, row = std::min<int64_t>(n0 + (lane & 15), args.outer - 1);
   const int tokens = (int)args.tokens, part = (lane >> 4) * 16;
+  const int token = std::min(lane & 15, tokens - 1);
   v4i acc = {0, 0, 0, 0};
-  for (int r = 0; r < args.nranks; ++r) {
-    const int width = args.width[r];
-    const int8_t* w = args.w[r] + row * args.w_stride[r] + part;
-    const int8_t* x = args.x[r] + std::min(lane & 15, tokens - 1) * args.x_stride[r] + part;
-    for (int k0 = wave * 64; k0 < width; k0 += 8 * 64 * kBatch) {
-      v4u a[kBatch], b[kBatch];
+  // pieces of 64 bytes are counted through the ranks; this wave's next one
+  int r = 0, k = wave * 64;
+  auto settle = [&] {
+    while (r < args.nranks && k >= args.width[r]) k -= (args.width[r] + 63) & ~63, ++r;
+  };
+  settle();
+  while (r < args.nranks) {
+    v4u a[kBatch], b[kBatch];
+    int drop[kBatch];  // bytes in front of the lane's part (from 16 on: nothing is there)
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int k = k0 + i * 8 * 64;
-        a[i] = b[i] = v4u{0, 0, 0, 0};
-        if (k + 64 <= width) {
-          a[i] = load_bytes(w + k, 16);
-          b[i] = load_bytes(x + k, 16);
-        } else if (k + part < width) {
-          a[i] = load_bytes(w + k, width - k - part);
-          b[i] = load_bytes(x + k, width - k - part);
-        }
+    for (int i = 0; i < kBatch; ++i) {
+      const int rank = std::min(r, args.nranks - 1), width = args.width[rank];
+      const int8_t* w = args.w[rank] + row * args.w_stride[rank];
+      const int8_t* x = args.x[rank] + token * args.x_stride[rank];
+      if (width >= 16) {  // a part beyond the row's end is read where whole ones end, and shifted
+        const int at = r < args.nranks ? std::min(k + part, width - 16) : 0;
+        drop[i] = r < args.nranks ? k + part - at : 16;
+        a[i] = load_bytes(w + at, 16);
+        b[i] = load_bytes(x + at, 16);
+      } else {
+        drop[i] = r < args.nranks && part == 0 ? 0 : 16;
+        a[i] = load_bytes(w, width);
+        b[i] = load_bytes(x, width);
       }
+      k += 8 * 64;
+      settle();
+    }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a[i]), __builtin_bit_cast(v4i, b[i]), acc, 0, 0, 0);
+    for (int i = 0; i < kBatch; ++i) {
+      if (__ballot(drop[i] > 0)) a[i] = shift_bytes(a[i], drop[i]), b[i] = shift_bytes(b[i], drop[i]);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a[i]), __builtin_bit_cast(v4i, b[i]), acc, 0, 0, 0);
     }
   }
   // lane l has token l & 15 and channels 4 (l >> 4) + 0..3
