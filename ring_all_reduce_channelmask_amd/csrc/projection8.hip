@@ -375,23 +375,23 @@ struct Tile {
         for (int i = 0; i < kLoadsX; ++i) to_lds(x0 + k0, ox[i], lds0 + stage * kStage + kN * kDepth + (i * kWaves + wave) * 1024);
       } else {  // a rank's last bytes, zeros behind
         const int mine = left - chunk * 16;
-        v4u some[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) some[i] = v4u{0, 0, 0, 0};
-        const int8_t* from[kLoads];
-        uint32_t to[kLoads];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          from[i] = i < kLoadsW ? w0 + k0 + ow[i < kLoadsW ? i : 0] : x0 + k0 + ox[i < kLoadsW ? 0 : i - kLoadsW];
-          to[i] = stage * kStage + ((i < kLoadsW ? i * kWaves : kN / 8 + (i - kLoadsW) * kWaves) + wave) * 1024;
-        }
+        auto from = [&](int i) { return i < kLoadsW ? w0 + k0 + ow[i < kLoadsW ? i : 0] : x0 + k0 + ox[i < kLoadsW ? 0 : i - kLoadsW]; };
+        auto to = [&](int i) { return stage * kStage + ((i < kLoadsW ? i * kWaves : kN / 8 + (i - kLoadsW) * kWaves) + wave) * 1024; };
         if (mine >= 16) {
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) to_lds(i < kLoadsW ? w0 + k0 : x0 + k0, i < kLoadsW ? ow[i < kLoadsW ? i : 0] : ox[i < kLoadsW ? 0 : i - kLoadsW], lds0 + to[i]);
+          for (int i = 0; i < kLoads; ++i) to_lds(i < kLoadsW ? w0 + k0 : x0 + k0, i < kLoadsW ? ow[i < kLoadsW ? i : 0] : ox[i < kLoadsW ? 0 : i - kLoadsW], lds0 + to(i));
         } else {
-          if (mine > 0) load_ends<kLoads>(from, left & 15, some);
+          constexpr int kGroup = kLoads > 6 ? 1 : kLoads;  // together as far as registers go
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) *reinterpret_cast<v4u*>(&lds[to[i] + lane * 16]) = some[i];
+          for (int g = 0; g < kLoads; g += kGroup) {
+            const int8_t* p[kGroup];
+            v4u some[kGroup];
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) p[i] = from(g + i), some[i] = v4u{0, 0, 0, 0};
+            if (mine > 0) load_ends<kGroup>(p, left & 15, some);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) *reinterpret_cast<v4u*>(&lds[to(g + i) + lane * 16]) = some[i];
+          }
         }
       }
       next();
