@@ -39,19 +39,21 @@ struct ForwardArgs {
   void* dst[kMaxRanks];
   int64_t dst_stride[kMaxRanks];
   const int64_t* ids;
-  int64_t width, pieces;  // pieces of a row: a workgroup takes one
+  int64_t tokens, width, pieces;  // pieces of a row
   float scale;
   int32_t ndst;
   Split split;
 };
 
-// A workgroup takes kVecs vectors a thread of one token's row.
-template <class T, int kVecs>
+// kThreads threads (64 or 256) take kVecs vectors each of one token's row.
+template <class T, int kVecs, int kThreads>
 __global__ void __launch_bounds__(256) embedding_kernel(ForwardArgs) {
   const ForwardArgs& args = kernel_args<ForwardArgs>();
-  const int64_t t = blockIdx.x / args.pieces, piece = blockIdx.x - t * args.pieces;
+  const int64_t item = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+  const int64_t t = item / args.pieces, piece = item - t * args.pieces;
+  if (t >= args.tokens) return;
   const int64_t id = args.ids[t];
-  const int64_t e0 = piece * (256 * kVecs * T::kVec) + threadIdx.x * T::kVec;
+  const int64_t e0 = piece * (kThreads * kVecs * T::kVec) + threadIdx.x % kThreads * T::kVec;
   v4u v[kVecs];
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) v[j] = v4u{0, 0, 0, 0};
@@ -59,11 +61,11 @@ __global__ void __launch_bounds__(256) embedding_kernel(ForwardArgs) {
     const int r = args.split.rank_of((int32_t)id);
     const typename T::bits* src = static_cast<const typename T::bits*>(args.table[r]) + (id - args.split.first[r]) * args.table_stride[r];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) v[j] = RowEdge<T>(e0 + j * (256 * T::kVec), args.width).load_shared(src);
+    for (int j = 0; j < kVecs; ++j) v[j] = RowEdge<T>(e0 + j * (kThreads * T::kVec), args.width).load_shared(src);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       float f[T::kVec];
-      RowEdge<T>(e0 + j * (256 * T::kVec), args.width).fix(v[j]);
+      RowEdge<T>(e0 + j * (kThreads * T::kVec), args.width).fix(v[j]);
       T::widen(v[j], f);
 #pragma unroll
       for (int i = 0; i < T::kVec; ++i) f[i] *= args.scale;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(256) embedding_kernel(ForwardArgs) {
     typename T::bits* dst = static_cast<typename T::bits*>(args.dst[k]) + t * args.dst_stride[k];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int64_t e = e0 + j * (256 * T::kVec);
+      const int64_t e = e0 + j * (kThreads * T::kVec);
       if (e < args.width) store_part<T>(dst + e, (int)(args.width - e > T::kVec ? T::kVec : args.width - e), v[j]);
     }
   }
@@ -590,6 +592,12 @@ rar_result_t check_sizes(int64_t tokens, int64_t width, int dtype, float scale) 
   return RAR_SUCCESS;
 }
 
+template <class T>
+const void* forward_kernel(int threads, int vecs) {
+  if (threads == 64) return reinterpret_cast<const void*>(&embedding_kernel<T, 1, 64>);
+  return vecs == 2 ? reinterpret_cast<const void*>(&embedding_kernel<T, 2, 256>) : reinterpret_cast<const void*>(&embedding_kernel<T, 1, 256>);
+}
+
 rar_result_t forward(const void* const* tables, const int64_t* rows, const int64_t* table_strides, int nranks, int64_t width, int dtype,
                      const int64_t* ids, int64_t tokens, float scale, void* const* recvbufs, const int64_t* recv_strides, int nrecv,
                      void* stream) {
@@ -624,12 +632,15 @@ rar_result_t forward(const void* const* tables, const int64_t* rows, const int64
   a.scale = scale;
   a.ndst = nrecv;
   const int vec = dtype == kFloat32 ? F32::kVec : BF16::kVec;
-  const int vecs = tokens * ((width + 256 * vec - 1) / (256 * vec)) > 2048 ? 2 : 1;
-  a.pieces = (width + 256 * vec * vecs - 1) / (256 * vec * vecs);
-  if (tokens * a.pieces > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
-  const void* fn = dtype == kFloat32 ? (vecs == 2 ? reinterpret_cast<const void*>(&embedding_kernel<F32, 2>) : reinterpret_cast<const void*>(&embedding_kernel<F32, 1>))
-                                     : (vecs == 2 ? reinterpret_cast<const void*>(&embedding_kernel<BF16, 2>) : reinterpret_cast<const void*>(&embedding_kernel<BF16, 1>));
-  return launch_kernel(fn, dim3((unsigned)(tokens * a.pieces)), dim3(256), &a, stream);
+  // a wave a row where that is enough for it, else a workgroup a piece
+  const int threads = width <= 64 * vec ? 64 : 256;
+  const int vecs = threads == 256 && tokens * ((width + 256 * vec - 1) / (256 * vec)) > 2048 ? 2 : 1;
+  a.tokens = tokens;
+  a.pieces = (width + threads * vec * vecs - 1) / (threads * vec * vecs);
+  const int64_t groups = (tokens * a.pieces + 256 / threads - 1) / (256 / threads);
+  if (groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
+  const void* fn = dtype == kFloat32 ? forward_kernel<F32>(threads, vecs) : forward_kernel<BF16>(threads, vecs);
+  return launch_kernel(fn, dim3((unsigned)groups), dim3(256), &a, stream);
 }
 
 template <class T, class G>

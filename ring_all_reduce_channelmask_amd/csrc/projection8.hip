@@ -732,8 +732,11 @@ Plan plan_of(const int64_t* widths, int nranks, int64_t tokens, int64_t outer, b
   return p;
 }
 // Whether tiles read an operand as it is: rows on multiples of 16 bytes, with
-// offsets of 32 bits within a tile.
-bool is_aligned(const int8_t* p, int64_t stride) { return ((reinterpret_cast<uintptr_t>(p) | stride) & 15) == 0 && stride < (1 << 24) - 256; }
+// offsets of 32 bits within a tile.  One row has no use for its stride.
+bool is_aligned(const int8_t* p, int64_t stride, int64_t rows) {
+  if (rows == 1) stride = 0;
+  return ((reinterpret_cast<uintptr_t>(p) | stride) & 15) == 0 && stride < (1 << 24) - 256;
+}
 
 struct Kind {
   int n, m, threads;
@@ -811,8 +814,8 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
   bool align_x = false, align_w = false;
   for (int r = 0; r < a.nranks; ++r) {
     a.steps += (a.width[r] + kDepth - 1) / kDepth;
-    align_x = align_x || !is_aligned(a.x[r], a.x_stride[r]);
-    align_w = align_w || !is_aligned(a.w[r], a.w_stride[r]);
+    align_x = align_x || !is_aligned(a.x[r], a.x_stride[r], tokens);
+    align_w = align_w || !is_aligned(a.w[r], a.w_stride[r], outer);
   }
   const Plan plan = plan_of(widths, nranks, tokens, outer, align_x, align_w);
   const int64_t need = plan.align_x + plan.align_w + plan.partial;

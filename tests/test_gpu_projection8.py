@@ -279,3 +279,53 @@ def test_no_tokens_and_no_columns():
         assert torch.equal(out, res)
     q, s = rar.quantize_rows([torch.empty((3, 0), device="cuda")])
     assert q[0].shape == (3, 0) and not s.any()
+
+
+@pytest.mark.parametrize("tokens", [1, 40, 300])
+def test_one_channel_of_padded_weights(tokens):
+    """A single row of weights, whose stride means nothing, as quantize_rows
+    lays it out."""
+    dev, want = _case("float32", tokens, [17, 40], 1, seed=tokens)
+    dev["weights"] = [_bytes(w.cpu().numpy(), (-w.shape[1]) % 16) for w in dev["weights"]]
+    dev["xs"] = [_bytes(x.cpu().numpy(), (-x.shape[1]) % 16) for x in dev["xs"]]
+    _check(_run(dev, tokens, 1, "float32")[0], want)
+
+
+def test_rows_as_far_apart_as_large_tiles_take():
+    """Offsets of more than 2^31 bytes within a tile of 256 rows."""
+    import torch
+    tokens, outer, width, stride = 1024, 10240, 144, (1 << 24) - 272
+    held = torch.empty(tokens * stride, dtype=torch.int8, device="cuda")
+    x = held.as_strided((tokens, width), (stride, 1))
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x.copy_(torch.randint(-128, 128, (tokens, width), generator=g, device="cuda"))
+    w = torch.randint(-128, 128, (outer, width), generator=g, device="cuda").to(torch.int8)
+    sx, sw = torch.rand(tokens, generator=g, device="cuda"), torch.rand(outer, generator=g, device="cuda")
+    out = torch.empty(tokens, outer, device="cuda")
+    _run(dict(xs=[x], weights=[w], x_scales=sx, weight_scales=sw, residual=None), tokens, outer, "float32", recvs=[out])
+    acc = (x.float() @ w.float().T).double()  # below 2^24: exact
+    want = acc * sx.double()[:, None] * sw.double()
+    # the sum to fp32 is exact, two products are rounded
+    assert ((out.double() - want).abs() <= want.abs() * 3 * 2.0 ** -24).all()
+
+
+# tiles of 256 x 256 and 256 x 192 together, of 128 x 128, of 128 x 64 with parts of the inner dimension
+SHAPES = [(4097, [96], 2900), (2600, [33, 40], 4500), (2300, [200], 2310), (1030, [1000, 24], 300)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,widths,outer", SHAPES, ids=[f"t{c[0]}-o{c[2]}" for c in SHAPES])
+def test_every_size_of_tile(dtype, tokens, widths, outer):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    xs, ws = ([torch.randint(-128, 128, (n, w), generator=g, device="cuda").to(torch.int8) for w in widths] for n in (tokens, outer))
+    sx, sw = torch.rand(tokens, generator=g, device="cuda"), torch.rand(outer, generator=g, device="cuda")
+    res = torch.randn(tokens, outer, generator=g, device="cuda").to(getattr(torch, dtype))
+    got = _run(dict(xs=xs, weights=ws, x_scales=sx, weight_scales=sw, residual=res), tokens, outer, dtype, copies=2)
+    # below 2^53: exact
+    prod = sum(x.double() @ w.double().T for x, w in zip(xs, ws)) * sx.double()[:, None] * sw.double()
+    want = prod + res.double()
+    bound = prod.abs() * 3 * model_ops.U + want.abs() * 2 * model_ops.U
+    bound = bound + (want.abs() + bound) * model_ops.ROUND[dtype]
+    for y in got:
+        assert ((y.double() - want).abs() <= bound).all()

@@ -209,6 +209,10 @@ def test_projection_refusals():
         (dict(wstrides=(1 << 60, 32)), "far stride"), (dict(recvs=(A,)), "over an input"), (dict(recvs=(A + 3 * M,)), "over a weight"), (dict(recvs=(A + 5 * M,)), "over scales"),
         (dict(recvs=(A + 6 * M, A + 6 * M + 8), copies=2), "outputs overlap"), (dict(res=A + 6 * M + 8), "in part over the residual"),
         (dict(tokens=1 << 24, outer=1 << 24), "too large"),
+        (dict(tokens=100, xs=(A + 1, A + M), work=None), "no workspace for rows to be laid out"), (dict(tokens=100, wstrides=(65, 32), work=None), "no workspace"),
+        (dict(tokens=100, xs=(A + 1, A + M), work_bytes=100 * 64), "workspace too small"), (dict(tokens=100, xs=(A + 1, A + M), work=A + 7 * M + 8), "misaligned workspace"),
+        (dict(tokens=100, xs=(A + 1, A + M), work=A + 3 * M), "workspace over a weight"), (dict(tokens=100, xs=(A + 1, A + M), work=A + 6 * M), "workspace over an output"),
+        (dict(tokens=100, widths=(65536, 32), work=None, n=1), "no workspace for parts of the sums"),
     ]
     for kw, why in bad:
         assert _project(**kw) == BAD, why
@@ -221,6 +225,12 @@ def test_projection_workspace():
     assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, BF16, 1, None) == BAD
     assert lib.rar_int8_projection_workspace(None, 1, 5, 64, BF16, 1, ctypes.byref(n)) == BAD
     assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 0, BF16, 1, ctypes.byref(n)) == BAD
+    # rows to be laid out need room, and so do parts of the sums
+    sizes = {}
+    for aligned in (0, 1):
+        assert lib.rar_int8_projection_workspace(_l([6400]), 1, 100, 640, BF16, aligned, ctypes.byref(n)) == OK
+        sizes[aligned] = n.value
+    assert sizes[0] >= sizes[1] + 740 * 6400 and sizes[1] > 0
     assert lib.rar_int8_projection_workspace(_l([64]), 1, 5, 64, I32, 1, ctypes.byref(n)) == BAD
 
 
