@@ -9,6 +9,13 @@
 // their positions, and adds up each group in fp32; every table row is written
 // by one wave, once, so no float is added atomically and the same inputs give
 // the same bits.
+//
+// Bound by memory.  Measured (kernels, bf16): 4096 tokens of 7168, 4 copies 38 us
+// (235 MB written, 6.1 TB/s; a text's frequent rows come from the caches: with
+// loads that bypass them 59), 1 token 3.1 us; gradient of 65536 tokens of 2048
+// (vocabulary 131072) 24 us for the order, 162 for the sums and the zeros (805
+// MB: 5.0 TB/s) and 15 for the groups that chunks cut; of 333 tokens of 1001 in
+// fp32 13 us (32 MB written).
 #include "op_common.h"
 
 namespace rar {
@@ -19,8 +26,12 @@ constexpr int64_t kMaxVocab = int64_t(1) << 30;
 constexpr int64_t kMaxWidth = int64_t(1) << 24;
 typedef float v4f_user __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kRow = 512;        // 16-bit elements of a wave's piece of a row (256 of 32 bits)
-constexpr int kSmallTokens = 1024;  // up to here a group's positions are found by looking at all ids
-constexpr int kRankTokens = 8192;  // up to here the order comes from comparing all pairs
+// Up to kSmallTokens a group's positions are found by looking at all ids, in
+// one launch (1000 tokens of 4096: 64 us; 1100 in three launches 63).  Up to
+// kRankTokens the order comes from comparing all pairs (4096 tokens 9.3 us,
+// 16384 27; the radix sort 22 to 24 whatever the number there).
+constexpr int kSmallTokens = 1024;
+constexpr int kRankTokens = 8192;
 
 // Where the ranks' rows begin in the vocabulary; first[nranks] is its size.
 struct Split {

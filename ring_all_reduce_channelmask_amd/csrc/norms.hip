@@ -16,7 +16,14 @@
 //
 // A workgroup takes a row at a time, its elements in registers between the
 // two reductions; every stream is read and written once.  Sums are fp32, in
-// an order that depends on the shapes alone.
+// an order that depends on the shapes alone; the gradient takes the statistics
+// of h and s from the stored rows, which it reads anyway.
+//
+// Bound by memory.  Measured (kernels): forward, 4096 x 7168 bf16, 4 partials, a
+// residual, a gate, 6 outputs 117 us (5.5 TB/s of 646 MB), 1 row 6.2 us (two
+// dependent reductions of a row over 14 waves); gradient, 4096 x 7168 bf16, 9
+// streams 122 us (4.3 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.6 +
+// 4.4; 56100 x 526 bf16 116 + 11.
 #include "op_common.h"
 
 namespace rar {
@@ -423,6 +430,9 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
 // waits are for the row in hand alone.  An absent input is another one read
 // again, and the row's end is as RowEdge has it (kEdge: it is not where a
 // wave's vectors end).  Further gradients (kMore) are read where they are added.
+// 16 waves of 128 registers a CU, so one workgroup of a wide row: without the
+// loads ahead 4096 x 7168 took 151 us, with them 122 (16 rows a workgroup, each
+// 5.5 us of memory and 3.3 of arithmetic, which overlap in part).
 template <class T, bool kEdge, bool kMore>
 __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
