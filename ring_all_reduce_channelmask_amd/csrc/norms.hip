@@ -22,7 +22,7 @@
 // Bound by memory.  Measured (kernels): forward, 4096 x 7168 bf16, 4 partials, a
 // residual, a gate, 6 outputs 117 us (5.5 TB/s of 646 MB), 1 row 6.2 us (two
 // dependent reductions of a row over 14 waves); gradient, 4096 x 7168 bf16, 9
-// streams 122 us (4.3 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.6 +
+// streams 121 us (4.4 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.6 +
 // 4.4; 56100 x 526 bf16 116 + 11.
 #include "op_common.h"
 
@@ -430,9 +430,11 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
 // waits are for the row in hand alone.  An absent input is another one read
 // again, and the row's end is as RowEdge has it (kEdge: it is not where a
 // wave's vectors end).  Further gradients (kMore) are read where they are added.
-// 16 waves of 128 registers a CU, so one workgroup of a wide row: without the
-// loads ahead 4096 x 7168 took 151 us, with them 122 (16 rows a workgroup, each
-// 5.5 us of memory and 3.3 of arithmetic, which overlap in part).
+// The row behind a piece's last is the first of the workgroup's next piece
+// (73153 x 328 with a gate a row: 137 us without that, 95 with it).  16 waves of
+// 128 registers a CU, so one workgroup of a wide row: without the loads ahead
+// 4096 x 7168 took 151 us, with them 121 (16 rows a workgroup, each 5.5 us of
+// memory and 3.3 of arithmetic, which overlap in part).
 template <class T, bool kEdge, bool kMore>
 __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
@@ -512,26 +514,38 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
   };
   weights[0] = weight(has_out ? args.pre : nullptr, 0);
   weights[blockDim.x] = weight(args.post, 0);
-  float dpre[T::kVec], both[T::kVec];
+  float dpre[T::kVec];
 #pragma unroll
   for (int i = 0; i < T::kVec; ++i) dpre[i] = 0.0f;
 #pragma unroll
   for (int i = 0; i < T::kVec / 4; ++i) dpost[i * blockDim.x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t piece = blockIdx.x; piece < args.pieces; piece += args.groups) {
-    const int64_t group = piece / args.group_pieces, first = (piece - group * args.group_pieces) * args.piece_rows;
-    const int64_t row0 = group * args.group_rows + first;
-    const int64_t row1 = group * args.group_rows + std::min(args.group_rows, first + args.piece_rows);
+  float both[T::kVec];
+  int64_t piece = blockIdx.x, group, row, row1;  // the row in hand and its piece's end
+  auto begin_piece = [&] {
+    group = piece / args.group_pieces;
+    const int64_t first = (piece - group * args.group_pieces) * args.piece_rows;
+    row = group * args.group_rows + first;
+    row1 = group * args.group_rows + std::min(args.group_rows, first + args.piece_rows);
     weights[2 * blockDim.x] = weight(args.gate, group * args.gate_stride);
 #pragma unroll
     for (int i = 0; i < T::kVec; ++i) both[i] = 0.0f;
-    auto one_row = [&](int64_t row, Inputs& now, Inputs& ahead) {
+  };
+  // the row behind this one, of this piece or the workgroup's next; or itself
+  auto next_row = [&] {
+    if (row + 1 < row1) return row + 1;
+    const int64_t next = piece + args.groups;
+    if (next >= args.pieces) return row;
+    const int64_t g = next / args.group_pieces;
+    return g * args.group_rows + (next - g * args.group_pieces) * args.piece_rows;
+  };
+    auto one_row = [&](Inputs& now, Inputs& ahead) {
       float more[T::kVec];  // of the gradients of outs
       if (kMore && args.ngrad_out > kOuts) {
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) more[i] = 0.0f;
         add_more(args.grad_out, args.grad_out_stride, kOuts, args.ngrad_out, row, more);
       }
-      load(std::min(row + 1, row1 - 1), ahead);
+      load(next_row(), ahead);
       __builtin_amdgcn_sched_barrier(0);
       if (edge) {
         now.s = fix(now.s), now.h = fix(now.h), now.e = fix(now.e);
@@ -618,33 +632,47 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
       // scratch, unless there is only one of the two
       if (has_out != (args.post != nullptr) && waves > 1) __syncthreads();
     };
-    Inputs in[2];
-    load(row0, in[0]);
-    for (int64_t row = row0; row < row1; row += 2) {
-      one_row(row, in[0], in[1]);
-      if (row + 1 < row1) one_row(row + 1, in[1], in[0]);
-    }
-    if (!there) continue;
-    if (args.dpost) {
-      float g[T::kVec];
-      T::widen(weights[2 * blockDim.x], g);
+    // The sums of a piece that has ended.
+    auto end_piece = [&] {
+      if (!there) return;
+      if (args.dpost) {
+        float g[T::kVec];
+        T::widen(weights[2 * blockDim.x], g);
 #pragma unroll
-      for (int i = 0; i < T::kVec; ++i) dpost[i / 4 * blockDim.x][i % 4] += g[i] * both[i];
-    }
-    if (args.dgate) {
-      float k[T::kVec];
-      T::widen(weights[blockDim.x], k);
-#pragma unroll
-      for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
-      if (args.group_pieces == 1) {
-        put(args.dgate, group * args.dgate_stride, both);
-      } else {
-        float* p = args.partial + (2 * args.groups + piece) * width + e;
-#pragma unroll
-        for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, both + i);
+        for (int i = 0; i < T::kVec; ++i) dpost[i / 4 * blockDim.x][i % 4] += g[i] * both[i];
       }
+      if (args.dgate) {
+        float k[T::kVec];
+        T::widen(weights[blockDim.x], k);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
+        if (args.group_pieces == 1) {
+          put(args.dgate, group * args.dgate_stride, both);
+        } else {
+          float* p = args.partial + (2 * args.groups + piece) * width + e;
+#pragma unroll
+          for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, both + i);
+        }
+      }
+    };
+    // The next row is the one in hand; false: there is none.
+    auto advance = [&] {
+      if (++row < row1) return true;
+      end_piece();
+      piece += args.groups;
+      if (piece >= args.pieces) return false;
+      begin_piece();
+      return true;
+    };
+    Inputs in[2];
+    begin_piece();
+    load(row, in[0]);
+    for (;;) {
+      one_row(in[0], in[1]);
+      if (!advance()) break;
+      one_row(in[1], in[0]);
+      if (!advance()) break;
     }
-  }
   if (!there) return;
   float* p = args.partial + 2 * (int64_t)blockIdx.x * width + e;
 #pragma unroll

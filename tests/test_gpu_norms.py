@@ -148,6 +148,14 @@ def test_many_rows(dtype, rows, groups):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,groups,width", [(5001, 5001, 130), (9000, 4500, 60), (1640, 820, 2100), (3003, 1001, 2051)])
+def test_more_runs_of_rows_than_workgroups(dtype, rows, groups, width):
+    """A workgroup takes several gates' rows in turn, odd numbers of them too."""
+    case = Case(dtype, 2, rows, width, groups=groups, seed=rows)
+    case.check_backward(case.backward())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_a_gate_as_a_vector(dtype):
     case = Case(dtype, 2, 20, 300, groups=1)
     case.dev["gate"] = case.dev["gate"].view(300)
