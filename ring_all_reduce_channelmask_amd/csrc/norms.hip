@@ -22,8 +22,8 @@
 // Bound by memory.  Measured (kernels): forward, 4096 x 7168 bf16, 4 partials, a
 // residual, a gate, 6 outputs 117 us (5.5 TB/s of 646 MB), 1 row 6.2 us (two
 // dependent reductions of a row over 14 waves); gradient, 4096 x 7168 bf16, 9
-// streams 121 us (4.4 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.6 +
-// 4.4; 56100 x 526 bf16 116 + 11.
+// streams 121 us (4.4 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.1 +
+// 4.4; 73153 x 328 bf16 with a gate a row 98 to 102 + 16.
 #include "op_common.h"
 
 namespace rar {
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
 // again, and the row's end is as RowEdge has it (kEdge: it is not where a
 // wave's vectors end).  Further gradients (kMore) are read where they are added.
 // The row behind a piece's last is the first of the workgroup's next piece
-// (73153 x 328 with a gate a row: 137 us without that, 95 with it).  16 waves of
+// (73153 x 328 with a gate a row: 137 us without that, 95 to 102 with it).  16 waves of
 // 128 registers a CU, so one workgroup of a wide row: without the loads ahead
 // 4096 x 7168 took 151 us, with them 121 (16 rows a workgroup, each 5.5 us of
 // memory and 3.3 of arithmetic, which overlap in part).

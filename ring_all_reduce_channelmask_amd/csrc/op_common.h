@@ -1,7 +1,7 @@
 // op_common.h -- what the operators around an AllReduce share (dropout.hip,
 // logprobs.hip, adapters.hip, embedding.hip, norms.hip, projection8.hip): host-side
-// argument checks, the C boundary's
-// exception guard, and the device types and conversions.
+// argument checks, the C boundary's exception guard, and the device types and
+// conversions.
 #pragma once
 
 #include <hip/hip_runtime.h>
