@@ -557,8 +557,8 @@ rar_result_t rar_embedding_workspace(const int64_t* rows, int nranks, int64_t to
  *   outs[k]   = rms(hidden) * pre_weight
  * total is what the gradient needs, hidden the residual stream behind the
  * block, outs the next block's input.  Each norm is taken of the fp32 values,
- * before they are rounded.  A row whose mean of x^2 leaves fp32's range
- * counts it as infinity. */
+ * before they are rounded, and of rows of any finite magnitude, in
+ * the gradient too: their squares may leave fp32's range. */
 typedef struct {
   int64_t rows, width;      /* 0..2^24 (0 launches nothing forward), 1..32768    */
   int32_t dtype;            /* rar_dtype_t of every operand                      */

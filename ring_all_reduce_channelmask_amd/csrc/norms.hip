@@ -51,6 +51,41 @@ __device__ __forceinline__ void block_sum2(float& a, float& b, v2f* scratch, int
 }
 __device__ __forceinline__ float rstd_of(float squares, float width, float eps) { return 1.0f / __builtin_sqrtf(squares / width + eps); }
 
+// What a row x and, for its gradient, a row v of the gradients of x / rms(x)
+// are reduced to.  A row whose sum of squares leaves fp32's range is taken
+// times kDown (`scale_down` changes it in place) and summed again: no square of
+// a finite number leaves it then, and what is lost at the other end is below
+// 2^-60 of the row's largest element.  Where the sum of v x leaves it, v's
+// part of that sum is taken times kDown.  All threads agree on both, and other
+// rows see nothing of it but a comparison.
+constexpr float kDown = 0x1p-80f;
+struct Stats {
+  float r;     // rstd of the row as it is now
+  float c;     // mean(v x) r^2, likewise
+  float rstd;  // of the row as it was
+};
+// sums(squares, dot, factor): of x^2 and of (v factor) x, over the workgroup
+template <class S, class D>
+__device__ __forceinline__ Stats row_stats(float width, float eps, S sums, D scale_down) {
+  float squares = 0.0f, dot = 0.0f;
+  sums(squares, dot, 1.0f);
+  Stats s;
+  s.r = s.rstd = rstd_of(squares, width, eps);
+  s.c = dot / width * s.r * s.r;
+  const bool in_range = s.r > 0.0f, dot_in_range = __builtin_fabsf(dot) < __builtin_inff();
+  if (__builtin_expect(__ballot(!in_range || !dot_in_range) != 0, 0)) {
+    const float factor = dot_in_range ? 1.0f : kDown;
+    if (!in_range) scale_down();
+    __syncthreads();  // the first sums have been read
+    squares = dot = 0.0f;
+    sums(squares, dot, factor);
+    s.r = rstd_of(squares, width, in_range ? eps : eps * kDown * kDown);
+    s.rstd = in_range ? s.r : s.r * kDown;
+    s.c = dot / width * s.r * s.r / factor;
+  }
+  return s;
+}
+
 // This thread's vectors of a row: vector j starts at element (j * threads +
 // threadIdx.x) * kVec.
 template <class T, int kVecs>
@@ -75,6 +110,16 @@ struct Row {
   }
   __device__ __forceinline__ void widen(int j, float* f) const { T::widen(v[j], f); }
   __device__ __forceinline__ void set(int j, const float* f) { v[j] = T::round(f); }
+  __device__ __forceinline__ void scale_down() {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float f[T::kVec];
+      widen(j, f);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
+      set(j, f);
+    }
+  }
   __device__ __forceinline__ void store(void* buf, int64_t stride, int64_t row, int width) const {
     typename T::bits* p = static_cast<typename T::bits*>(buf) + row * stride;
 #pragma unroll
@@ -130,14 +175,30 @@ struct ForwardArgs {
   float eps, scale;
 };
 
+// Up to two vectors a thread, two workgroups of 16 waves a CU: 2048 x 16384 bf16
+// 139 us, although 12 registers spill; with none spilled and one workgroup 144.
 template <class T, int kVecs>
-__global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
+__global__ void __launch_bounds__(kMaxThreads) __attribute__((amdgpu_waves_per_eu(kVecs <= 2 ? 8 : 4))) norms_kernel(ForwardArgs) {
   const ForwardArgs& args = kernel_args<ForwardArgs>();
   __shared__ v2f scratch[2][kMaxThreads / 64];
   const int width = args.width, waves = blockDim.x >> 6;
   const int64_t row = blockIdx.x;
   Row<T, kVecs> x, w, g;
   float h[kVecs][T::kVec];
+  auto rstd_of_h = [&](v2f* sums) {
+    return row_stats((float)width, args.eps, [&](float& squares, float& none, float) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) squares += h[j][i] * h[j][i];
+      block_sum2(squares, none, sums, waves);
+    }, [&] {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) h[j][i] *= kDown;
+    }).r;
+  };
   sum_rows<T, kVecs>(args.src, args.src_stride, args.nsrc, row, width, h);
   if (args.residual) x.load(args.residual, args.residual_stride, row, width);
   if (args.total) {
@@ -149,13 +210,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
   if (args.gate) g.load_shared(args.gate, args.gate_stride, row / args.group_rows, width);
   if (args.post) {
     w.load_shared(args.post, 0, 0, width);
-    float squares = 0.0f, none = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-      for (int i = 0; i < T::kVec; ++i) squares += h[j][i] * h[j][i];
-    block_sum2(squares, none, scratch[0], waves);
-    const float q = rstd_of(squares, (float)width, args.eps);
+    const float q = rstd_of_h(scratch[0]);
     w.fix(width);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
@@ -190,13 +245,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_kernel(ForwardArgs) {
   for (int k = 0; k < args.nhidden; ++k) x.store(args.hidden[k], args.hidden_stride[k], row, width);
   if (args.nout == 0) return;
   w.load_shared(args.pre, 0, 0, width);
-  float squares = 0.0f, none = 0.0f;
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-    for (int i = 0; i < T::kVec; ++i) squares += h[j][i] * h[j][i];
-  block_sum2(squares, none, scratch[1], waves);
-  const float r = rstd_of(squares, (float)width, args.eps);
+  const float r = rstd_of_h(scratch[1]);
   w.fix(width);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
@@ -283,21 +332,20 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
         w.load_shared(args.pre, 0, 0, width);
         h.fix(width);
         w.fix(width);
-        float squares = 0.0f, dot = 0.0f;
+        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          float f[T::kVec], k[T::kVec];
-          h.widen(j, f);
-          w.widen(j, k);
+          for (int j = 0; j < kVecs; ++j) {
+            float f[T::kVec], k[T::kVec];
+            h.widen(j, f);
+            w.widen(j, k);
 #pragma unroll
-          for (int i = 0; i < T::kVec; ++i) {
-            squares = __builtin_fmaf(f[i], f[i], squares);
-            dot = __builtin_fmaf(n[j][i] * k[i], f[i], dot);
+            for (int i = 0; i < T::kVec; ++i) {
+              squares = __builtin_fmaf(f[i], f[i], squares);
+              dot = __builtin_fmaf(n[j][i] * k[i] * factor, f[i], dot);
+            }
           }
-        }
-        block_sum2(squares, dot, scratch[0], waves);
-        const float r = rstd_of(squares, (float)width, args.eps);
-        const float c = dot / (float)width * r * r;
+          block_sum2(squares, dot, scratch[0], waves);
+        }, [&] { h.scale_down(); });
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float f[T::kVec], k[T::kVec];
@@ -305,8 +353,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           w.widen(j, k);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            dpre[j][i] = __builtin_fmaf(n[j][i], f[i] * r, dpre[j][i]);
-            d[j][i] = __builtin_fmaf(r, __builtin_fmaf(-f[i], c, n[j][i] * k[i]), d[j][i]);
+            dpre[j][i] = __builtin_fmaf(n[j][i], f[i] * of.r, dpre[j][i]);
+            d[j][i] = __builtin_fmaf(of.rstd, __builtin_fmaf(-f[i], of.c, n[j][i] * k[i]), d[j][i]);
           }
         }
       }
@@ -328,22 +376,21 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
       if (args.post) {
         w.load_shared(args.post, 0, 0, width);
         w.fix(width);
-        float squares = 0.0f, dot = 0.0f;
+        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-          float f[T::kVec], k[T::kVec], a[T::kVec];
-          s.widen(j, f);
-          w.widen(j, k);
-          if (args.gate) g.widen(j, a);
+          for (int j = 0; j < kVecs; ++j) {
+            float f[T::kVec], k[T::kVec], a[T::kVec];
+            s.widen(j, f);
+            w.widen(j, k);
+            if (args.gate) g.widen(j, a);
 #pragma unroll
-          for (int i = 0; i < T::kVec; ++i) {
-            squares = __builtin_fmaf(f[i], f[i], squares);
-            dot = __builtin_fmaf(d[j][i] * (args.gate ? a[i] : 1.0f) * k[i], f[i], dot);
+            for (int i = 0; i < T::kVec; ++i) {
+              squares = __builtin_fmaf(f[i], f[i], squares);
+              dot = __builtin_fmaf(d[j][i] * (args.gate ? a[i] : 1.0f) * k[i] * factor, f[i], dot);
+            }
           }
-        }
-        block_sum2(squares, dot, scratch[1], waves);
-        const float q = rstd_of(squares, (float)width, args.eps);
-        const float c = dot / (float)width * q * q;
+          block_sum2(squares, dot, scratch[1], waves);
+        }, [&] { s.scale_down(); });
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float f[T::kVec], k[T::kVec], a[T::kVec];
@@ -352,8 +399,8 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           if (args.gate) g.widen(j, a);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
-            both[j][i] = __builtin_fmaf(d[j][i], f[i] * q, both[j][i]);
-            d[j][i] = q * __builtin_fmaf(-f[i], c, d[j][i] * (args.gate ? a[i] : 1.0f) * k[i]);
+            both[j][i] = __builtin_fmaf(d[j][i], f[i] * of.r, both[j][i]);
+            d[j][i] = of.rstd * __builtin_fmaf(-f[i], of.c, d[j][i] * (args.gate ? a[i] : 1.0f) * k[i]);
           }
         }
       } else if (args.gate) {
@@ -570,26 +617,28 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
         }
         T::widen(now.h, f);
         T::widen(weights[0], k);
-        float squares = 0.0f, dot = 0.0f;
+        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) {
+            squares = __builtin_fmaf(f[i], f[i], squares);
+            dot = __builtin_fmaf(n[i] * k[i] * factor, f[i], dot);
+          }
+          block_sum2(squares, dot, scratch[0], waves);
+        }, [&] {
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
+        });
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) {
-          squares = __builtin_fmaf(f[i], f[i], squares);
-          dot = __builtin_fmaf(n[i] * k[i], f[i], dot);
-        }
-        block_sum2(squares, dot, scratch[0], waves);
-        const float r = rstd_of(squares, (float)width, args.eps);
-        const float c = dot / (float)width * r * r;
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) {
-          dpre[i] = __builtin_fmaf(n[i], f[i] * r, dpre[i]);
-          n[i] = __builtin_fmaf(-f[i], c, n[i] * k[i]);
+          dpre[i] = __builtin_fmaf(n[i], f[i] * of.r, dpre[i]);
+          n[i] = __builtin_fmaf(-f[i], of.c, n[i] * k[i]);
         }
         T::widen(now.e, d);
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) d[i] = has_hidden ? d[i] : 0.0f;
         if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(r, n[i], d[i]);
+        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(of.rstd, n[i], d[i]);
       } else {
         T::widen(now.e, d);
         if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
@@ -606,19 +655,21 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
       if (args.post) {
         float k[T::kVec];
         T::widen(weights[blockDim.x], k);
-        float squares = 0.0f, dot = 0.0f;
+        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) {
+            squares = __builtin_fmaf(f[i], f[i], squares);
+            dot = __builtin_fmaf(d[i] * g[i] * k[i] * factor, f[i], dot);
+          }
+          block_sum2(squares, dot, scratch[1], waves);
+        }, [&] {
+#pragma unroll
+          for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
+        });
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) {
-          squares = __builtin_fmaf(f[i], f[i], squares);
-          dot = __builtin_fmaf(d[i] * g[i] * k[i], f[i], dot);
-        }
-        block_sum2(squares, dot, scratch[1], waves);
-        const float q = rstd_of(squares, (float)width, args.eps);
-        const float c = dot / (float)width * q * q;
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) {
-          both[i] = __builtin_fmaf(d[i], f[i] * q, both[i]);
-          d[i] = q * __builtin_fmaf(-f[i], c, d[i] * g[i] * k[i]);
+          both[i] = __builtin_fmaf(d[i], f[i] * of.r, both[i]);
+          d[i] = of.rstd * __builtin_fmaf(-f[i], of.c, d[i] * g[i] * k[i]);
         }
       } else {
 #pragma unroll
