@@ -374,8 +374,10 @@ def _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, p
     def weight(t, what):
         return None if t is None else _vector(t, width, dtype, dev, what)
     at, groups, stride = None, 0, 0
-    if gate is not None and rows:
+    if gate is not None:
         at, groups, stride = _gate(gate, width, dtype, dev, "gate")
+        if not rows:  # then a gate has any number of groups, and no use
+            at, groups, stride = None, 0, 0
     return _lib.Norm(rows, width, dt, eps, residual_scale, 0, weight(post_weight, "post_weight"),
                      weight(pre_weight, "pre_weight"), at, groups, stride)
 
@@ -491,10 +493,9 @@ def norm_allreduce_backward(grad_hidden, grad_outs, dpartials, total=None, hidde
     if dgate is not None:
         if gate is None or dgate.shape != gate.shape:
             raise ValueError("dgate must have the shape of gate")
-        if rows:
-            dgate_ptr, _, dgate_stride = _gate(dgate, width, dtype, dev, "dgate", False)
-        else:
-            dgate.zero_()
+        dgate_ptr, _, dgate_stride = _gate(dgate, width, dtype, dev, "dgate", False)
+        if not rows:  # zeroed below, whatever its number of groups
+            dgate_ptr, dgate_stride = None, 0
     handle, other = _on(dev, stream)
     lib, need = _lib.load(), _norm_workspace(rows, width, dt, n.gate_groups)
     work = None
@@ -509,6 +510,8 @@ def norm_allreduce_backward(grad_hidden, grad_outs, dpartials, total=None, hidde
         *_single(dresidual, rows, width, dtype, dev, "dresidual", False),
         vector(dpost_weight, "dpost_weight"), dgate_ptr, dgate_stride,
         vector(dpre_weight, "dpre_weight"), work.data_ptr() if need else None, need, handle))
+    if dgate is not None and not rows:
+        _new(other, dgate.zero_)
 
 
 def quantize_rows(xs, quantized=None, scales=None, stream=None):
