@@ -567,7 +567,8 @@ typedef struct {
   int32_t pad;
   const void* post_weight;  /* [width]; NULL: no norm of the sum (total itself)  */
   const void* pre_weight;   /* [width]; needed where there are outs              */
-  const void* gate;         /* [gate_groups] of width elements; NULL for none    */
+  const void* gate;         /* [gate_groups] of width elements; NULL for none,   */
+                            /* whatever the two below hold                       */
   int64_t gate_groups;      /* divides the rows: row i has gate                  */
                             /* i / (rows / gate_groups); 1: one for all          */
   int64_t gate_stride;      /* between gates; 0: width                           */

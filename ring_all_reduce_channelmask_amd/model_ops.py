@@ -378,6 +378,8 @@ def _norm(rows, width, dtype, dt, dev, eps, residual_scale, post_weight, gate, p
         at, groups, stride = _gate(gate, width, dtype, dev, "gate")
         if not rows:  # then a gate has any number of groups, and no use
             at, groups, stride = None, 0, 0
+        elif not groups:  # no address either, which would mean: no gate
+            raise ValueError(f"gate must have groups that divide the {rows} rows")
     return _lib.Norm(rows, width, dt, eps, residual_scale, 0, weight(post_weight, "post_weight"),
                      weight(pre_weight, "pre_weight"), at, groups, stride)
 

@@ -75,3 +75,23 @@ def test_a_refused_call_of_no_rows_changes_no_gradient(machine, log, monkeypatch
         with pytest.raises(rar.RarError):
             _no_rows(log)
     assert not log
+
+
+def test_a_gate_of_no_groups_is_refused(machine, log):  # noqa: F811
+    """An empty tensor has no address, which would mean: no gate."""
+    class Empty(Tensor):
+        def data_ptr(self):
+            return 0
+    x, w, gate = Tensor(4, 5), Tensor(5), Empty(0, 5)
+    with pytest.raises(ValueError, match="groups"):
+        rar.norm_allreduce([x], [x], [], gate=gate)
+    with pytest.raises(ValueError, match="groups"):
+        rar.norm_allreduce_backward([x], [], [x], total=x, gate=gate)
+    with pytest.raises(ValueError, match="groups"):
+        rar.norm_allreduce_backward([x], [], [x], total=x, gate=gate, dgate=Empty(0, 5))
+    assert not machine.launches
+    e = Tensor(0, 5)  # without rows there is nothing to gate
+    rar.norm_allreduce([e], [e], [], gate=gate)
+    rar.norm_allreduce_backward([e], [], [e], total=e, gate=gate, dgate=Written(0, 5, log=log))
+    assert len(machine.launches) == 2 and len(log) == 1
+    assert rar.norm_allreduce([x], [x], [], gate=Tensor(2, 5), post_weight=w) is None
