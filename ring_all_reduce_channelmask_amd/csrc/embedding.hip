@@ -53,6 +53,7 @@ struct ForwardArgs {
   int64_t tokens, width, pieces;  // pieces of a row
   float scale;
   int32_t ndst;
+  uint32_t block0;  // workgroups in earlier launches
   Split split;
 };
 
@@ -60,7 +61,7 @@ struct ForwardArgs {
 template <class T, int kVecs, int kThreads>
 __global__ void __launch_bounds__(256) embedding_kernel(ForwardArgs) {
   const ForwardArgs& args = kernel_args<ForwardArgs>();
-  const int64_t item = (int64_t)blockIdx.x * (256 / kThreads) + threadIdx.x / kThreads;
+  const int64_t item = (int64_t)(args.block0 + blockIdx.x) * (256 / kThreads) + threadIdx.x / kThreads;
   const int64_t t = item / args.pieces, piece = item - t * args.pieces;
   if (t >= args.tokens) return;
   const int64_t id = args.ids[t];
@@ -111,6 +112,7 @@ struct BackwardArgs {
   float scale;
   int32_t ngrads, accumulate, chunk, chunks, sorted;  // sorted: which of keys/places is in order
   int32_t shift, blocks, fill_rows;
+  uint32_t block0;  // workgroups in earlier launches
   Split split;
 };
 
@@ -199,6 +201,7 @@ constexpr int kFillRows = 64;  // table rows that a filling workgroup looks at, 
 template <class T, class G>
 __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
+  const uint32_t block = args.block0 + blockIdx.x;
   constexpr int kRounds = kSmallTokens / 256;
   __shared__ int32_t list[kSmallTokens];
   __shared__ int32_t counts[kRounds][4];
@@ -211,8 +214,8 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
     const int32_t u = i * 256 + threadIdx.x;
     keys[i] = u < tokens ? key_of(args.ids[u], vocab) : vocab;
   }
-  if (blockIdx.x >= args.sum_groups) {
-    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
+  if (block >= args.sum_groups) {
+    const int32_t r0 = (int32_t)(block - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
     int32_t* used = list;
     if (threadIdx.x < kFillRows) used[threadIdx.x] = 0;
     __syncthreads();
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
       if (!used[i]) zero_row<G>(args, r0 + i, lane);
     return;
   }
-  const int32_t t = (int32_t)(blockIdx.x / args.slices);
+  const int32_t t = (int32_t)(block / args.slices);
   const int32_t key = key_of(args.ids[t], vocab);
   if (key == vocab) return;
   uint64_t same[kRounds];
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(256) few_tokens_kernel(BackwardArgs) {
       total += counts[i][w];
     }
   __syncthreads();
-  const int64_t e = (blockIdx.x - t * args.slices) * (64 * T::kVec) + lane * T::kVec;
+  const int64_t e = (block - t * args.slices) * (64 * T::kVec) + lane * T::kVec;
   const int n = (int)(args.width - e >= T::kVec ? T::kVec : args.width - e < 0 ? 0 : args.width - e);
   float sum[T::kVec];
 #pragma unroll
@@ -433,12 +436,13 @@ __device__ __forceinline__ int64_t lower_bound(const int32_t* keys, int64_t n, i
 template <class T, class G>
 __global__ void __launch_bounds__(256) sum_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
+  const uint32_t block = args.block0 + blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t vocab = args.split.first[args.split.nranks];
   const int32_t* keys = args.keys[args.sorted];
-  if (blockIdx.x >= args.sum_groups) {
+  if (block >= args.sum_groups) {
     __shared__ uint32_t used[kFillRows];
-    const int32_t r0 = (int32_t)(blockIdx.x - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
+    const int32_t r0 = (int32_t)(block - args.sum_groups) * args.fill_rows, r1 = std::min(vocab, r0 + args.fill_rows);
     if (threadIdx.x < kFillRows) used[threadIdx.x] = 0;
     __syncthreads();
     if (wave == 0) {
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(256) sum_kernel(BackwardArgs) {
       if (!used[i]) zero_row<G>(args, r0 + i, lane);
     return;
   }
-  const int64_t item = (int64_t)blockIdx.x * 4 + wave;
+  const int64_t item = (int64_t)block * 4 + wave;
   const int64_t c = item / args.slices;
   if (c >= args.chunks) return;
   const int64_t e = (item - c * args.slices) * (64 * T::kVec) + lane * T::kVec;
@@ -493,12 +497,13 @@ constexpr int kJoinWaves = 4, kJoinColumns = 512, kJoinVecs = kJoinColumns / 256
 template <class T, class G>
 __global__ void __launch_bounds__(64 * kJoinWaves) join_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
+  const uint32_t block = args.block0 + blockIdx.x;
   __shared__ float parts[kJoinWaves][kJoinColumns];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t vocab = args.split.first[args.split.nranks];
   const int32_t* keys = args.keys[args.sorted];
   const int64_t slices = (args.width + kJoinColumns - 1) / kJoinColumns;
-  const int64_t c = blockIdx.x / slices, e = (blockIdx.x - c * slices) * kJoinColumns + lane * 4;
+  const int64_t c = block / slices, e = (block - c * slices) * kJoinColumns + lane * 4;
   const int64_t i0 = c * args.chunk, i1 = i0 + args.chunk;  // not the last chunk
   const int32_t v = keys[i1 - 1], first = keys[i0], before = i0 > 0 ? keys[i0 - 1] : -1;
   if (v == vocab || keys[i1] != v || (first == v && before == v)) return;
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) join_kernel(BackwardArgs) {
     for (int i = 0; i < 4; ++i) parts[wave][h * 256 + lane * 4 + i] = sum[h * 4 + i];
   __syncthreads();
   for (int i = threadIdx.x; i < kJoinColumns; i += 64 * kJoinWaves) {
-    const int64_t column = (blockIdx.x - c * slices) * kJoinColumns + i;
+    const int64_t column = (block - c * slices) * kJoinColumns + i;
     if (column >= args.width) return;
     float all = 0.0f;
 #pragma unroll
@@ -649,23 +654,16 @@ rar_result_t forward(const void* const* tables, const int64_t* rows, const int64
   a.tokens = tokens;
   a.pieces = (width + threads * vec * vecs - 1) / (threads * vec * vecs);
   const int64_t groups = (tokens * a.pieces + 256 / threads - 1) / (256 / threads);
-  if (groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
+  if (groups > kMaxGroups) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
   const void* fn = dtype == kFloat32 ? forward_kernel<F32>(threads, vecs) : forward_kernel<BF16>(threads, vecs);
-  return launch_kernel(fn, dim3((unsigned)groups), dim3(256), &a, stream);
+  return launch_groups(fn, groups, 256, &a, &a.block0, stream);
 }
 
 template <class T, class G>
-rar_result_t launch_sums(BackwardArgs& a, int64_t fill_groups, void* stream) {
-  const bool small = a.tokens <= kSmallTokens;
-  a.slices = (a.width + 64 * T::kVec - 1) / (64 * T::kVec);
-  a.sum_groups = small ? a.tokens * a.slices : (a.chunks * a.slices + 3) / 4;
-  if (a.sum_groups + fill_groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
-  const dim3 grid((unsigned)(a.sum_groups + fill_groups));
-  if (small) return launch_kernel(reinterpret_cast<const void*>(&few_tokens_kernel<T, G>), grid, dim3(256), &a, stream);
-  if (rar_result_t r = launch_kernel(reinterpret_cast<const void*>(&sum_kernel<T, G>), grid, dim3(256), &a, stream)) return r;
-  const int64_t joins = (int64_t)(a.chunks - 1) * ((a.width + kJoinColumns - 1) / kJoinColumns);
-  if (joins > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
-  return launch_kernel(reinterpret_cast<const void*>(&join_kernel<T, G>), dim3((unsigned)joins), dim3(64 * kJoinWaves), &a, stream);
+rar_result_t launch_sums(BackwardArgs& a, int64_t fill_groups, int64_t joins, void* stream) {
+  if (joins == 0) return launch_groups(reinterpret_cast<const void*>(&few_tokens_kernel<T, G>), a.sum_groups + fill_groups, 256, &a, &a.block0, stream);
+  if (rar_result_t r = launch_groups(reinterpret_cast<const void*>(&sum_kernel<T, G>), a.sum_groups + fill_groups, 256, &a, &a.block0, stream)) return r;
+  return launch_groups(reinterpret_cast<const void*>(&join_kernel<T, G>), joins, 64 * kJoinWaves, &a, &a.block0, stream);
 }
 
 rar_result_t backward(const void* const* grads, const int64_t* grad_strides, int ngrads, int64_t tokens, int64_t width, int dtype,
@@ -718,6 +716,15 @@ rar_result_t backward(const void* const* grads, const int64_t* grad_strides, int
   a.chunk = s.chunk;
   a.chunks = s.chunks;
   a.blocks = s.blocks;
+  const int64_t piece = 64 * (dtype == kFloat32 ? F32::kVec : BF16::kVec);
+  a.slices = (width + piece - 1) / piece;
+  a.sum_groups = s.bytes ? (s.chunks * a.slices + 3) / 4 : tokens * a.slices;
+  // the groups that two chunks share; 0 where there are no chunks
+  const int64_t joins = s.bytes ? (int64_t)(s.chunks - 1) * ((width + kJoinColumns - 1) / kJoinColumns) : 0;
+  // enough workgroups for all CUs where the vocabulary is small
+  a.fill_rows = (int32_t)std::max<int64_t>(4, std::min<int64_t>(kFillRows, vocab / 2048));
+  const int64_t fill = accumulate ? 0 : (vocab + a.fill_rows - 1) / a.fill_rows;
+  if (std::max(a.sum_groups + fill, joins) > kMaxGroups) return set_error(RAR_INVALID_ARGUMENT, "tokens * width is too large");
   if (s.bytes) {
     char* p = static_cast<char*>(workspace);
     for (int i = 0; i < 2; ++i) {
@@ -736,11 +743,8 @@ rar_result_t backward(const void* const* grads, const int64_t* grad_strides, int
       }
     }
   }
-  // enough workgroups for all CUs where the vocabulary is small
-  a.fill_rows = (int32_t)std::max<int64_t>(4, std::min<int64_t>(kFillRows, vocab / 2048));
-  const int64_t fill = accumulate ? 0 : (vocab + a.fill_rows - 1) / a.fill_rows;
-  if (dtype == kFloat32) return launch_sums<F32, F32>(a, fill, stream);
-  return table_dtype == kFloat32 ? launch_sums<BF16, F32>(a, fill, stream) : launch_sums<BF16, BF16>(a, fill, stream);
+  if (dtype == kFloat32) return launch_sums<F32, F32>(a, fill, joins, stream);
+  return table_dtype == kFloat32 ? launch_sums<BF16, F32>(a, fill, joins, stream) : launch_sums<BF16, BF16>(a, fill, joins, stream);
 }
 
 }  // namespace

@@ -114,6 +114,20 @@ inline rar_result_t launch_kernel(const void* fn, dim3 grid, dim3 block, void* a
   return RAR_SUCCESS;
 }
 
+// A grid holds less than 2^32 threads.  Workgroups beyond that go out in further
+// launches, launch after launch; `block0`, a member of the kernel's arguments,
+// is the number of those before.  A call checks its kernels' workgroups against
+// kMaxGroups before it launches any.
+constexpr int64_t kMaxGroups = 0x7FFFFFFF;
+inline rar_result_t launch_groups(const void* fn, int64_t groups, int threads, void* args, uint32_t* block0, void* stream) {
+  const int64_t most = ((int64_t(1) << 32) - 1) / threads;
+  for (int64_t done = 0; done < groups; done += most) {
+    *block0 = (uint32_t)done;
+    if (rar_result_t r = launch_kernel(fn, dim3((unsigned)std::min(most, groups - done)), dim3(threads), args, stream)) return r;
+  }
+  return RAR_SUCCESS;
+}
+
 // ---- device -----------------------------------------------------------------
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
