@@ -173,6 +173,7 @@ struct ForwardArgs {
   int64_t rows, group_rows;  // group_rows: rows that share a gate
   int32_t width, nsrc, nhidden, nout;
   float eps, scale;
+  uint32_t block0;  // rows in earlier launches
 };
 
 // Up to two vectors a thread, two workgroups of 16 waves a CU: 2048 x 16384 bf16
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kMaxThreads) __attribute__((amdgpu_waves_per_e
   const ForwardArgs& args = kernel_args<ForwardArgs>();
   __shared__ v2f scratch[2][kMaxThreads / 64];
   const int width = args.width, waves = blockDim.x >> 6;
-  const int64_t row = blockIdx.x;
+  const int64_t row = args.block0 + blockIdx.x;
   Row<T, kVecs> x, w, g;
   float h[kVecs][T::kVec];
   auto rstd_of_h = [&](v2f* sums) {
@@ -907,8 +908,8 @@ rar_result_t forward(const rar_norm_t* norm, const void* const* partials, const 
   a.width = (int32_t)n.width, a.nsrc = nranks, a.nhidden = nhidden, a.nout = nouts;
   a.eps = n.eps, a.scale = n.residual_scale;
   const Launch l = launch_of(n.width, n.dtype);
-  return launch_kernel(n.dtype == kFloat32 ? norm_kernel<F32>(l.vecs, false) : norm_kernel<BF16>(l.vecs, false), dim3((unsigned)n.rows),
-                       dim3(l.threads), &a, stream);
+  return launch_groups(n.dtype == kFloat32 ? norm_kernel<F32>(l.vecs, false) : norm_kernel<BF16>(l.vecs, false), n.rows, l.threads, &a,
+                       &a.block0, stream);
 }
 
 rar_result_t backward(const rar_norm_t* norm, const void* const* grad_hidden, const int64_t* grad_hidden_strides, int ngrad_hidden,

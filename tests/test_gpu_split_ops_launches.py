@@ -76,3 +76,25 @@ def test_gradient_of_few_tokens_of_2_24_columns():
     for v in range(6):
         want = (1 + 0.5 * (weight * (ids == v)).sum() * row.float()).bfloat16()
         assert torch.equal(table[v], want), v
+
+
+def test_norms_of_2_24_rows():
+    """A workgroup of 256 threads a row: the last row is alone in the second
+    launch.  In place; the rows are some hundred, over and over."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    width = 1544
+    some = torch.randn(255, width, device="cuda").bfloat16()
+    x = torch.empty(ALL, width, dtype=torch.bfloat16, device="cuda")
+    ids = torch.arange(ALL, device="cuda") % 255
+    for at in range(0, ALL, 1 << 21):
+        x[at:at + (1 << 21)] = some[ids[at:at + (1 << 21)]]
+    weight, gate = torch.randn(width, device="cuda").bfloat16(), torch.randn(2, width, device="cuda").bfloat16()
+    wants = []
+    for k in range(2):
+        want = torch.empty_like(some)
+        rar.norm_allreduce([some], [], [want], gate=gate[k], pre_weight=weight)
+        wants.append(want)
+    rar.norm_allreduce([x], [], [x], gate=gate, pre_weight=weight)
+    for at in range(0, ALL, 1 << 21):
+        assert torch.equal(x[at:at + (1 << 21)], wants[at // (ALL // 2)][ids[at:at + (1 << 21)]])

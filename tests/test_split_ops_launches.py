@@ -45,6 +45,17 @@ def _embedding_back(tokens, width, dtype, vocab, acc=0):
                                                         1 << 37, None)
 
 
+def _norm(rows, width, dtype):
+    n = _lib.Norm(rows=rows, width=width, dtype=dtype, eps=1e-6, residual_scale=1.0, pre_weight=A + G)
+    return _lib.load().rar_norm_allreduce(ctypes.byref(n), _p([A]), None, 1, None, 0, _p([A]), None, 1, None, None, 0, None, 0, None)
+
+
+def _norm_back(rows, width, dtype, groups):
+    n = _lib.Norm(rows=rows, width=width, dtype=dtype, eps=1e-6, residual_scale=1.0, pre_weight=A + G, gate=A + 4 * G, gate_groups=groups)
+    return _lib.load().rar_norm_allreduce_backward(ctypes.byref(n), _p([A]), None, 1, None, None, 0, A + 5 * G, 0, None, 0, _p([A]), None, 1, None, 0, None, A + 6 * G, 0,
+                                                   None, A + 7 * G, 1 << 37, None)
+
+
 ALL = 1 << 24
 # call, arguments, workgroups of each kind of launch (None: not looked at)
 CASES = {
@@ -59,6 +70,11 @@ CASES = {
     "embedding gradient, by pairs and 2^30 rows": (_embedding_back, (2000, 5, BF16, 1 << 30), [32, None, 249]),
     "embedding gradient, by digits and 2^30 rows": (_embedding_back, (8193, 5, BF16, 1 << 30), [9] * 8 + [None, 1024]),
     "embedding gradient, 2^24 tokens": (_embedding_back, (ALL, 1000, BF16, 100, 1), [256] * 2 + [ALL // 64 * 2 // 4, (ALL // 64 - 1) * 2]),
+    "norms, ordinary": (_norm, (4096, 7168, BF16), [4096]),
+    "norms, 2^24 rows of 256 threads": (_norm, (ALL, 1544, BF16), [ALL]),
+    "norms, 2^24 rows of 1024 threads": (_norm, (ALL, 4096, F32), [ALL]),
+    "norms, 2^22 rows of 1024 threads": (_norm, (1 << 22, 7700, BF16), [1 << 22]),
+    "norms gradient, a gate a row": (_norm_back, (ALL, 1544, BF16, ALL), [1024]),
 }
 
 
