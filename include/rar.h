@@ -635,7 +635,8 @@ rar_result_t rar_quantize_rows(const void* const* xs, const int64_t* widths,
  *   residual, recvbufs   [tokens] of outer elements of dtype; residual NULL for
  *              none, residual_stride 0: outer.  An output may be exactly the
  *              residual (in place).
- *   tokens 0..2^24 (0 launches nothing), outer 1..2^24, nranks, nrecv 1..64.
+ *   tokens 0..2^24 (0 launches nothing), outer 1..2^24, tokens * outer up to
+ *   2^38, nranks, nrecv 1..64.
  *   workspace  16-byte aligned device memory, rar_int8_projection_workspace
  *              bytes (0: NULL allowed): less where `aligned` says that every
  *              row of xs and weights begins on a multiple of 16 bytes and that

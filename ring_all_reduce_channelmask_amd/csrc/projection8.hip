@@ -27,6 +27,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxOuter = int64_t(1) << 24;
+constexpr int64_t kMaxResults = int64_t(1) << 38;
 constexpr int64_t kMaxInner = 131071;  // 2^14 a product of two bytes, 2^31 a sum
 
 typedef int32_t v4i __attribute__((ext_vector_type(4)));
@@ -43,6 +44,7 @@ struct QuantArgs {
   float* scales;
   int32_t nranks, pieces;
   int32_t first[kMaxRanks];  // the pieces before a rank's
+  uint32_t block0;           // rows in earlier launches
 };
 
 // rint(127 x / most), a tie to the even integer as the quotient itself has it.
@@ -82,7 +84,7 @@ template <class T>
 __global__ void __launch_bounds__(1024) quantize_kernel(QuantArgs) {
   const QuantArgs& args = kernel_args<QuantArgs>();
   __shared__ uint32_t scratch[16];
-  const int64_t row = blockIdx.x;
+  const int64_t row = args.block0 + blockIdx.x;
   const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // this lane's elements of a piece: how many are there (0: none)
   auto find = [&](int piece, int* rank, int64_t* e) {
@@ -657,13 +659,15 @@ struct AlignArgs {
   int32_t width[kMaxRanks];
   int64_t rows;
   int32_t nranks;
+  uint32_t block0;  // workgroups in earlier launches
 };
 __global__ void __launch_bounds__(256) align_kernel(AlignArgs) {
   const AlignArgs& args = kernel_args<AlignArgs>();
+  const int block = (int)(args.block0 + blockIdx.x);
   int i = 0;
-  while (i + 1 < args.nranks && args.first[i + 1] <= (int)blockIdx.x) ++i;
+  while (i + 1 < args.nranks && args.first[i + 1] <= block) ++i;
   const int width = args.width[i], pieces = (width + 15) / 16;
-  const int64_t at = (int64_t)((int)blockIdx.x - args.first[i]) * 256 + threadIdx.x, row = at / pieces;
+  const int64_t at = (int64_t)(block - args.first[i]) * 256 + threadIdx.x, row = at / pieces;
   if (row >= args.rows) return;
   const int k = (int)(at - row * pieces) * 16;
   *reinterpret_cast<v4u*>(args.dst[i] + at * 16) = load_bytes(args.src[i] + row * args.stride[i] + k, width - k);
@@ -720,7 +724,7 @@ rar_result_t quantize(const void* const* xs, const int64_t* widths, const int64_
   // as many waves as the device holds (8192), a wave for every kKept pieces
   const int64_t most = std::max<int64_t>((a.pieces + kKept - 1) / kKept, 8192 / rows);
   const int waves = (int)std::max<int64_t>(1, std::min<int64_t>({most, a.pieces, 16}));
-  return launch_kernel(fn, dim3((unsigned)rows), dim3(64 * waves), &a, stream);
+  return launch_groups(fn, rows, 64 * waves, &a, &a.block0, stream);
 }
 
 rar_result_t check_sizes(int64_t tokens, int64_t outer, int dtype) {
@@ -804,6 +808,9 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
   if (nrecv < 1 || nrecv > kMaxRanks) return set_error(RAR_INVALID_ARGUMENT, "nrecv must be in [1, 64]");
   if (rar_result_t r = check_sizes(tokens, outer, dtype)) return r;
   if (tokens == 0) return RAR_SUCCESS;
+  // so all tiles' threads are less than 2^32: 512 for 256 x 192 results at least,
+  // or for what is left at the two edges
+  if (tokens > kMaxResults / outer) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer must be at most 2^38");
   if (!xs || !weights || !recvbufs) return set_error(RAR_INVALID_ARGUMENT, "an array of buffers is NULL");
   ProjArgs a{};
   const int64_t es = elem_size(dtype);
@@ -881,13 +888,12 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
   a.tiles_n = (int32_t)tiles_n;
   grid += (a.tiles_m * tiles_n + 7) / 8 * 8;
   if (plan.kind == kFew) grid = tiles_n;
-  if (grid > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens * outer is too large");
   a.splits = plan.splits;
   char* work = static_cast<char*>(workspace);
   a.partial = reinterpret_cast<int32_t*>(work + plan.align_x + plan.align_w);
-  auto align = [&](const int8_t** p, int64_t* stride, int64_t rows, char* to) {
-    AlignArgs g{};
-    int64_t groups = 0;
+  AlignArgs aligned_x{}, aligned_w{};
+  int64_t groups_x = 0, groups_w = 0;
+  auto align = [&](AlignArgs& g, int64_t& groups, const int8_t** p, int64_t* stride, int64_t rows, char* to) -> rar_result_t {
     for (int r = 0; r < a.nranks; ++r) {
       const int64_t pitch = round_up(a.width[r], 16);
       g.src[r] = p[r], g.stride[r] = stride[r], g.dst[r] = reinterpret_cast<int8_t*>(to);
@@ -895,17 +901,20 @@ rar_result_t project(const int8_t* const* xs, const int64_t* widths, const int64
       p[r] = reinterpret_cast<int8_t*>(to), stride[r] = pitch;
       to += rows * pitch;
       groups += (rows * (pitch / 16) + 255) / 256;
-      if (groups > 0x7FFFFFFF) return set_error(RAR_INVALID_ARGUMENT, "tokens or outer times the widths is too large");
+      if (groups > kMaxGroups) return set_error(RAR_INVALID_ARGUMENT, "tokens or outer times the widths is too large");
       g.first[r + 1] = (int32_t)groups;
     }
     g.rows = rows;
     g.nranks = a.nranks;
-    return launch_kernel(reinterpret_cast<const void*>(&align_kernel), dim3((unsigned)groups), dim3(256), &g, stream);
+    return RAR_SUCCESS;
   };
   if (plan.align_x)
-    if (rar_result_t r = align(a.x, a.x_stride, tokens, work)) return r;
+    if (rar_result_t r = align(aligned_x, groups_x, a.x, a.x_stride, tokens, work)) return r;
   if (plan.align_w)
-    if (rar_result_t r = align(a.w, a.w_stride, outer, work + plan.align_x)) return r;
+    if (rar_result_t r = align(aligned_w, groups_w, a.w, a.w_stride, outer, work + plan.align_x)) return r;
+  const void* align_fn = reinterpret_cast<const void*>(&align_kernel);
+  if (rar_result_t r = launch_groups(align_fn, groups_x, 256, &aligned_x, &aligned_x.block0, stream)) return r;
+  if (rar_result_t r = launch_groups(align_fn, groups_w, 256, &aligned_w, &aligned_w.block0, stream)) return r;
   if (rar_result_t r = launch_kernel(k.fn, dim3((unsigned)grid, (unsigned)a.splits), dim3(k.threads), &a, stream)) return r;
   if (a.splits == 1) return RAR_SUCCESS;
   const int vec = f32 ? F32::kVec : BF16::kVec;

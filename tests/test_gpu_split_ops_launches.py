@@ -98,3 +98,40 @@ def test_norms_of_2_24_rows():
     rar.norm_allreduce([x], [], [x], gate=gate, pre_weight=weight)
     for at in range(0, ALL, 1 << 21):
         assert torch.equal(x[at:at + (1 << 21)], wants[at // (ALL // 2)][ids[at:at + (1 << 21)]])
+
+
+def test_quantisation_of_2_24_rows():
+    """64 ranks of a column each, 16 waves a row: five launches."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    x = torch.randint(-4, 5, (64, ALL, 1), device="cuda").bfloat16()
+    q = torch.full((64, ALL, 1), 99, dtype=torch.int8, device="cuda")
+    _, scales = rar.quantize_rows(list(x), quantized=list(q))
+    most = x.abs().amax((0, 2)).float()
+    assert torch.equal(scales, most / 127)
+    for k in range(0, 64, 16):  # whole numbers up to 4: no quotient but 127/2 is near a tie, and 127 x is exact
+        want = (x[k:k + 16, :, 0].float() * 127 / most.clamp(min=1)).round().to(torch.int8)
+        assert torch.equal(q[k:k + 16, :, 0], want)
+
+
+def test_projection_of_2_24_unaligned_tokens():
+    """Rows of 4112 bytes, a byte off: 257 pieces of 16 for each token are laid
+    out, 2^24 + 2^16 workgroups."""
+    import torch
+    import ring_all_reduce_channelmask_amd as rar
+    if torch.cuda.mem_get_info()[0] < 150e9:
+        pytest.skip("needs 150 GB of device memory")
+    width = 4112
+    # enough rows for the second launch to lay out the last ones
+    some = torch.randint(-127, 128, (255, width), dtype=torch.int8, device="cuda")
+    held = torch.empty(ALL * width + 1, dtype=torch.int8, device="cuda")
+    x = held[1:].view(ALL, width)
+    ids = torch.arange(ALL, device="cuda") % 255
+    for at in range(0, ALL, 1 << 20):
+        x[at:at + (1 << 20)] = some[ids[at:at + (1 << 20)]]
+    w = torch.randint(-127, 128, (3, width), dtype=torch.int8, device="cuda")
+    scale = 0.5 + torch.rand(ALL, device="cuda")
+    y = torch.empty(ALL, 3, device="cuda")
+    rar.int8_projection_allreduce([x], scale, [w], torch.ones(3, device="cuda"), [y])
+    sums = (some.double() @ w.double().T).float()  # below 2^53: exact, rounded once
+    assert torch.equal(y, sums[ids] * scale[:, None])

@@ -56,6 +56,16 @@ def _norm_back(rows, width, dtype, groups):
                                                    None, A + 7 * G, 1 << 37, None)
 
 
+def _quantize(rows, widths, dtype):
+    xs, qs = [A + i * G for i in range(len(widths))], [A + (100 + i) * G for i in range(len(widths))]
+    return _lib.load().rar_quantize_rows(_p(xs), _l(widths), None, len(widths), rows, dtype, _p(qs), None, A + 200 * G, None)
+
+
+def _project(tokens, width, outer, dtype, skew=0):
+    return _lib.load().rar_int8_projection_allreduce(_p([A + skew]), _l([width]), None, A + G, _p([A + 2 * G + skew]), None, A + 3 * G, 1, tokens, outer, dtype, None, 0,
+                                                     _p([A + 4 * G]), None, 1, A + 10 * G, 1 << 38, None)
+
+
 ALL = 1 << 24
 # call, arguments, workgroups of each kind of launch (None: not looked at)
 CASES = {
@@ -75,6 +85,13 @@ CASES = {
     "norms, 2^24 rows of 1024 threads": (_norm, (ALL, 4096, F32), [ALL]),
     "norms, 2^22 rows of 1024 threads": (_norm, (1 << 22, 7700, BF16), [1 << 22]),
     "norms gradient, a gate a row": (_norm_back, (ALL, 1544, BF16, ALL), [1024]),
+    "quantisation, 2^24 rows of 64 ranks": (_quantize, (ALL, [1] * 64, BF16), [ALL]),
+    "quantisation, ordinary": (_quantize, (4096, [1792] * 4, BF16), [4096]),
+    "projection, 2^24 channels": (_project, (1, 100, ALL, BF16), [ALL // 16]),
+    "projection, 2^24 tokens laid out first": (_project, (ALL, 5000, 1, F32, 1), [-(-ALL * 313 // 256), 2, None]),
+    "projection, 2^24 channels laid out first": (_project, (17, 131071, ALL // 16, BF16, 1), [-(-17 * 8192 // 256), (ALL // 16) * 8192 // 256, None]),
+    "projection, 2^38 results": (_project, (ALL, 112, 1 << 14, BF16), [1 << 22]),
+    "projection, 2^38 results of another shape": (_project, (1 << 19, 112, 1 << 19, F32), [None]),
 }
 
 
