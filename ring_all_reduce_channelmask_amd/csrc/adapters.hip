@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
       const bits* w = static_cast<const bits*>(args.down[r]) + (int64_t)a * args.rank * width + col;
       auto row_at = [&](int i) {
         const int row = i * 8 + lane / 8;
-        if (i < 2 * kM) return x + (members >> row & 1 ? row : first) * args.x_stride[r];
+        if (i < 2 * kM) return x + (bit_of(members, row) ? row : first) * args.x_stride[r];
         const int n = row - 16 * kM;
         return w + (int64_t)(n < args.rank ? n : args.rank - 1) * width;
       };
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = m * 16 + 4 * group + i;
-        if (col < args.rank && (members >> row & 1))
+        if (col < args.rank && bit_of(members, row))
           args.h[((int64_t)part * args.tokens + token0 + row) * args.rank + col] = s[i];
       }
     }

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "capi_internal.h"
+#include "lane_bits.h"
 
 namespace rar {
 
@@ -245,11 +246,6 @@ __device__ __forceinline__ float group_reduce(float v, Op op) {
   return v;
 }
 
-// How many of the mask's bits are below this lane's.
-__device__ __forceinline__ int bits_below(uint64_t mask) {
-  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-}
-
 // A row's address, the same in all lanes, kept out of vector registers: the
 // lanes' offsets are added to it in the access.
 __device__ __forceinline__ char* row_at(const char* p, int64_t offset) {
@@ -266,8 +262,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // A vector without its first n (0 to kVec) elements, zeros behind.  In 32-bit
-// steps: 64-bit shifts by a lane's own amount gave wrong results here where the
-// amount was in the wave's last vector register.
+// steps, as lane_bits.h says.
 template <class T>
 __device__ __forceinline__ v4u shift_elements(v4u v, int n) {
   if constexpr (T::kVec == 8) {

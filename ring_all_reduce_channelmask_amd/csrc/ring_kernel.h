@@ -19,6 +19,7 @@
 #include <cstddef>
 #include <type_traits>
 
+#include "lane_bits.h"
 #include "rar_device.h"
 
 namespace rar {
@@ -663,10 +664,11 @@ __device__ bool ll_wait_line(const uint64_t* line, uint32_t flag, uint64_t& a, u
 template <class S>
 __device__ __forceinline__ uint64_t load_bytes8(const uint8_t* p, int64_t valid) {
   if (valid >= 8) return *(const g_u64_user*)p;
-  uint64_t v = 0;
-  for (int64_t b = 0; b < valid; b += sizeof(S))
-    v |= (uint64_t)(*G(reinterpret_cast<const S*>(p + b))) << (8 * b);
-  return v;
+  uint32_t half[2] = {0, 0};  // element by element: no shift by a lane's amount
+#pragma unroll
+  for (int b = 0; b < 8; b += sizeof(S))
+    if (b < valid) half[b / 4] |= (uint32_t)(*G(reinterpret_cast<const S*>(p + b))) << (8 * (b & 3));
+  return (uint64_t)half[1] << 32 | half[0];
 }
 template <class S>
 __device__ __forceinline__ void store_bytes8(uint8_t* p, uint64_t v, int64_t valid) {
@@ -674,7 +676,9 @@ __device__ __forceinline__ void store_bytes8(uint8_t* p, uint64_t v, int64_t val
     *(g_u64_user*)p = v;
     return;
   }
-  for (int64_t b = 0; b < valid; b += sizeof(S)) *G(reinterpret_cast<S*>(p + b)) = (S)(v >> (8 * b));
+#pragma unroll
+  for (int b = 0; b < 8; b += sizeof(S))
+    if (b < valid) *G(reinterpret_cast<S*>(p + b)) = (S)(v >> (8 * b));
 }
 
 template <class Ty, int OP>
@@ -1229,7 +1233,7 @@ __device__ void load_batch(Shmem& sh, const Plan& a, uint32_t b, int lid) {
     sh.batch = hdr;
     sh.n_works = __popcll(bits);
   }
-  if ((bits >> lid) & 1ull) sh.slot_bit[__popcll(bits & ((1ull << lid) - 1ull))] = lid;
+  if (bit_of(bits, lid)) sh.slot_bit[bits_below(bits)] = lid;
   __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
   __builtin_amdgcn_wave_barrier();
   const int nw = __popcll(bits);
@@ -1245,9 +1249,8 @@ __device__ void load_batch(Shmem& sh, const Plan& a, uint32_t b, int lid) {
 // ---------------------------------------------------------------- entry
 // LL128 workgroups are small (4 waves in the measured shape) and the protocol
 // wants many of them: capping its registers at three waves per SIMD lets three
-// such workgroups share a CU (fp32 and int32, with 4 groups of lines in flight,
-// then spill 4 registers per lane, 12 for avg and PreMulSum; bf16 with 3
-// groups spills none).  Measured at 64 MiB: this beats a two-waves-per-SIMD
+// such workgroups share a CU (fp32 and int32 with 4 groups of lines in flight,
+// bf16 with 3; no register spills).  Measured at 64 MiB: this beats a two-waves-per-SIMD
 // cap with 6 or 8 groups in flight and fewer workgroups (254-288 us against
 // 246 us).
 template <class Ty, int PROTO>
@@ -1304,7 +1307,7 @@ ring_allreduce_kernel(KernelArgs args) {
       sh.local_send = 0;
     }
     // the lane of the channel id also fetches what depends on it alone
-    if (((mask >> lid) & 1ull) && __popcll(mask & ((1ull << lid) - 1ull)) == n) {
+    if (bit_of(mask, lid) && bits_below(mask) == n) {
       sh.channel_id = lid;
       sh.first_batch = plan.first_batch[lid];
       sh.me = comm->ranks[lid][rank];
