@@ -90,6 +90,9 @@ CASES = {
     "projection, 2^24 channels": (_project, (1, 100, ALL, BF16), [ALL // 16]),
     "projection, 2^24 tokens laid out first": (_project, (ALL, 5000, 1, F32, 1), [-(-ALL * 313 // 256), 2, None]),
     "projection, 2^24 channels laid out first": (_project, (17, 131071, ALL // 16, BF16, 1), [-(-17 * 8192 // 256), (ALL // 16) * 8192 // 256, None]),
+    "projection, 256 and 192 channels a tile": (_project, (4000, 112, 7100, BF16), [16 * 16 + 16 * 16]),
+    "projection, 256 and 192 channels a tile, whole": (_project, (4096, 64, 7168, BF16), [16 * 16 + 16 * 16]),
+    "projection, 256 and 192 channels a tile, 32 rows": (_project, (8100, 96, 2900, F32), [32 * 8 + 32 * 5]),
     "projection, 2^38 results": (_project, (ALL, 112, 1 << 14, BF16), [1 << 22]),
     "projection, 2^38 results of another shape": (_project, (1 << 19, 112, 1 << 19, F32), [None]),
 }
