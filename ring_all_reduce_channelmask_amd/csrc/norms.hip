@@ -53,7 +53,7 @@ __device__ __forceinline__ float rstd_of(float squares, float width, float eps) 
 
 // What a row x and, for its gradient, a row v of the gradients of x / rms(x)
 // are reduced to.  A row whose sum of squares leaves fp32's range is taken
-// times kDown (`scale_down` changes it in place) and summed again: no square of
+// times kDown (from `scale_down` on) and summed again: no square of
 // a finite number leaves it then, and what is lost at the other end is below
 // 2^-60 of the row's largest element.  Where the sum of v x leaves it, v's
 // part of that sum is taken times kDown.  All threads agree on both, and other
@@ -110,16 +110,6 @@ struct Row {
   }
   __device__ __forceinline__ void widen(int j, float* f) const { T::widen(v[j], f); }
   __device__ __forceinline__ void set(int j, const float* f) { v[j] = T::round(f); }
-  __device__ __forceinline__ void scale_down() {
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      float f[T::kVec];
-      widen(j, f);
-#pragma unroll
-      for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
-      set(j, f);
-    }
-  }
   __device__ __forceinline__ void store(void* buf, int64_t stride, int64_t row, int width) const {
     typename T::bits* p = static_cast<typename T::bits*>(buf) + row * stride;
 #pragma unroll
@@ -333,6 +323,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
         w.load_shared(args.pre, 0, 0, width);
         h.fix(width);
         w.fix(width);
+        float down = 1.0f;  // scaling the row in its registers instead: 213 us where this takes 192 (2048 x 16384 bf16)
         const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
 #pragma unroll
           for (int j = 0; j < kVecs; ++j) {
@@ -341,12 +332,13 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
             w.widen(j, k);
 #pragma unroll
             for (int i = 0; i < T::kVec; ++i) {
+              f[i] *= down;
               squares = __builtin_fmaf(f[i], f[i], squares);
               dot = __builtin_fmaf(n[j][i] * k[i] * factor, f[i], dot);
             }
           }
           block_sum2(squares, dot, scratch[0], waves);
-        }, [&] { h.scale_down(); });
+        }, [&] { down = kDown; });
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float f[T::kVec], k[T::kVec];
@@ -354,6 +346,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           w.widen(j, k);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
+            f[i] *= down;
             dpre[j][i] = __builtin_fmaf(n[j][i], f[i] * of.r, dpre[j][i]);
             d[j][i] = __builtin_fmaf(of.rstd, __builtin_fmaf(-f[i], of.c, n[j][i] * k[i]), d[j][i]);
           }
@@ -377,6 +370,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
       if (args.post) {
         w.load_shared(args.post, 0, 0, width);
         w.fix(width);
+        float down = 1.0f;
         const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
 #pragma unroll
           for (int j = 0; j < kVecs; ++j) {
@@ -386,12 +380,13 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
             if (args.gate) g.widen(j, a);
 #pragma unroll
             for (int i = 0; i < T::kVec; ++i) {
+              f[i] *= down;
               squares = __builtin_fmaf(f[i], f[i], squares);
               dot = __builtin_fmaf(d[j][i] * (args.gate ? a[i] : 1.0f) * k[i] * factor, f[i], dot);
             }
           }
           block_sum2(squares, dot, scratch[1], waves);
-        }, [&] { s.scale_down(); });
+        }, [&] { down = kDown; });
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
           float f[T::kVec], k[T::kVec], a[T::kVec];
@@ -400,6 +395,7 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
           if (args.gate) g.widen(j, a);
 #pragma unroll
           for (int i = 0; i < T::kVec; ++i) {
+            f[i] *= down;
             both[j][i] = __builtin_fmaf(d[j][i], f[i] * of.r, both[j][i]);
             d[j][i] = of.rstd * __builtin_fmaf(-f[i], of.c, d[j][i] * (args.gate ? a[i] : 1.0f) * k[i]);
           }
