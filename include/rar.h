@@ -530,7 +530,8 @@ rar_result_t rar_embedding_allreduce(const void* const* tables, const int64_t* r
 
 /* Its gradient from the gradients of the copies (ngrads 1..64):
  *   dE[v] = scale * sum over t with ids[t] = v of sum over k of grads[k][t],
- * summed in fp32 in the order of the positions t.  Without `accumulate` every
+ * summed in fp32, in parts and an order that depend on the sizes and the ids
+ * alone: the same inputs give the same bits.  Without `accumulate` every
  * row of dtables is written, those of tokens that do not occur with zeros
  * (tokens 0: all); with it (1), the rows of tokens that occur are added to and
  * no others are read or written.
@@ -629,7 +630,8 @@ rar_result_t rar_quantize_rows(const void* const* xs, const int64_t* widths,
  *   recvbufs[k][t][d] = residual[t][d] + x_scales[t] * weight_scales[d] *
  *                       sum over r, i of xs[r][t][i] * weights[r][d][i]
  * for every copy k.  The sum is one of integers, exact, so the result does not
- * depend on how the columns are split.
+ * depend on how the columns are split; rounded to fp32 it is multiplied by
+ * x_scales, then by weight_scales, and each product has fp32's range.
  *   xs         [tokens] of widths[r] int8     weights  [outer] of widths[r] int8
  *   x_scales   [tokens] fp32                  weight_scales  [outer] fp32
  *   residual, recvbufs   [tokens] of outer elements of dtype; residual NULL for

@@ -20,10 +20,14 @@
 // of h and s from the stored rows, which it reads anyway.
 //
 // Bound by memory.  Measured (kernels): forward, 4096 x 7168 bf16, 4 partials, a
-// residual, a gate, 6 outputs 117 us (5.5 TB/s of 646 MB), 1 row 6.2 us (two
-// dependent reductions of a row over 14 waves); gradient, 4096 x 7168 bf16, 9
-// streams 121 us (4.4 TB/s) and 5 for the weights' sums; 104 x 2051 fp32 9.1 +
-// 4.4; 73153 x 328 bf16 with a gate a row 98 to 102 + 16.
+// residual, a gate, 6 outputs 117 to 124 us (5.5 TB/s of 646 MB), 4096 x 4096 fp32
+// 138, 1 row of 7168 6.4 us (two dependent reductions of a row over 14 waves);
+// gradient, 4096 x 7168 bf16, 9 streams 121 us (4.4 TB/s) and 5 for the weights'
+// sums; 104 x 2051 fp32 9.1 + 4.4; 73153 x 328 bf16 with a gate a row 98 to 102 +
+// 16.  Rows of more than a vector a thread (8192 of bf16, 4096 of fp32) do not fit
+// their registers and spill: gradient, 2048 x 16384 bf16 189 us + 9, 4096 x 7168
+// fp32 251 to 269 + 5, 512 x 32768 fp32 631 + 17; forward, from 16385 of fp32 on
+// (1024 x 32768 379).
 #include "op_common.h"
 
 namespace rar {
@@ -482,6 +486,9 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_kernel(BackwardArg
 template <class T, bool kEdge, bool kMore>
 __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(BackwardArgs) {
   const BackwardArgs& args = kernel_args<BackwardArgs>();
+  // gradients of outs on their way ahead, what registers hold.  4096 x 7168 bf16:
+  // 4 ranks 121 us; 1 rank, where three loads read the same row again, 109; 8
+  // ranks, the other four loaded when they are added, 162
   constexpr int kOuts = 4;
   typedef typename T::bits Bits;
   struct Inputs {
@@ -582,145 +589,145 @@ __global__ void __launch_bounds__(kMaxThreads) norms_backward_ahead_kernel(Backw
     const int64_t g = next / args.group_pieces;
     return g * args.group_rows + (next - g * args.group_pieces) * args.piece_rows;
   };
-    auto one_row = [&](Inputs& now, Inputs& ahead) {
-      float more[T::kVec];  // of the gradients of outs
+  auto one_row = [&](Inputs& now, Inputs& ahead) {
+    float more[T::kVec];  // of the gradients of outs
+    if (kMore && args.ngrad_out > kOuts) {
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) more[i] = 0.0f;
+      add_more(args.grad_out, args.grad_out_stride, kOuts, args.ngrad_out, row, more);
+    }
+    load(next_row(), ahead);
+    __builtin_amdgcn_sched_barrier(0);
+    if (edge) {
+      now.s = fix(now.s), now.h = fix(now.h), now.e = fix(now.e);
+#pragma unroll
+      for (int k = 0; k < kOuts; ++k) now.n[k] = fix(now.n[k]);
+    }
+    float d[T::kVec], g[T::kVec];
+    if (has_out) {
+      float n[T::kVec], f[T::kVec], k[T::kVec];
+      T::widen(now.n[0], n);
+#pragma unroll
+      for (int o = 1; o < kOuts; ++o) {
+        float x[T::kVec];
+        T::widen(now.n[o], x);
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) n[i] = o < args.ngrad_out ? n[i] + x[i] : n[i];
+      }
+      __builtin_amdgcn_sched_barrier(0);
       if (kMore && args.ngrad_out > kOuts) {
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) more[i] = 0.0f;
-        add_more(args.grad_out, args.grad_out_stride, kOuts, args.ngrad_out, row, more);
+        for (int i = 0; i < T::kVec; ++i) n[i] += more[i];
       }
-      load(next_row(), ahead);
-      __builtin_amdgcn_sched_barrier(0);
-      if (edge) {
-        now.s = fix(now.s), now.h = fix(now.h), now.e = fix(now.e);
-#pragma unroll
-        for (int k = 0; k < kOuts; ++k) now.n[k] = fix(now.n[k]);
-      }
-      float d[T::kVec], g[T::kVec];
-      if (has_out) {
-        float n[T::kVec], f[T::kVec], k[T::kVec];
-        T::widen(now.n[0], n);
-#pragma unroll
-        for (int o = 1; o < kOuts; ++o) {
-          float x[T::kVec];
-          T::widen(now.n[o], x);
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) n[i] = o < args.ngrad_out ? n[i] + x[i] : n[i];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (kMore && args.ngrad_out > kOuts) {
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) n[i] += more[i];
-        }
-        T::widen(now.h, f);
-        T::widen(weights[0], k);
-        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) {
-            squares = __builtin_fmaf(f[i], f[i], squares);
-            dot = __builtin_fmaf(n[i] * k[i] * factor, f[i], dot);
-          }
-          block_sum2(squares, dot, scratch[0], waves);
-        }, [&] {
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
-        });
+      T::widen(now.h, f);
+      T::widen(weights[0], k);
+      const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
 #pragma unroll
         for (int i = 0; i < T::kVec; ++i) {
-          dpre[i] = __builtin_fmaf(n[i], f[i] * of.r, dpre[i]);
-          n[i] = __builtin_fmaf(-f[i], of.c, n[i] * k[i]);
+          squares = __builtin_fmaf(f[i], f[i], squares);
+          dot = __builtin_fmaf(n[i] * k[i] * factor, f[i], dot);
         }
-        T::widen(now.e, d);
+        block_sum2(squares, dot, scratch[0], waves);
+      }, [&] {
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) d[i] = has_hidden ? d[i] : 0.0f;
-        if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
+        for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
+      });
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(of.rstd, n[i], d[i]);
-      } else {
-        T::widen(now.e, d);
-        if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
+      for (int i = 0; i < T::kVec; ++i) {
+        dpre[i] = __builtin_fmaf(n[i], f[i] * of.r, dpre[i]);
+        n[i] = __builtin_fmaf(-f[i], of.c, n[i] * k[i]);
       }
-      if (args.dresidual) {
-        float f[T::kVec];
+      T::widen(now.e, d);
 #pragma unroll
-        for (int i = 0; i < T::kVec; ++i) f[i] = args.scale * d[i];
-        put(args.dresidual, row * args.dresidual_stride, f);
-      }
-      T::widen(weights[2 * blockDim.x], g);
-      float f[T::kVec];
-      T::widen(now.s, f);
-      if (args.post) {
-        float k[T::kVec];
-        T::widen(weights[blockDim.x], k);
-        const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
+      for (int i = 0; i < T::kVec; ++i) d[i] = has_hidden ? d[i] : 0.0f;
+      if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
 #pragma unroll
-          for (int i = 0; i < T::kVec; ++i) {
-            squares = __builtin_fmaf(f[i], f[i], squares);
-            dot = __builtin_fmaf(d[i] * g[i] * k[i] * factor, f[i], dot);
-          }
-          block_sum2(squares, dot, scratch[1], waves);
-        }, [&] {
-#pragma unroll
-          for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
-        });
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) {
-          both[i] = __builtin_fmaf(d[i], f[i] * of.r, both[i]);
-          d[i] = of.rstd * __builtin_fmaf(-f[i], of.c, d[i] * g[i] * k[i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) {
-          both[i] = __builtin_fmaf(d[i], f[i], both[i]);
-          d[i] *= g[i];
-        }
-      }
-      for (int k = 0; k < args.ndsrc; ++k) put(args.dsrc[k], row * args.dsrc_stride[k], d);
-      // with several waves the barrier of one reduction frees the other's
-      // scratch, unless there is only one of the two
-      if (has_out != (args.post != nullptr) && waves > 1) __syncthreads();
-    };
-    // The sums of a piece that has ended.
-    auto end_piece = [&] {
-      if (!there) return;
-      if (args.dpost) {
-        float g[T::kVec];
-        T::widen(weights[2 * blockDim.x], g);
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) dpost[i / 4 * blockDim.x][i % 4] += g[i] * both[i];
-      }
-      if (args.dgate) {
-        float k[T::kVec];
-        T::widen(weights[blockDim.x], k);
-#pragma unroll
-        for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
-        if (args.group_pieces == 1) {
-          put(args.dgate, group * args.dgate_stride, both);
-        } else {
-          float* p = args.partial + (2 * args.groups + piece) * width + e;
-#pragma unroll
-          for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, both + i);
-        }
-      }
-    };
-    // The next row is the one in hand; false: there is none.
-    auto advance = [&] {
-      if (++row < row1) return true;
-      end_piece();
-      piece += args.groups;
-      if (piece >= args.pieces) return false;
-      begin_piece();
-      return true;
-    };
-    Inputs in[2];
-    begin_piece();
-    load(row, in[0]);
-    for (;;) {
-      one_row(in[0], in[1]);
-      if (!advance()) break;
-      one_row(in[1], in[0]);
-      if (!advance()) break;
+      for (int i = 0; i < T::kVec; ++i) d[i] = __builtin_fmaf(of.rstd, n[i], d[i]);
+    } else {
+      T::widen(now.e, d);
+      if (kMore && args.ngrad_hidden > 1) add_more(args.grad_hidden, args.grad_hidden_stride, 1, args.ngrad_hidden, row, d);
     }
+    if (args.dresidual) {
+      float f[T::kVec];
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) f[i] = args.scale * d[i];
+      put(args.dresidual, row * args.dresidual_stride, f);
+    }
+    T::widen(weights[2 * blockDim.x], g);
+    float f[T::kVec];
+    T::widen(now.s, f);
+    if (args.post) {
+      float k[T::kVec];
+      T::widen(weights[blockDim.x], k);
+      const Stats of = row_stats((float)width, args.eps, [&](float& squares, float& dot, float factor) {
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) {
+          squares = __builtin_fmaf(f[i], f[i], squares);
+          dot = __builtin_fmaf(d[i] * g[i] * k[i] * factor, f[i], dot);
+        }
+        block_sum2(squares, dot, scratch[1], waves);
+      }, [&] {
+#pragma unroll
+        for (int i = 0; i < T::kVec; ++i) f[i] *= kDown;
+      });
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) {
+        both[i] = __builtin_fmaf(d[i], f[i] * of.r, both[i]);
+        d[i] = of.rstd * __builtin_fmaf(-f[i], of.c, d[i] * g[i] * k[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) {
+        both[i] = __builtin_fmaf(d[i], f[i], both[i]);
+        d[i] *= g[i];
+      }
+    }
+    for (int k = 0; k < args.ndsrc; ++k) put(args.dsrc[k], row * args.dsrc_stride[k], d);
+    // with several waves the barrier of one reduction frees the other's
+    // scratch, unless there is only one of the two
+    if (has_out != (args.post != nullptr) && waves > 1) __syncthreads();
+  };
+  // The sums of a piece that has ended.
+  auto end_piece = [&] {
+    if (!there) return;
+    if (args.dpost) {
+      float g[T::kVec];
+      T::widen(weights[2 * blockDim.x], g);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) dpost[i / 4 * blockDim.x][i % 4] += g[i] * both[i];
+    }
+    if (args.dgate) {
+      float k[T::kVec];
+      T::widen(weights[blockDim.x], k);
+#pragma unroll
+      for (int i = 0; i < T::kVec; ++i) both[i] *= k[i];
+      if (args.group_pieces == 1) {
+        put(args.dgate, group * args.dgate_stride, both);
+      } else {
+        float* p = args.partial + (2 * args.groups + piece) * width + e;
+#pragma unroll
+        for (int i = 0; i < T::kVec; i += 4) store4<F32>(reinterpret_cast<uint32_t*>(p + i), left - i, both + i);
+      }
+    }
+  };
+  // The next row is the one in hand; false: there is none.
+  auto advance = [&] {
+    if (++row < row1) return true;
+    end_piece();
+    piece += args.groups;
+    if (piece >= args.pieces) return false;
+    begin_piece();
+    return true;
+  };
+  Inputs in[2];
+  begin_piece();
+  load(row, in[0]);
+  for (;;) {
+    one_row(in[0], in[1]);
+    if (!advance()) break;
+    one_row(in[1], in[0]);
+    if (!advance()) break;
+  }
   if (!there) return;
   float* p = args.partial + 2 * (int64_t)blockIdx.x * width + e;
 #pragma unroll

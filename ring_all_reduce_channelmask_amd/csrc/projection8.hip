@@ -14,7 +14,7 @@
 // Measured (kernels, 7168 x 7168, bf16, 4 ranks, 4 copies): 1 token 13.7 us
 // (51 MB of weights: 3.8 TB/s), 16 tokens 18.3, 104 tokens 17.9 + 5.9, 256
 // tokens 26.6 + 6.0, 1024 tokens 62, 4096 tokens 207 to 235 by the card's clock
-// (2.0 TOP/us; 177 with one copy, 2.4); 8192^3 440 to 510.  A library's product
+// (2030 TOP/s; 177 with one copy, 2380 TOP/s); 8192^3 440 to 510.  A library's product
 // of the same integers to int32 alone took 180 us (4096 x 7168 x 7168) and 438
 // (8192^3).  Quantisation of 4096 x 7168 bf16 23 to 27 us (88 MB), of 1000 x
 // 5001 fp32 10.8.
@@ -585,7 +585,11 @@ __global__ void __launch_bounds__(256) sum_kernel(ProjArgs) {
 constexpr int kFewTokens = 16;
 template <class T>
 __global__ void __launch_bounds__(512, 4) few_kernel(ProjArgs) {
-  constexpr int kBatch = 7;  // pieces whose loads are issued together
+  // Pieces whose loads are issued together: the 14 that a wave has of 7168 columns
+  // are two batches (13.7 us; in batches of 4 15.3, of 14 17.9).  Measured there
+  // alone: 4096 columns take two batches too, with 6 of the second's 7 loads for
+  // nothing (14.4), 8192 three (18.0).
+  constexpr int kBatch = 7;
   const ProjArgs& args = kernel_args<ProjArgs>();
   __shared__ __attribute__((aligned(16))) int32_t sums[8][kFewTokens][16 + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -746,7 +750,9 @@ rar_result_t check_sizes(int64_t tokens, int64_t outer, int dtype) {
 //   else k128x64.
 // Two workgroups a CU of the smallest tiles share the inner dimension where
 // tiles are fewer (104, 4 copies: whole 31.6, in 4 parts 16.0 + 5.8; 256: whole
-// 30.7, in 2 parts 24.1 + 4.9).
+// 30.7, in 2 parts 24.1 + 4.9).  So above 256 tiles nothing is divided, and tiles
+// of 128 x 128 never are: 1000 x 5001 x 2051 in fp32 is 264 tiles of 42 steps, 40 us.
+// The limits are those of 7168 x 7168; other sizes have not been measured for them.
 enum { kFew, kBig, k128x128, k64x128, k128x64 };
 struct Plan {
   int kind, splits = 1;

@@ -343,7 +343,8 @@ def embedding_allreduce_backward(grads, ids, dtables, scale=1.0, accumulate=Fals
     """The gradient of embedding_allreduce's tables from those of its copies,
     into ``dtables`` (like the tables, of the gradients' dtype or float32):
     every row is written, or with ``accumulate`` the rows of tokens that occur
-    are added to.  Equal tokens are summed in fp32, in order."""
+    are added to.  Equal tokens are summed in fp32, in an order that depends on
+    the sizes and the ids alone."""
     like, dt, dev = _start(grads, "grads")
     if _current_device() != dev:
         with _torch.cuda.device(dev):
