@@ -1252,9 +1252,12 @@ __device__ void load_batch(Shmem& sh, const Plan& a, uint32_t b, int lid) {
 // such workgroups share a CU (fp32 and int32 with 4 groups of lines in flight,
 // bf16 with 3; no register spills).  Measured at 64 MiB: this beats a two-waves-per-SIMD
 // cap with 6 or 8 groups in flight and fewer workgroups (254-288 us against
-// 246 us).
+// 246 us).  Simple of bf16 has the same cap, which all its operators fit: a
+// launch is taken only if all its workgroups are resident at once, so a kernel
+// that grows beyond it would refuse launches of up to three workgroups a CU.
 template <class Ty, int PROTO>
-__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(PROTO == kLL128 ? 3 : 1)))
+__global__ void __launch_bounds__(512)
+    __attribute__((amdgpu_waves_per_eu(PROTO == kLL128 || (PROTO == kSimple && sizeof(typename Ty::S) == 2) ? 3 : 1)))
 ring_allreduce_kernel(KernelArgs args) {
   __shared__ Shmem sh;
   __shared__ __attribute__((aligned(16))) uint8_t
